@@ -38,6 +38,27 @@ class PisaShape(ctypes.Structure):
 FORCE_SINK, FORCE_LOCAL = 1, 2   # pisa_shape.forced_blocks bits
 
 
+_i64x3 = ctypes.c_int64 * 3
+
+
+class PisaNormRopeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "tokens", "heads_q", "heads_kv", "head_dim", "rotary_dim",
+                                               "interleaved")] + \
+               [("eps", ctypes.c_float)] + [(n, _i64x3) for n in ("xq_stride", "xk_stride", "dxq_stride", "dxk_stride")]
+
+
+class PisaCacheShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "heads_kv", "capacity", "head_dim", "format")]
+
+
+class PisaTreeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "heads_q", "heads_kv", "drafts", "capacity", "head_dim", "format",
+                                               "block", "seq_kv", "topk", "select_per_qhead")] + \
+               [("scale", ctypes.c_float)]
+
+CACHE_BF16, CACHE_E4M3 = 0, 1   # pisa_cache_shape.format
+
+
 class PisaError(RuntimeError):
     def __init__(self, status: int, where: str, detail: int | None = None):
         self.status = status
@@ -50,6 +71,7 @@ class PisaError(RuntimeError):
 
 _vp, _i32p, _f32p, _szp = ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)
 _SP = ctypes.POINTER(PisaShape)
+_NP, _CP, _TP = ctypes.POINTER(PisaNormRopeShape), ctypes.POINTER(PisaCacheShape), ctypes.POINTER(PisaTreeShape)
 _sig = {
     "pisa_num_levels": (ctypes.c_int32, [_SP]),
     "pisa_level_layout": (ctypes.c_int, [_SP, _i32p, _i32p]),
@@ -68,6 +90,14 @@ _sig = {
     "pisa_last_launch_count": (ctypes.c_int32, []),
     "pisa_decode_attention_noalloc": (ctypes.c_int, [_SP, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "pisa_decode_noalloc_check_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _vp]),
+    "pisa_qk_norm_rope": (ctypes.c_int, [_NP] + [_vp] * 9),
+    "pisa_norm_rope_workspace_size": (ctypes.c_int, [_NP, _szp]),
+    "pisa_qk_norm_rope_backward": (ctypes.c_int, [_NP] + [_vp] * 13 + [ctypes.c_size_t, _vp]),
+    "pisa_cache_write": (ctypes.c_int, [_CP, ctypes.c_int32, _vp, _vp, _i64x3, _i64x3] + [_vp] * 8),
+    "pisa_cache_read": (ctypes.c_int, [_CP, ctypes.c_int32] + [_vp] * 10),
+    "pisa_cache_append_pyramid": (ctypes.c_int, [_SP, _vp, _vp, _vp, ctypes.c_int32, _vp]),
+    "pisa_tree_workspace_size": (ctypes.c_int, [_TP, _szp]),
+    "pisa_tree_attention": (ctypes.c_int, [_TP] + [_vp] * 13 + [ctypes.c_size_t, _vp]),
     "pisa_selftest_wait_timeout": (ctypes.c_int, [_vp, ctypes.c_uint32, _vp]),
 }
 for _name, (_res, _args) in _sig.items():
@@ -113,6 +143,15 @@ class Shape:
     def kv_rows(self) -> int:
         """Rows of one K/V plane: the capacity of a growing cache, else seq_kv."""
         return self.kv_capacity or self.seq_kv
+
+    @property
+    def n_nodes(self) -> int:
+        """Rows of one pyramid plane: level sizes n_0 = kv_rows / block, ceil(n / factor) while n > factor."""
+        n = total = self.kv_rows // self.block
+        while n > self.factor >= 2:
+            n = -(-n // self.factor)
+            total += n
+        return total
 
     @property
     def hsel(self) -> int:
@@ -408,6 +447,370 @@ class Session:
                 ho[a:b].copy_(do[a:b], non_blocking=True)
         compute.wait_stream(self.out_stream)
         return out
+
+
+# ----------------------------------------------------------------------------- around the attention
+
+def _device_of(named, stream):
+    """The one CUDA device that all tensors of `named` ((tensor, name), tensor None = absent) are on,
+    and the raw stream: `stream`, which must be that device's, or the device's current one."""
+    torch = _torch()
+    dev = None
+    for t, name in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if stream is None:
+        return dev, torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"the stream must be one of {dev}, got {stream.device}")
+    return dev, stream.cuda_stream
+
+
+def _on(dev, call, *args) -> int:
+    """The call's status with `dev` current (kernels launch on the current device)."""
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        return call(*args)
+    with torch.cuda.device(dev):
+        return call(*args)
+
+
+def _like(t, dtype, shape, name):
+    """A contiguous tensor of this type and shape (its device is checked by _device_of)."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _rows_like(t, dtype, shape, name):
+    """A tensor of this type and shape whose last dim is adjacent; returns its other strides (0 for
+    dims of one, whose stride says nothing)."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name} must have adjacent elements in its last dimension")
+    return _i64x3(*[0 if n == 1 else x for n, x in zip(shape[:3], st[:3])])
+
+
+def _status_word(ws):
+    torch = _torch()
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.numel() < 256:
+        raise ValueError("ws must be a contiguous uint8 tensor of at least 256 bytes")
+    return ws
+
+
+@dataclasses.dataclass(frozen=True)
+class NormRopeShape:
+    """Problem description of qk_norm_rope (mirrors pisa_norm_rope_shape; the strides come from the
+    tensors of a call)."""
+    batch: int
+    tokens: int
+    heads_q: int
+    heads_kv: int
+    head_dim: int
+    rotary_dim: int
+    interleaved: int = 0
+    eps: float = 1e-6
+
+    def c(self, xq=None, xk=None, dxq=None, dxk=None) -> PisaNormRopeShape:
+        z = _i64x3()
+        return PisaNormRopeShape(self.batch, self.tokens, self.heads_q, self.heads_kv, self.head_dim, self.rotary_dim,
+                                 int(self.interleaved), float(self.eps), xq or z, xk or z, dxq or z, dxk or z)
+
+
+def norm_rope_workspace_size(shape: NormRopeShape) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.pisa_norm_rope_workspace_size(ctypes.byref(shape.c()), ctypes.byref(n)),
+           "pisa_norm_rope_workspace_size")
+    return n.value
+
+
+def new_norm_rope_workspace(shape: NormRopeShape, device):
+    """Workspace of qk_norm_rope_backward (needs no clearing)."""
+    torch = _torch()
+    return torch.empty(norm_rope_workspace_size(shape), dtype=torch.uint8, device=device)
+
+
+def _norm_rope_args(s: NormRopeShape, Xq, Xk, pos, inv_freq, wq, wk):
+    torch = _torch()
+    B, T, D = s.batch, s.tokens, s.head_dim
+    sq = _rows_like(Xq, torch.bfloat16, (B, T, s.heads_q, D), "Xq")
+    sk = _rows_like(Xk, torch.bfloat16, (B, T, s.heads_kv, D), "Xk")
+    if s.rotary_dim or pos is not None:
+        _like(pos, torch.int32, (B, T), "pos")
+    if s.rotary_dim or inv_freq is not None:
+        _like(inv_freq, torch.float32, (s.rotary_dim // 2,), "inv_freq")
+    for w, name in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            _like(w, torch.float32, (D,), name)
+    return sq, sk
+
+
+def qk_norm_rope(shape: NormRopeShape, Xq, Xk, pos, inv_freq, wq=None, wk=None, Q=None, K=None, stream=None):
+    """RMS norm of every head of Xq [B, T, heads_q, D] and Xk [B, T, heads_kv, D] (bf16, any strides:
+    views into a packed projection) with weights wq, wk (fp32 [D], None = ones), and rotation of its
+    first rotary_dim dims by pos (int32 [B, T]) times inv_freq (fp32 [rotary_dim / 2]). Returns Q
+    [B, heads_q, T, D] and K [B, heads_kv, T, D], the attention's layout."""
+    torch = _torch()
+    s = shape
+    sq, sk = _norm_rope_args(s, Xq, Xk, pos, inv_freq, wq, wk)
+    if Q is None:
+        Q = torch.empty((s.batch, s.heads_q, s.tokens, s.head_dim), dtype=torch.bfloat16, device=Xq.device)
+    else:
+        _like(Q, torch.bfloat16, (s.batch, s.heads_q, s.tokens, s.head_dim), "Q")
+    if K is None:
+        K = torch.empty((s.batch, s.heads_kv, s.tokens, s.head_dim), dtype=torch.bfloat16, device=Xq.device)
+    else:
+        _like(K, torch.bfloat16, (s.batch, s.heads_kv, s.tokens, s.head_dim), "K")
+    dev, st = _device_of(((Xq, "Xq"), (Xk, "Xk"), (pos, "pos"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"),
+                          (Q, "Q"), (K, "K")), stream)
+    _check(_on(dev, _lib.pisa_qk_norm_rope, s.c(sq, sk), Xq.data_ptr(), Xk.data_ptr(), _ptr(wq), _ptr(wk),
+               _ptr(inv_freq), _ptr(pos), Q.data_ptr(), K.data_ptr(), st), "pisa_qk_norm_rope")
+    return Q, K
+
+
+def qk_norm_rope_backward(shape: NormRopeShape, Xq, Xk, pos, inv_freq, dQ, dK, wq=None, wk=None, ws=None, dXq=None,
+                          dXk=None, stream=None):
+    """Gradients of qk_norm_rope for dQ [B, heads_q, T, D] and dK: (dXq, dXk, dwq, dwk). dXq and dXk
+    (the shapes of Xq and Xk; new contiguous tensors if None) may be views into a packed gradient.
+    dwq, dwk: fp32 [D], None where the weight is None."""
+    torch = _torch()
+    s = shape
+    B, T, D = s.batch, s.tokens, s.head_dim
+    sq, sk = _norm_rope_args(s, Xq, Xk, pos, inv_freq, wq, wk)
+    _like(dQ, torch.bfloat16, (B, s.heads_q, T, D), "dQ")
+    _like(dK, torch.bfloat16, (B, s.heads_kv, T, D), "dK")
+    dev = Xq.device
+    if dXq is None:
+        dXq = torch.empty((B, T, s.heads_q, D), dtype=torch.bfloat16, device=dev)
+    if dXk is None:
+        dXk = torch.empty((B, T, s.heads_kv, D), dtype=torch.bfloat16, device=dev)
+    gq = _rows_like(dXq, torch.bfloat16, (B, T, s.heads_q, D), "dXq")
+    gk = _rows_like(dXk, torch.bfloat16, (B, T, s.heads_kv, D), "dXk")
+    dwq = torch.empty(D, dtype=torch.float32, device=dev) if wq is not None else None
+    dwk = torch.empty(D, dtype=torch.float32, device=dev) if wk is not None else None
+    if ws is None:
+        ws = new_norm_rope_workspace(s, dev)
+    dev, st = _device_of(((Xq, "Xq"), (Xk, "Xk"), (pos, "pos"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"),
+                          (dQ, "dQ"), (dK, "dK"), (dXq, "dXq"), (dXk, "dXk"), (ws, "ws")), stream)
+    _check(_on(dev, _lib.pisa_qk_norm_rope_backward, s.c(sq, sk, gq, gk), Xq.data_ptr(), Xk.data_ptr(), _ptr(wq),
+               _ptr(wk), _ptr(inv_freq), _ptr(pos), dQ.data_ptr(), dK.data_ptr(), dXq.data_ptr(), dXk.data_ptr(),
+               _ptr(dwq), _ptr(dwk), ws.data_ptr(), ws.numel() * ws.element_size(), st), "pisa_qk_norm_rope_backward")
+    return dXq, dXk, dwq, dwk
+
+
+@dataclasses.dataclass(frozen=True)
+class CacheShape:
+    """Problem description of a K/V cache (mirrors pisa_cache_shape)."""
+    batch: int
+    heads_kv: int
+    capacity: int
+    head_dim: int
+    format: int = CACHE_E4M3
+
+    def c(self) -> PisaCacheShape:
+        return PisaCacheShape(self.batch, self.heads_kv, self.capacity, self.head_dim, int(self.format))
+
+
+class Cache:
+    """A K/V cache's buffers: k and v [B, heads_kv, capacity, D] (bf16, or float8_e4m3fn with the
+    exponent bytes k_exp and v_exp, uint8 [B, heads_kv, capacity]: a row is its values times
+    2^(byte - 127)). v and v_exp may be None for calls that only read keys (cache_append_pyramid)."""
+
+    def __init__(self, shape: CacheShape, k, v, k_exp=None, v_exp=None):
+        torch = _torch()
+        s = shape
+        fp8 = s.format == CACHE_E4M3
+        rows = (s.batch, s.heads_kv, s.capacity)
+        for t, e, name in ((k, k_exp, "k"), (v, v_exp, "v")):
+            if t is None and name == "v":
+                if e is not None:
+                    raise ValueError("v_exp without v")
+                continue
+            _like(t, torch.float8_e4m3fn if fp8 else torch.bfloat16, (*rows, s.head_dim), name)
+            if fp8:
+                if e is None:
+                    raise ValueError(f"{name}_exp is missing")
+                _like(e, torch.uint8, rows, f"{name}_exp")
+            elif e is not None:
+                raise ValueError(f"{name}_exp belongs to an e4m3 cache")
+        self.shape, self.k, self.v, self.k_exp, self.v_exp = s, k, v, k_exp, v_exp
+        self.device = k.device
+        self._c = s.c()
+        self._named = ((k, "k"), (v, "v"), (k_exp, "k_exp"), (v_exp, "v_exp"))
+        _device_of(self._named, None) if k.is_cuda else None
+
+    def _both(self):
+        if self.v is None:
+            raise ValueError("the cache has no v")
+        return self
+
+
+def new_cache(shape: CacheShape, device) -> Cache:
+    """A cache whose rows are all zero."""
+    torch = _torch()
+    s = shape
+    fp8 = s.format == CACHE_E4M3
+    dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    k, v = (torch.zeros((s.batch, s.heads_kv, s.capacity, s.head_dim), dtype=dt, device=device) for _ in range(2))
+    ke, ve = (torch.ones((s.batch, s.heads_kv, s.capacity), dtype=torch.uint8, device=device) if fp8 else None
+              for _ in range(2))
+    return Cache(s, k, v, ke, ve)
+
+
+def new_cache_workspace(device):
+    """A status word for cache_write and cache_read (any other workspace serves as well)."""
+    torch = _torch()
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def _ranges(B, start, count):
+    torch = _torch()
+    for t, name in ((start, "start"), (count, "count")):
+        if t is not None:
+            _like(t, torch.int32, (B,), name)
+
+
+def cache_write(cache: Cache, K, V, ws, start=None, count=None, stream=None) -> None:
+    """Writes the rows of K and V (bf16 [B, heads_kv, tokens, D], any strides) to the positions
+    start[b] + t, t < count[b] (int32 [B] on the device; 0 and all rows if None), quantising them if
+    the cache is e4m3. A sequence whose rows do not fit is left alone and recorded in ws."""
+    torch = _torch()
+    s = cache._both().shape
+    rows = (s.batch, s.heads_kv, K.shape[2] if K.dim() == 4 else -1, s.head_dim)
+    sk, sv = _rows_like(K, torch.bfloat16, rows, "K"), _rows_like(V, torch.bfloat16, rows, "V")
+    _ranges(s.batch, start, count)
+    _status_word(ws)
+    dev, st = _device_of(((cache.k, "cache"), (K, "K"), (V, "V"), (start, "start"), (count, "count"), (ws, "ws")), stream)
+    _check(_on(dev, _lib.pisa_cache_write, cache._c, rows[2], K.data_ptr(), V.data_ptr(), sk, sv, _ptr(start),
+               _ptr(count), cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_exp), _ptr(cache.v_exp),
+               ws.data_ptr(), st), "pisa_cache_write")
+
+
+def cache_read(cache: Cache, tokens: int, ws, start=None, count=None, K=None, V=None, stream=None):
+    """The rows start[b] + t, t < count[b], of K and V as bf16 [B, heads_kv, tokens, D]. Rows that do
+    not count keep what K and V held (zeros in new tensors)."""
+    torch = _torch()
+    s = cache._both().shape
+    rows = (s.batch, s.heads_kv, int(tokens), s.head_dim)
+    if tokens < 1:
+        raise ValueError("tokens must be at least 1")
+    make = torch.empty if count is None and start is None else torch.zeros
+    K = make(rows, dtype=torch.bfloat16, device=cache.device) if K is None else _like(K, torch.bfloat16, rows, "K")
+    V = make(rows, dtype=torch.bfloat16, device=cache.device) if V is None else _like(V, torch.bfloat16, rows, "V")
+    _ranges(s.batch, start, count)
+    _status_word(ws)
+    dev, st = _device_of(((cache.k, "cache"), (K, "K"), (V, "V"), (start, "start"), (count, "count"), (ws, "ws")), stream)
+    _check(_on(dev, _lib.pisa_cache_read, cache._c, rows[2], cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_exp),
+               _ptr(cache.v_exp), _ptr(start), _ptr(count), K.data_ptr(), V.data_ptr(), ws.data_ptr(), st),
+           "pisa_cache_read")
+    return K, V
+
+
+def cache_append_pyramid(shape: Shape, cache: Cache, pyramid, seq_kv_old: int, stream=None):
+    """append_pyramid for an e4m3 cache: brings `pyramid` (fp32 [B, heads_kv, nodes, D], that of the
+    cache at length seq_kv_old; zeros for 0) up to shape.seq_kv."""
+    torch = _torch()
+    s = cache.shape
+    if s.format != CACHE_E4M3:
+        raise ValueError("cache_append_pyramid takes an e4m3 cache (append_pyramid a bf16 one)")
+    if (s.batch, s.heads_kv, s.capacity, s.head_dim) != (shape.batch, shape.heads_kv, shape.kv_rows, shape.head_dim):
+        raise ValueError("the shape's batch, heads_kv, capacity and head_dim must be the cache's")
+    _like(pyramid, torch.float32, (s.batch, s.heads_kv, shape.n_nodes, s.head_dim), "pyramid")
+    dev, st = _device_of(((cache.k, "cache"), (pyramid, "pyramid")), stream)
+    _check(_on(dev, _lib.pisa_cache_append_pyramid, shape.c(), cache.k.data_ptr(), cache.k_exp.data_ptr(),
+               pyramid.data_ptr(), int(seq_kv_old), st), "pisa_cache_append_pyramid")
+    return pyramid
+
+
+@dataclasses.dataclass(frozen=True)
+class TreeShape:
+    """Problem description of tree_attention (mirrors pisa_tree_shape)."""
+    batch: int
+    heads_q: int
+    heads_kv: int
+    drafts: int
+    capacity: int
+    head_dim: int
+    format: int = CACHE_E4M3
+    block: int = 64
+    seq_kv: int = 0
+    topk: int = 0
+    select_per_qhead: int = 0
+    scale: float = 0.0
+
+    def c(self) -> PisaTreeShape:
+        return PisaTreeShape(self.batch, self.heads_q, self.heads_kv, self.drafts, self.capacity, self.head_dim,
+                             int(self.format), self.block, self.seq_kv, self.topk, int(self.select_per_qhead),
+                             float(self.scale))
+
+    @property
+    def hsel(self) -> int:
+        return self.heads_q if self.select_per_qhead else self.heads_kv
+
+
+def tree_workspace_size(shape: TreeShape) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.pisa_tree_workspace_size(ctypes.byref(shape.c()), ctypes.byref(n)), "pisa_tree_workspace_size")
+    return n.value
+
+
+def new_tree_workspace(shape: TreeShape, device):
+    """Workspace of tree_attention with a cleared status word."""
+    torch = _torch()
+    ws = torch.empty(tree_workspace_size(shape), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def tree_attention(shape: TreeShape, cache: Cache, Q, K, V, mask, cache_len, ws, idx=None, O=None, lse=True,
+                   stream=None):
+    """Attention of the drafted tokens Q [B, heads_q, T, D] over the cache's first cache_len[b] rows
+    (int32 [B]; those of the blocks of idx [B, Hsel, 1, topk] and from seq_kv on, or all) and over the
+    drafted K, V [B, heads_kv, T, D] whose bits are set in mask (int64 [B, T], bit j of token t's word
+    = token t attends drafted token j). Returns (O, lse)."""
+    torch = _torch()
+    s, c = shape, cache._both().shape
+    B, Hq, Hkv, T, D = s.batch, s.heads_q, s.heads_kv, s.drafts, s.head_dim
+    if (c.batch, c.heads_kv, c.capacity, c.head_dim, c.format) != (B, Hkv, s.capacity, D, s.format):
+        raise ValueError("the shape's batch, heads_kv, capacity, head_dim and format must be the cache's")
+    _like(Q, torch.bfloat16, (B, Hq, T, D), "Q")
+    _like(K, torch.bfloat16, (B, Hkv, T, D), "K")
+    _like(V, torch.bfloat16, (B, Hkv, T, D), "V")
+    _like(mask, torch.int64, (B, T), "mask")
+    _like(cache_len, torch.int32, (B,), "cache_len")
+    if (idx is not None) != (s.topk > 0):
+        raise ValueError("idx goes with topk > 0")
+    if idx is not None:
+        _like(idx, torch.int32, (B, s.hsel, 1, s.topk), "idx")
+    O = torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=Q.device) if O is None \
+        else _like(O, torch.bfloat16, (B, Hq, T, D), "O")
+    if lse is True:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=Q.device)
+    elif lse is False:
+        lse = None
+    elif lse is not None:
+        _like(lse, torch.float32, (B, Hq, T), "lse")
+    _status_word(ws)
+    dev, st = _device_of(((Q, "Q"), (K, "K"), (V, "V"), (mask, "mask"), (cache_len, "cache_len"), (cache.k, "cache"),
+                          (idx, "idx"), (O, "O"), (lse, "lse"), (ws, "ws")), stream)
+    _check(_on(dev, _lib.pisa_tree_attention, s.c(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), mask.data_ptr(),
+               cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_exp), _ptr(cache.v_exp), cache_len.data_ptr(),
+               _ptr(idx), O.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), st), "pisa_tree_attention")
+    return O, lse
 
 
 # ----------------------------------------------------------------------------- measurement helpers

@@ -21,7 +21,7 @@ bool configure_smem_once(const void* func, int bytes, std::atomic<uint64_t>& don
     return true;
 }
 
-static thread_local int32_t g_launches = 0;
+thread_local int32_t g_launches = 0;
 
 static size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 

@@ -64,7 +64,12 @@ enum : uint32_t {
     kKernSelect = 3,
     kKernAttnBackward = 4,
     kKernSelftest = 5,
+    kKernCache = 6,
+    kKernTree = 7,
 };
+
+// Kernel launches of the calling thread's last compute call (pisa_last_launch_count).
+extern thread_local int32_t g_launches;
 
 // Fault injection on the host: true when the environment variable PISA_FAULT
 // is "launch". Every enqueuing entry point then returns PISA_ERR_CUDA after
@@ -212,6 +217,70 @@ struct BwdParams {
     float scale, scale_log2;
 };
 
+// Blocks of the norm-and-rotation grids: four of 256 threads on each of 148 SMs (rows of partial
+// weight gradients; smaller tiles are taken while a grid has fewer).
+constexpr int kNormRopeBlocks = 592;
+
+struct NormRopeParams {
+    const __nv_bfloat16 *Xq, *Xk;   // strided inputs
+    const __nv_bfloat16 *dQ, *dK;   // backward: gradients of the outputs [B, H, T, D]
+    __nv_bfloat16 *Q, *K;           // outputs [B, H, T, D]
+    __nv_bfloat16 *dXq, *dXk;       // backward: strided outputs
+    const float *wq, *wk, *inv_freq;
+    const int32_t* pos;             // [B, T]
+    float* part;                    // backward: [blocks, 2, D]
+    int64_t xq[3], xk[3], dxq[3], dxk[3];  // element strides: batch, token, head
+    int64_t ntokens, tiles;         // B * T; tiles set by the launcher
+    int32_t T, Hq, Hkv, R, tb, hb;  // tb, hb: tokens and heads of a tile (set by the launcher)
+    float eps;
+};
+
+struct CacheParams {
+    const __nv_bfloat16 *K, *V;     // write: strided rows
+    __nv_bfloat16 *Ko, *Vo;         // read: [B, H, tokens, D]
+    void *Kc, *Vc;
+    uint8_t *ke, *ve;
+    const int32_t *start, *count;   // optional [B]
+    uint32_t* status;
+    int64_t ks[3], vs[3];           // element strides: batch, head, token
+    int32_t B, H, cap, tokens;
+};
+
+// Pyramid of an e4m3 cache: level-0 means of the blocks [b_lo, b_hi), then the nodes over them.
+struct CachePyramidParams {
+    const uint8_t* K;               // e4m3 [planes, N, D]
+    const uint8_t* e;               // [planes, N]
+    float* pyr;                     // fp32 [planes, plane_rows, D]
+    int32_t planes, N, D, blk, factor, L, plane_rows, n0, b_lo, b_hi;
+    int32_t lsize[PISA_MAX_LEVELS];
+    int32_t loff[PISA_MAX_LEVELS];
+};
+
+// Runs (CTAs) of the tree attention: two on each of 148 SMs, one for row tiles of 128 rows. Fixed, so
+// that the workspace and the order of every sum do not depend on the device.
+constexpr int kTreeRuns = 296;
+// Units of 64 keys that a run has on average at least (small jobs take fewer runs).
+constexpr int kTreeMinUnits = 2;
+
+struct TreeParams {
+    const __nv_bfloat16* Q;         // [B, Hq, T, D]
+    const uint64_t* mask;           // [B, T]
+    const uint8_t *k_exp, *v_exp;   // e4m3: [B, Hkv, cap]
+    const int32_t* len;             // [B]
+    const int32_t* idx;             // [B, Hsel, 1, topk] or null
+    float* part;                    // [2 * runs][rm * D + 2 * rm]: o, then (m, l) per row
+    __nv_bfloat16* O;
+    float* lse;                     // optional
+    uint32_t* status;
+    int32_t B, Hq, Hkv, Hsel, g, gh, T, cap, seq, topk, n0, per_qhead;
+    int32_t upb;                    // 64-key units per block
+    int32_t mt, rows_per_seq;       // row tiles per selection row, and per sequence (Hsel * mt)
+    int32_t runs, min_units;        // runs (CTAs) at most, and units one run has at least on average
+    int32_t tp;                     // drafted tokens rounded up to 16
+    int32_t nstg;                   // ring stages (set by the launcher)
+    float scale_log2;
+};
+
 // ---------------------------------------------------------------- launchers (return false on launch error)
 
 bool launch_block_mean(const MeanParams& p, cudaStream_t st);
@@ -232,6 +301,17 @@ pisa_status launch_attn_prefill(const Plan& pl, const void* Q, const void* K, co
 bool launch_attn_prefill_dual(int D, int blk, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                               const AttnParams& p, dim3 grid, cudaStream_t st);
 bool launch_attn_decode(const Plan& pl, const DecodeParams& p, cudaStream_t st, int32_t* launches);
+void norm_rope_tiles(NormRopeParams* p, int D);
+bool launch_norm_rope(NormRopeParams p, int D, bool inter, cudaStream_t st);
+bool launch_norm_rope_backward(NormRopeParams p, int D, bool inter, float* dwq, float* dwk, cudaStream_t st,
+                               int32_t* launches);
+bool launch_cache_write(const CacheParams& p, int D, bool e4m3, cudaStream_t st);
+bool launch_cache_read(const CacheParams& p, int D, bool e4m3, cudaStream_t st);
+bool launch_cache_pyramid(const CachePyramidParams& p, cudaStream_t st, int32_t* launches);
+// Rows of one row tile for a selection row that `rows` = heads x drafted tokens share.
+int tree_row_tile(int rows);
+bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* V, const void* Kc,
+                      const void* Vc, cudaStream_t st, int32_t* launches);
 bool launch_attn_backward(const BwdParams& p, int32_t batch, cudaStream_t st, int32_t* launches);
 // Backward column pass (dK, dV) on the tensor cores (head dim 64 or 128, 64- or 128-key blocks:
 // every shape the library accepts); false when the shape is another one or on a launch error.
@@ -249,6 +329,9 @@ bool configure_smem_once(const void* func, int bytes, std::atomic<uint64_t>& don
 bool make_tmap_2d(CUtensorMap* m, const void* ptr, int64_t rows, int D, int box_rows);
 // 2-D TMA view [rows, D] of an fp32 tensor, boxes of 32 columns x 128 rows, 128-byte swizzle.
 bool make_tmap_2d_f32(CUtensorMap* m, const void* ptr, int64_t rows, int D);
+// 2-D TMA view [rows, D] of an 8-bit tensor, boxes of D columns x box_rows rows, swizzled by the row's
+// D = 64 or 128 bytes.
+bool make_tmap_2d_u8(CUtensorMap* m, const void* ptr, int64_t rows, int D, int box_rows);
 // Dense prefill scoring of one chunk on the tensor cores (grid: tiles, Hsel, batch).
 bool launch_score_tc(const SelectParams& p, dim3 grid, cudaStream_t st);
 // Splits n fp32 values (n % 4 == 0, 16-byte aligned) into a tf32 head (the 13 low mantissa bits

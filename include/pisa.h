@@ -98,7 +98,8 @@ typedef enum {
     PISA_ERR_WORKSPACE = 3,    /* workspace smaller than pisa_workspace_size                 */
     PISA_ERR_CUDA = 4,         /* a CUDA call or kernel launch failed                        */
     PISA_ERR_TIMEOUT = 5,      /* device: a pipeline wait ran out of time                    */
-    PISA_ERR_BAD_INDEX = 6     /* device: a selected block outside [0, n0) or after the query */
+    PISA_ERR_BAD_INDEX = 6     /* device: a selected block outside [0, n0) or after the query, or
+                                  a cache position or length outside the cache             */
 } pisa_status;
 
 #define PISA_MAX_LEVELS 24
@@ -274,6 +275,147 @@ PISA_API pisa_status pisa_decode_attention_noalloc(const pisa_shape *shape, cons
  * library's array (PISA_OK if none) and clears it. `detail`, if not NULL,
  * receives the code locating the error. Allocates nothing. */
 PISA_API pisa_status pisa_decode_noalloc_check_status(uint32_t *detail, pisa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Serving and training operators around the attention. Index and length arrays (int32, uint64)
+ * and fp32 vectors need their own type's alignment only; everything else 16 bytes.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Normalisation and rotation of queries and keys, straight from the projection's output.
+ *   batch, tokens           : T tokens of each of B sequences, both >= 1.
+ *   heads_q, heads_kv       : query and key heads, >= 1 each.
+ *   head_dim                : D, 64 or 128.
+ *   rotary_dim              : R, 0 or a multiple of 16 up to D: the first R dims of a head turn.
+ *   interleaved             : 0 = pairs (i, i + R/2); 1 = pairs (2i, 2i + 1); i < R/2.
+ *   eps                     : added to the mean square, >= 0 and finite.
+ *   xq_stride, xk_stride    : elements between batches, tokens and heads of Xq and Xk (head dims
+ *                             are adjacent). Each >= 0 and a multiple of 8; 0 repeats an input.
+ *   dxq_stride, dxk_stride  : the same for dXq and dXk, which must not overlap in themselves
+ *                             (used by the backward call only). */
+typedef struct {
+    int32_t batch, tokens, heads_q, heads_kv, head_dim, rotary_dim, interleaved;
+    float eps;
+    int64_t xq_stride[3], xk_stride[3];
+    int64_t dxq_stride[3], dxk_stride[3];
+} pisa_norm_rope_shape;
+
+/* For every token and head, with r = (mean x^2 + eps)^(-1/2) and u = x r w (all fp32):
+ *   y_a = u_a cos t - u_b sin t,  y_b = u_a sin t + u_b cos t   for each pair (a, b) of the first R dims,
+ *   y = u elsewhere;  t = pos * inv_freq[i], formed in 64 bits. One rounding, to bf16.
+ *   Xq, Xk   : bf16, strided as the shape says (the query and key parts of a packed projection).
+ *   wq, wk   : fp32 [D] norm weights, or NULL for ones.
+ *   inv_freq : fp32 [R/2] (NULL only when R = 0).
+ *   pos      : int32 [B, T], any values (NULL only when R = 0).
+ *   Q, K     : bf16 outputs [B, heads_q, T, D] and [B, heads_kv, T, D], the attention's layout;
+ *              they must not overlap the inputs. */
+PISA_API pisa_status pisa_qk_norm_rope(const pisa_norm_rope_shape *shape, const void *Xq, const void *Xk,
+                                       const float *wq, const float *wk, const float *inv_freq,
+                                       const int32_t *pos, void *Q, void *K, pisa_stream_t stream);
+
+/* Workspace bytes of pisa_qk_norm_rope_backward (the weight gradients' partial sums). Host only. */
+PISA_API pisa_status pisa_norm_rope_workspace_size(const pisa_norm_rope_shape *shape, size_t *bytes);
+
+/* Gradients of pisa_qk_norm_rope. With du the back-rotated dy and dn = du w:
+ *   dx = r (dn - x r^2 mean(dn x)),  dw = sum over tokens and heads of du x r.
+ *   dQ, dK   : bf16 [B, H, T, D], the gradients of Q and K (those of pisa_sparse_attention_backward).
+ *   dXq, dXk : bf16, strided (so they may be the parts of a packed gradient); every element written;
+ *              they must not overlap the inputs or each other.
+ *   dwq, dwk : fp32 [D] or NULL; with wq (wk) NULL the sums are those of a weight of ones.
+ *   ws       : >= pisa_norm_rope_workspace_size bytes; needs no clearing.
+ * Deterministic: no atomics, every sum in a fixed order. */
+PISA_API pisa_status pisa_qk_norm_rope_backward(const pisa_norm_rope_shape *shape, const void *Xq, const void *Xk,
+                                                const float *wq, const float *wk, const float *inv_freq,
+                                                const int32_t *pos, const void *dQ, const void *dK, void *dXq,
+                                                void *dXk, float *dwq, float *dwk, void *ws, size_t ws_bytes,
+                                                pisa_stream_t stream);
+
+/* A K/V cache: [batch, heads_kv, capacity, head_dim] for K and for V.
+ *   PISA_CACHE_BF16 : bf16 rows, no exponents (k_exp = v_exp = NULL).
+ *   PISA_CACHE_E4M3 : 8-bit rows (e4m3) and one exponent byte e per row in k_exp and v_exp
+ *                     (uint8 [batch, heads_kv, capacity]): the row's values are its bytes' values
+ *                     times 2^(e - 127).
+ *   head_dim 64 or 128, capacity >= 1, batch * heads_kv * capacity < 2^31. */
+#define PISA_CACHE_BF16 0
+#define PISA_CACHE_E4M3 1
+typedef struct {
+    int32_t batch, heads_kv, capacity, head_dim, format;
+} pisa_cache_shape;
+
+/* Writes `tokens` rows of K and V of every sequence into the cache, quantising as it writes: row t
+ * of sequence b goes to position start[b] + t. For PISA_CACHE_E4M3 a row's e is the smallest byte
+ * >= 1 with max |x| <= 448 * 2^(e - 127), and its values are x * 2^(127 - e) rounded to nearest even
+ * (the scaling is exact, so there is one rounding; relative error <= 2^-4, or 2^-10 of 2^(e - 127)
+ * for values that small). A row that holds an infinity or a NaN gets e = 255 and zero bytes, and
+ * reads back as NaN.
+ *   K, V     : bf16 [batch, heads_kv, tokens, D] by strides: k_stride, v_stride = elements between
+ *              batches, heads and tokens, each >= 0 and a multiple of 8 (HOST arrays of 3).
+ *   start    : int32 [batch], device, or NULL for 0.
+ *   count    : int32 [batch], device, or NULL for `tokens`: the rows of each sequence that count;
+ *              the cache keeps what it held elsewhere.
+ *   A sequence with count outside [0, tokens], or whose rows do not fit [0, capacity), is left as
+ *   it was and recorded as PISA_ERR_BAD_INDEX.
+ *   ws       : status word, >= 256 bytes (that of any workspace of this library). */
+PISA_API pisa_status pisa_cache_write(const pisa_cache_shape *shape, int32_t tokens, const void *K, const void *V,
+                                      const int64_t *k_stride, const int64_t *v_stride, const int32_t *start,
+                                      const int32_t *count, void *Kc, void *Vc, uint8_t *k_exp, uint8_t *v_exp,
+                                      void *ws, pisa_stream_t stream);
+
+/* Reads rows back: K[b, h, t] and V[b, h, t] (bf16, contiguous [batch, heads_kv, tokens, D]) are the
+ * cache's rows start[b] + t, for t < count[b]; the outputs keep what they held elsewhere. Values are
+ * rounded once, to bf16 (exact but for exponents below bf16's). start, count, ws and refusals as in
+ * pisa_cache_write. */
+PISA_API pisa_status pisa_cache_read(const pisa_cache_shape *shape, int32_t tokens, const void *Kc, const void *Vc,
+                                     const uint8_t *k_exp, const uint8_t *v_exp, const int32_t *start,
+                                     const int32_t *count, void *K, void *V, void *ws, pisa_stream_t stream);
+
+/* pisa_append_pyramid for a PISA_CACHE_E4M3 cache: the pyramid of the rows' values. `shape` as there
+ * (kv_capacity, or seq_kv when it is 0, is the cache's capacity). The result equals one call from
+ * seq_kv_old = 0 on a zero-filled buffer bit for bit. Nothing at or past seq_kv is read. */
+PISA_API pisa_status pisa_cache_append_pyramid(const pisa_shape *shape, const void *Kc, const uint8_t *k_exp,
+                                               float *pyramid, int32_t seq_kv_old, pisa_stream_t stream);
+
+/* Attention of a tree of drafted tokens over a cache (one drafted token is plain decode).
+ *   batch, heads_q, heads_kv : as in pisa_shape.
+ *   drafts                   : T drafted tokens per sequence, 1 .. 64.
+ *   capacity, head_dim, format : the cache's. capacity is a multiple of block.
+ *   block                    : 64 or 128, the block size of the selection.
+ *   topk                     : entries of one selection row (<= 4096), or 0 to attend the whole cache.
+ *   seq_kv                   : topk > 0: positions that the selection chose from, a multiple of block,
+ *                              block <= seq_kv <= capacity; topk = 0: must be 0.
+ *   select_per_qhead         : 1 = one selection row per query head (topk > 0 only).
+ *   scale                    : softmax scale; <= 0 selects 1/sqrt(head_dim).
+ * Drafted token t of sequence b attends
+ *   - the cached positions p < cache_len[b] that lie in a block of its selection row or at or past
+ *     seq_kv (the tail that no selection covers); with topk = 0 every p < cache_len[b];
+ *   - the drafted tokens j with bit j of mask[b][t] set. */
+typedef struct {
+    int32_t batch, heads_q, heads_kv, drafts, capacity, head_dim, format;
+    int32_t block, seq_kv, topk, select_per_qhead;
+    float scale;
+} pisa_tree_shape;
+
+/* Workspace bytes of pisa_tree_attention; zero the first 256 once (status word). Host only. */
+PISA_API pisa_status pisa_tree_workspace_size(const pisa_tree_shape *shape, size_t *bytes);
+
+/* O = softmax(scale q . k) V over the keys above, and LSE, computed tile by tile.
+ *   Q         : bf16 [B, heads_q, T, D].
+ *   K, V      : bf16 [B, heads_kv, T, D], the drafted tokens' own keys and values (not in the cache).
+ *   mask      : uint64 [B, T], bit j = drafted token j is attended; bits >= T are ignored.
+ *   Kc, Vc, k_exp, v_exp : the cache. What it holds at or past cache_len is never used.
+ *   cache_len : int32 [B], device. A value outside [0, capacity] is clamped and recorded as
+ *               PISA_ERR_BAD_INDEX.
+ *   idx       : int32 [B, Hsel, 1, topk], device, rows as pisa_select_blocks writes them for one query
+ *               token per sequence (Hsel = heads_kv, or heads_q with select_per_qhead); NULL when
+ *               topk = 0. Entries < 0 are skipped; an entry >= seq_kv / block is skipped and recorded as
+ *               PISA_ERR_BAD_INDEX; a repeated entry is attended twice.
+ *   O         : bf16 [B, heads_q, T, D].  lse : optional fp32 [B, heads_q, T] (natural log).
+ *   A token that attends nothing gets O = 0 and LSE = -inf. Keys and values of drafted tokens that a
+ *   token does not attend do not touch its result, whatever they hold.
+ * The result depends on the inputs alone (no atomics in any sum). */
+PISA_API pisa_status pisa_tree_attention(const pisa_tree_shape *shape, const void *Q, const void *K, const void *V,
+                                         const uint64_t *mask, const void *Kc, const void *Vc, const uint8_t *k_exp,
+                                         const uint8_t *v_exp, const int32_t *cache_len, const int32_t *idx, void *O,
+                                         float *lse, void *ws, size_t ws_bytes, pisa_stream_t stream);
 
 /* Self-test of the bounded waits (no counterpart in the paper): enqueues one kernel whose single
  * mbarrier wait can never complete (nothing arrives on the barrier and no copy or MMA is issued).
