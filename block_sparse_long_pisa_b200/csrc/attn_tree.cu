@@ -1,40 +1,48 @@
 // Attention of a tree of drafted tokens over a K/V cache (one drafted token is plain decode).
 //
-//   rows   the T drafted tokens of the gh query heads that share a selection row: gh * T rows, in
-//          row tiles of RM = 16 MG, the M side of every product
-//   keys   the drafted tokens themselves (masked by their ancestor bits), then the cache in units of
-//          64 keys: selected blocks and tail, or all of it, up to the sequence's length
-//   O = softmax(scale Q K^T) V with a running maximum and sum (fp32); no score leaves the registers
+//   rows   the T drafted tokens of the gh query heads that share a selection row: gh * T rows, cut
+//          into row tiles of R (16 .. 128)
+//   keys   the cache in units of 64 keys (selected blocks and tail, or all of it, up to the
+//          sequence's length), two units to a tile of 128, and last the drafted tokens themselves,
+//          masked by their ancestor bits
+//   O = softmax(scale Q K^T) V with a running maximum and sum (fp32); no score leaves the SM
 //
-// Bound: with few rows, the bytes of the cache that are read (each byte once per row tile, and the
-// row tiles of a sequence read it close together, from L2 after the first); with many rows the
-// tensor cores.
+// Bound: the bytes of the cache that are read, each once per row tile (the row tiles of a sequence
+// read them close together, from L2 after the first).
+//
+// Keys on the M side. Both products are taken transposed, S^T = K Q^T and O^T = V^T P^T: the 128
+// keys of a tile fill the M = 128 lanes of tcgen05.mma whatever the number of rows, which is N (16
+// for a decode step: an MMA costs by N), K and V are the A operands straight from the tiles that
+// TMA wrote (V as MN-major), and a softmax thread owns one key: its mask, its exponent bytes and its
+// store of P are its own. The row maximum is the only thing that crosses lanes, so it is kept (in
+// shared memory) until some score exceeds it by 2^kLazy: a tile normally needs one barrier with a
+// vote, and only when the vote says so the maxima are found anew and O is rescaled in TMEM.
+// (Rows on the M side with mma.sync, 16 rows a warp, took 144 us for a decode step over 64 caches of
+// 128K rows, 64 selected 8-bit blocks, and 507 us for trees of 48 tokens over 8 ragged bf16 caches:
+// converting 8-bit fragments was bound by issue, the bf16 rows by that instruction's rate.)
+//
+// e4m3 rows go into the MMA as they are (kind::f8f6f4, K = 32); what is not 8-bit is split:
+//   * a row of Q is scaled by a power of two to a maximum in [224, 448) and taken as e4m3 (4
+//     significant bits) + e5m2 (the remainder of bf16's 8 bits needs 3): exact for values down to
+//     2^-14 of the row's largest, off by 2^-26 of it below;
+//   * P, as fp16, is cut into three e5m2 terms: an e5m2 value is the upper byte of an fp16 one, so
+//     t1 = upper byte of p, t2 of p - t1, t3 of p - t1 - t2: 9 bits or more (bf16 has 8), P at most
+//     2^15, so a probability of 2^-18 of the row's largest still has them and one of 2^-28 counts;
+//   * K's row exponent and Q's multiply the score in fp32; V's goes into P: P' = p 2^(e - 127 - u), O
+//     in units of 2^u, u set by the largest V exponent so far.
+// A bf16 cache takes P as bf16 (range of V); so do the drafted tokens, which are bf16 in both.
 //
 // Work split. Sequences have unlike lengths that only the device knows, so the units of all row
 // tiles are laid end to end and cut into equal runs, one per CTA of a fixed grid; a run may end one
 // row tile, hold whole ones and begin another. A row tile inside one run is finished there; one that
 // crosses runs leaves partial (o, m, l) that attn_tree_merge_kernel joins in run order. Every CTA
-// finds its run by summing the lengths itself: no scheduling pass, no atomics, and the same inputs
-// give the same bits.
+// finds its run by summing the lengths itself: no scheduling pass, no atomics in any sum, and the
+// same inputs give the same bits.
 //
-// CTA: one producer warp keeps a ring of units in flight by TMA (K and V tiles of 64 keys, 128- or
-// 64-byte swizzle, and the exponent bytes of an e4m3 cache); MG x KS consumer warps take 16 rows and
-// every KS-th 16-key chunk each, with mma.sync m16n8k16 (few rows: the chunks are split so that four
-// warps share 16 rows; many rows: each warp has its own). Drafted K/V have a buffer of their own.
-//
-// e4m3 rows are used as fp16: e4m3 values are exact there, and one conversion instruction makes two.
-//   * Q is scaled by a power of two per row to a maximum in [2^14, 2^15) and rounded to fp16, which
-//     keeps bf16's 8 bits for values down to 2^-29 of the row's largest.
-//   * K's row exponent and Q's come back as an exact factor of the score, in fp32.
-//   * V's row exponent goes into P: P' = p 2^(e - u), u the largest exponent so far less 7, O in
-//     units of 2^u. P <= 2^8 (below), so P' <= 2^15 fits fp16; P' keeps its 11 bits down to 2^-21
-//     of the largest row times the largest p, and a floor of 2^-31 below.
-//   * A byte tile's fragments come by ldmatrix as pairs of bytes, so the order of dims inside a
-//     16-dim chunk (Q.K^T, where any order will do) and of output columns (P.V: even dims in one
-//     n-tile, odd in the next) is the one that needs no shuffling.
-// P is bf16 for a bf16 cache (range of V) and for the drafted tokens.
-//
-// The running maximum moves only when a score exceeds it by 2^8, so O is rescaled rarely.
+// CTA (two on an SM where shared memory allows): four softmax warps (thread = key = TMEM lane), a
+// producer warp that keeps a ring of tiles in flight by TMA, and an MMA warp (TMEM allocation, one
+// issuing lane). Order of the MMA lane: S(i+1), then P.V(i), so a tile's scores are formed while the
+// softmax of the one before runs; S is double buffered.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,12 +52,13 @@
 namespace pisa {
 
 constexpr uint32_t kTreeDetail = kKernTree << 8;
-constexpr float kTreeLazy = 8.0f;   // log2 units a score may exceed the kept maximum by
-constexpr int kTreeUMin = -100;     // smallest unit exponent of O (e4m3)
+constexpr int kTreeUMin = -100;  // smallest unit exponent of O (e4m3)
+constexpr int kTreeMaxStages = 8;
+enum : int { kTileEnd = 0, kTileCache = 1, kTileDraft = 2 };
 
 // ---------------------------------------------------------------- the runs
 
-// Units of one row tile of sequence b: the drafted tokens, then the cache.
+// Units of one row tile of sequence b: the cache's, then one for the drafted tokens.
 __device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
     return min(max(p.len[b], 0), p.cap);
 }
@@ -114,249 +123,139 @@ __device__ __forceinline__ void tree_find(const TreeParams& p, int64_t x, int64_
     unit = 0;
 }
 
-// ---------------------------------------------------------------- fragments
+// ---------------------------------------------------------------- operands
 
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+// Shared-memory matrix descriptor; layout: 0 = none, 2 = 128-byte, 4 = 64-byte swizzle.
+__device__ __forceinline__ uint64_t tree_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(layout) << 61);
 }
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+// Instruction descriptor for kind::f8f6f4: A e4m3, B e4m3 (0) or e5m2 (1), fp32 accumulator, M = 128.
+__host__ __device__ constexpr uint32_t idesc_f8(int n, int b_type, int a_mn, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(b_type) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (F16)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
-// two e4m3 values (low 16 bits) -> two fp16
-__device__ __forceinline__ uint32_t f16_of(uint32_t two) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(two));
-    return h;
+
+__device__ __forceinline__ float pow2i(int e) {  // e in [-126, 127]
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
-__device__ __forceinline__ uint32_t f16_of_hi(uint32_t two) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(h) : "r"(two));
-    return h;
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// byte offset of 16-byte chunk `c` of row `row` in a tile of 128-byte (64-byte) swizzled rows
-__device__ __forceinline__ uint32_t at128(int row, int c) {
-    return static_cast<uint32_t>(row * 128 + ((c ^ (row & 7)) << 4));
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
-__device__ __forceinline__ uint32_t at64(int row, int c) {
-    return static_cast<uint32_t>(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
-__device__ __forceinline__ float pow2i(int e) {  // e in [-126, 127]
-    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t cvt_e5m2x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3x2_f32(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+// Barrier over the softmax threads; true if `x` holds in any of them.
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void softmax_sync() { named_bar_sync(1, 128); }
+
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 32)
+        tmem_ld32(taddr, r);
+    else
+        tmem_ld16(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t (&r)[N]) {
+    if constexpr (N == 32)
+        tmem_st32(taddr, r);
+    else
+        tmem_st16(taddr, r);
 }
 
-// Rows r and r + 8 of one warp: running maximum (log2 units), sum of this thread's columns, output
-// accumulators, and the unit exponent of the output (e4m3).
-template <int D>
-struct TreeState {
-    float o[D / 8][4];
-    float m0, m1, l0, l1;
-    int u;
-    bool unit_set;
-};
+// ---------------------------------------------------------------- layout
 
-template <int D>
-__device__ __forceinline__ void scale_rows(TreeState<D>& s, float a0, float a1) {
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-        s.o[j][0] *= a0;
-        s.o[j][1] *= a0;
-        s.o[j][2] *= a1;
-        s.o[j][3] *= a1;
-    }
-}
-
-// Scores (log2 units, -inf where masked) -> probabilities against the running maximum, which moves
-// when a score exceeds it by kTreeLazy. NT n-tiles of 8 keys.
-template <int D, int NT>
-__device__ __forceinline__ void softmax_step(TreeState<D>& s, float (&sc)[NT][4]) {
-    float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        x0 = fmax3(x0, sc[n][0], sc[n][1]);
-        x1 = fmax3(x1, sc[n][2], sc[n][3]);
-    }
-    x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
-    x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 2));
-    const bool up0 = x0 > s.m0 + kTreeLazy, up1 = x1 > s.m1 + kTreeLazy;
-    if (__any_sync(0xFFFFFFFFu, up0 || up1)) {
-        const float a0 = up0 ? fast_exp2(s.m0 - x0) : 1.f, a1 = up1 ? fast_exp2(s.m1 - x1) : 1.f;
-        s.m0 = up0 ? x0 : s.m0;
-        s.m1 = up1 ? x1 : s.m1;
-        s.l0 *= a0;
-        s.l1 *= a1;
-        scale_rows<D>(s, a0, a1);
-    }
-    // a row with no key yet keeps m = -inf: its scores are all -inf and give 0
-    const float r0 = s.m0 == -INFINITY ? 0.f : s.m0, r1 = s.m1 == -INFINITY ? 0.f : s.m1;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        sc[n][0] = fast_exp2(sc[n][0] - r0);
-        sc[n][1] = fast_exp2(sc[n][1] - r0);
-        sc[n][2] = fast_exp2(sc[n][2] - r1);
-        sc[n][3] = fast_exp2(sc[n][3] - r1);
-        s.l0 += sc[n][0] + sc[n][1];
-        s.l1 += sc[n][2] + sc[n][3];
-    }
-}
-
-// Q.K^T of 16 keys from a bf16 tile (128-byte swizzled column tiles of 64 dims, SUB bytes apart).
-template <int D>
-__device__ __forceinline__ void scores_bf16(const uint32_t (&q)[D / 16][4], uint32_t kbase, int sub, int key0,
-                                            float (&c0)[4], float (&c1)[4]) {
-    const int lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-        float (&c)[4] = nt == 0 ? c0 : c1;
-        c[0] = c[1] = c[2] = c[3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-            const int dim = 32 * j + 8 * mi;
-            uint32_t b[4];
-            ldsm4(kbase + (dim / 64) * sub + at128(key0 + 8 * nt + mr, (dim % 64) / 8), b);
-            mma16816<false>(c, q[2 * j], b[0], b[1]);
-            mma16816<false>(c, q[2 * j + 1], b[2], b[3]);
-        }
-    }
-}
-template <int D>
-__device__ __forceinline__ void pv_bf16(TreeState<D>& s, const uint32_t (&p)[4], uint32_t vbase, int sub, int key0) {
-    const int lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-        const int dim = 16 * j + 8 * (mi >> 1);
-        uint32_t b[4];
-        ldsm4_t(vbase + (dim / 64) * sub + at128(key0 + mr + 8 * (mi & 1), (dim % 64) / 8), b);
-        mma16816<false>(s.o[2 * j], p, b[0], b[1]);
-        mma16816<false>(s.o[2 * j + 1], p, b[2], b[3]);
-    }
-}
-
-template <int D>
-__device__ __forceinline__ uint32_t at_e4m3(int key, int c) {
-    return D == 128 ? at128(key, c) : at64(key, c);
-}
-// Q.K^T of 16 keys from an e4m3 tile; a thread's four bytes of a 16-dim chunk are dims 4 (lane % 4) ..
-template <int D>
-__device__ __forceinline__ void scores_e4m3(const uint32_t (&q)[D / 16][4], uint32_t kbase, int key0, float (&c0)[4],
-                                            float (&c1)[4]) {
-    const int lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-        float (&c)[4] = nt == 0 ? c0 : c1;
-        c[0] = c[1] = c[2] = c[3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-            uint32_t b[4];
-            ldsm4(kbase + at_e4m3<D>(key0 + 8 * nt + mr, 4 * j + mi), b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma16816<true>(c, q[4 * j + i], f16_of(b[i]), f16_of_hi(b[i]));
-        }
-    }
-}
-// P.V of 16 keys: n-tile 2g takes the even dims of 16-dim chunk g, n-tile 2g + 1 the odd ones.
-template <int D>
-__device__ __forceinline__ void pv_e4m3(TreeState<D>& s, const uint32_t (&p)[4], uint32_t vbase, int key0) {
-    const int lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-        uint32_t b[4];
-        ldsm4_t(vbase + at_e4m3<D>(key0 + mr + 8 * (mi & 1), 2 * j + (mi >> 1)), b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i], 0u, 0x3120);  // (even, even, odd, odd)
-        mma16816<true>(s.o[4 * j], p, f16_of(b[0]), f16_of(b[1]));
-        mma16816<true>(s.o[4 * j + 1], p, f16_of_hi(b[0]), f16_of_hi(b[1]));
-        mma16816<true>(s.o[4 * j + 2], p, f16_of(b[2]), f16_of(b[3]));
-        mma16816<true>(s.o[4 * j + 3], p, f16_of_hi(b[2]), f16_of_hi(b[3]));
-    }
-}
-
-// Output columns from the bf16 order (n-tile j: dims 8j + 2 (lane % 4), + 1) to the e4m3 order
-// (n-tiles 2g, 2g + 1: dims 16g + 4 (lane % 4) + {0, 2} and + {1, 3}).
-template <int D>
-__device__ __forceinline__ void to_paired_columns(TreeState<D>& s) {
-    const int lane = threadIdx.x & 31, q = lane & 3;
-    const int a = (lane & ~3) | ((2 * q) & 3), b = (lane & ~3) | ((2 * q + 1) & 3);
-#pragma unroll
-    for (int g = 0; g < D / 16; ++g) {
-#pragma unroll
-        for (int r = 0; r < 4; r += 2) {
-            const float e0 = s.o[2 * g][r], e1 = s.o[2 * g][r + 1], f0 = s.o[2 * g + 1][r], f1 = s.o[2 * g + 1][r + 1];
-            const float ea0 = __shfl_sync(0xFFFFFFFFu, e0, a), ea1 = __shfl_sync(0xFFFFFFFFu, e1, a);
-            const float eb0 = __shfl_sync(0xFFFFFFFFu, e0, b), eb1 = __shfl_sync(0xFFFFFFFFu, e1, b);
-            const float fa0 = __shfl_sync(0xFFFFFFFFu, f0, a), fa1 = __shfl_sync(0xFFFFFFFFu, f1, a);
-            const float fb0 = __shfl_sync(0xFFFFFFFFu, f0, b), fb1 = __shfl_sync(0xFFFFFFFFu, f1, b);
-            // dims 4q, 4q+1 live in lane 2q of the half tile (q < 2: first, else second), 4q+2, +3 in the next
-            s.o[2 * g][r] = q < 2 ? ea0 : fa0;
-            s.o[2 * g + 1][r] = q < 2 ? ea1 : fa1;
-            s.o[2 * g][r + 1] = q < 2 ? eb0 : fb0;
-            s.o[2 * g + 1][r + 1] = q < 2 ? eb1 : fb1;
-        }
-    }
-}
-
-// ---------------------------------------------------------------- the kernel
-
-template <int D, bool E4M3>
+template <int D, bool E4M3, int R>
 struct TreeCfg {
-    static constexpr int ROW = E4M3 ? D : 2 * D;           // bytes of a cache row
-    static constexpr int TILE = 64 * ROW;                  // K (or V) of one unit
-    static constexpr int EXPS = E4M3 ? 128 : 0;            // exponent bytes of K and of V
+    static constexpr int ROW = E4M3 ? D : 2 * D;         // bytes of a cache row
+    static constexpr int TILE = 128 * ROW;               // K (or V) of one tile
     static constexpr int STAGE = 2 * TILE;
+    static constexpr int EXPS = E4M3 ? 256 : 0;          // a stage's exponent bytes of K and of V
+    static constexpr int QB = R * 2 * D;                 // Q: bf16, or the e4m3 and the e5m2 terms
+    static constexpr int PTERM = R * 128;                // one 8-bit term of P
+    static constexpr int PB = E4M3 ? 3 * PTERM : 2 * PTERM;
+    // P buffers: one where a second would cost a CTA per SM (e4m3, 64 rows) or a stage (bf16, many rows)
+    static constexpr int NP = (E4M3 ? R == 64 : R > 64) ? 1 : 2;
+    static constexpr int CW = R < 32 ? 16 : 32;          // TMEM columns taken at a time
+    static constexpr int COLS = 3 * R <= 64 ? 64 : 3 * R <= 128 ? 128 : 3 * R <= 256 ? 256 : 512;
+    static constexpr float LAZY = E4M3 ? 4.f : 8.f;      // log2 units a score may exceed the kept maximum by
+    // dynamic shared memory without the ring: Q, P, masks, row parameters (8 floats a row)
+    static constexpr int FIXED = 1024 + QB + NP * PB + R * 8 + R * 32;
+    static constexpr int CTAS = E4M3 && R <= 64 ? 2 : 1;  // CTAs an SM's shared memory takes
 };
 
-// Bytes of dynamic shared memory: ring, exponents, drafted K/V (tp rows), and the combine area.
-template <int D, bool E4M3, int MG, int KS>
-constexpr size_t tree_smem(int nstg, int tp) {
-    return 1024 + static_cast<size_t>(nstg) * (TreeCfg<D, E4M3>::STAGE + TreeCfg<D, E4M3>::EXPS) +
-           2 * static_cast<size_t>(tp) * 2 * D + (KS > 1 ? static_cast<size_t>(KS) * 16 * MG * (16 + 2) * 4 : 0);
-}
-
-template <int D, bool E4M3, int MG, int KS>
-__global__ void __launch_bounds__((MG * KS + 1) * 32, MG == 8 ? 1 : 2)
+template <int D, bool E4M3, int R>
+__global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
                      const TreeParams p) {
-    using C = TreeCfg<D, E4M3>;
-    constexpr int W = MG * KS;       // consumer warps
-    constexpr int NCH = 4 / KS;      // 16-key chunks of a unit per warp
-    constexpr int RM = 16 * MG;
-    constexpr int kMaxStages = 8;
+    using C = TreeCfg<D, E4M3, R>;
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* dk_s = ring + p.nstg * C::STAGE;              // drafted K, then V: [D/64][tp][128 B]
-    const int dsub = p.tp * 128, dtile = (D / 64) * dsub;
-    uint8_t* exps = dk_s + 2 * dtile;                      // [stage][K 64, V 64]
-    float* comb = reinterpret_cast<float*>(exps + p.nstg * C::EXPS);
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], dfull, dempty;
-    __shared__ int meta[kMaxStages];
+    uint8_t* q_s = ring + p.nstg * C::STAGE;
+    uint8_t* p_s = q_s + C::QB;
+    uint64_t* mask_s = reinterpret_cast<uint64_t*>(p_s + C::NP * C::PB);  // [R]
+    float* rf_s = reinterpret_cast<float*>(mask_s + R);  // score factor of a row (e4m3: 2^-(Q's exponent))
+    float* nm_s = rf_s + R;                              // -(kept maximum), 0 while there is none
+    float* m_s = nm_s + R;                               // kept maximum, log2 units
+    float* al_s = m_s + R;                               // factor of O and l in a rescale; 1/l at the end
+    float* w_s = al_s + R;                               // [4 warps][R]
+    uint8_t* exps = reinterpret_cast<uint8_t*>(w_s + 4 * R);  // [stage][K 128, V 128]
+    __shared__ __align__(8) uint64_t full[kTreeMaxStages], empty[kTreeMaxStages], sfull[2], pfull[2], pvdone[2], qfull, done;
+    __shared__ int4 meta[kTreeMaxStages];  // kind, keys that count in the two halves
+    __shared__ uint32_t tmem_slot, dflag[2], wexp[4];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const TreeJob job = tree_job(p);
@@ -367,18 +266,28 @@ __global__ void __launch_bounds__((MG * KS + 1) * 32, MG == 8 ? 1 : 2)
     int unit;
     tree_find(p, pos, tile, unit);
     if (tid == 0) {
-        for (int s = 0; s < p.nstg; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], W);
+        for (int i = 0; i < p.nstg; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 5);  // the softmax warps, and P.V (or the MMA lane itself)
         }
-        mbar_init(&dfull, 1);
-        mbar_init(&dempty, W);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+            mbar_init(&pvdone[i], 1);
+        }
+        mbar_init(&qfull, 4);
+        mbar_init(&done, 1);
         fence_barrier_init();
     }
+    if (warp == 5) tmem_alloc(&tmem_slot, C::COLS);
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_slot;
+    const uint32_t tm_o = tm + 2 * R;
 
     int s = 0;            // ring stage, and the parity of its current use
-    uint32_t par = 0, dpar = 0;
+    uint32_t par = 0;
     bool ok = true;       // cleared by a wait that ran out: nothing more is waited for
     auto advance = [&]() {
         if (++s == p.nstg) {
@@ -386,16 +295,64 @@ __global__ void __launch_bounds__((MG * KS + 1) * 32, MG == 8 ? 1 : 2)
             par ^= 1u;
         }
     };
+    const int dtile = D * 128;  // drafted K (or V) in a stage: [D / 64][64 rows][128 B]
 
-    if (warp == W) {
+    if (warp == 4) {
         // ------------------------------------------------ producer
-        int used = 0, drafts = 0;   // ring slots and draft buffers handed out (lane 0's copies: all full by the end)
+        int used = 0;   // ring slots handed out
         if (lane == 0) {
             prefetch_tmap(&tmK);
             prefetch_tmap(&tmV);
             prefetch_tmap(&tmDK);
             prefetch_tmap(&tmDV);
         }
+        // one slot: kind, and for a tile the first keys of its halves (second -1: absent)
+        auto issue = [&](int kind, int64_t plane, int len, int a0, int a1) {
+            if (lane == 0) {
+                ok = used < p.nstg || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x01u);
+                if (ok) {
+                    uint8_t* kt = ring + s * C::STAGE;
+                    if (kind == kTileEnd) {
+                        meta[s] = make_int4(kind, 0, 0, 0);
+                        mbar_arrive(&full[s]);
+                    } else if (kind == kTileDraft) {
+                        meta[s] = make_int4(kind, 0, 0, 0);
+                        mbar_arrive_expect_tx(&full[s], 2 * p.tp * 2 * D);
+                        const int y = static_cast<int>(plane * p.T);
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            tma_load_2d(kt + c * 8192, &tmDK, 64 * c, y, &full[s]);
+                            tma_load_2d(kt + dtile + c * 8192, &tmDV, 64 * c, y, &full[s]);
+                        }
+                    } else {
+                        const int halves = a1 >= 0 ? 2 : 1;
+                        meta[s] = make_int4(kind, min(64, len - a0), a1 >= 0 ? min(64, len - a1) : 0, 0);
+                        mbar_arrive_expect_tx(&full[s], halves * (C::STAGE + C::EXPS) / 2);
+                        for (int h = 0; h < halves; ++h) {
+                            const int64_t row = plane * p.cap + (h == 0 ? a0 : a1);
+                            const int y = static_cast<int>(row);
+                            if constexpr (E4M3) {
+                                tma_load_2d(kt + h * 64 * D, &tmK, 0, y, &full[s]);
+                                tma_load_2d(kt + C::TILE + h * 64 * D, &tmV, 0, y, &full[s]);
+                                bulk_load(exps + s * 256 + h * 64, p.k_exp + row, 64, &full[s]);
+                                bulk_load(exps + s * 256 + 128 + h * 64, p.v_exp + row, 64, &full[s]);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < D / 64; ++c) {
+                                    tma_load_2d(kt + c * 16384 + h * 8192, &tmK, 64 * c, y, &full[s]);
+                                    tma_load_2d(kt + C::TILE + c * 16384 + h * 8192, &tmV, 64 * c, y, &full[s]);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (ok) {
+                ++used;
+                advance();
+            }
+        };
         while (pos < end && ok) {
             const int b = static_cast<int>(tile / p.rows_per_seq);
             const int hs = static_cast<int>(tile % p.rows_per_seq) / p.mt;
@@ -404,38 +361,17 @@ __global__ void __launch_bounds__((MG * KS + 1) * 32, MG == 8 ? 1 : 2)
             const int len = tree_len(p, b);
             const int units = tree_units(p, len);
             const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
-            const bool first_of_seq = tile % p.rows_per_seq == 0 && unit == 0;
-            if (first_of_seq && lane == 0 && p.len[b] != len)
+            if (tile % p.rows_per_seq == 0 && unit == 0 && lane == 0 && p.len[b] != len)
                 record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB0u);
-            int u = unit;
-            if (u == 0) {
-                if (lane == 0) {
-                    ok = drafts == 0 || mbar_wait(&dempty, dpar ^ 1u, p.status, kTreeDetail | 0x01u);
-                    if (ok) {
-                        mbar_arrive_expect_tx(&dfull, 2 * dtile);
-                        const int y = static_cast<int>(plane * p.T);
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c) {
-                            tma_load_2d(dk_s + c * dsub, &tmDK, 64 * c, y, &dfull);
-                            tma_load_2d(dk_s + dtile + c * dsub, &tmDV, 64 * c, y, &dfull);
-                        }
-                    }
-                }
-                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-                if (ok) {
-                    ++drafts;
-                    dpar ^= 1u;
-                }
-                ++u;
-            }
             const int32_t* row = p.topk > 0 ? p.idx + (static_cast<int64_t>(b) * p.Hsel + hs) * p.topk : nullptr;
             const int nsel = p.topk * p.upb;
-            while (u < u1 && ok) {
+            const int uc = min(u1, units - 1);  // the last unit is the drafted tokens
+            int first = -1;                     // a unit that waits for its partner
+            for (int u = unit; u < uc && ok; u += 32) {
                 // up to 32 units at a time: position of each unit's first key, -1 = nothing there
-                const int n = min(32, u1 - u);
                 int at = -1;
-                if (lane < n) {
-                    const int c = u + lane - 1;
+                if (u + lane < uc) {
+                    const int c = u + lane;
                     if (p.topk == 0) {
                         at = 64 * c;
                     } else if (c >= nsel) {
@@ -448,462 +384,596 @@ __global__ void __launch_bounds__((MG * KS + 1) * 32, MG == 8 ? 1 : 2)
                             at = (j * p.upb + c % p.upb) * 64;
                     }
                 }
-                const uint32_t have = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < len);
-                for (uint32_t left = have; left != 0 && ok; left &= left - 1) {
+                for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < len); left != 0 && ok; left &= left - 1) {
                     const int a = __shfl_sync(0xFFFFFFFFu, at, __ffs(left) - 1);
-                    if (lane == 0) {
-                        ok = used < p.nstg || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x02u);
-                        if (ok) {
-                            meta[s] = min(64, len - a);
-                            uint8_t* kt = ring + s * C::STAGE;
-                            mbar_arrive_expect_tx(&full[s], C::STAGE + C::EXPS);
-                            const int y = static_cast<int>(plane * p.cap + a);
-                            if constexpr (E4M3) {
-                                tma_load_2d(kt, &tmK, 0, y, &full[s]);
-                                tma_load_2d(kt + C::TILE, &tmV, 0, y, &full[s]);
-                                bulk_load(exps + s * 128, p.k_exp + plane * p.cap + a, 64, &full[s]);
-                                bulk_load(exps + s * 128 + 64, p.v_exp + plane * p.cap + a, 64, &full[s]);
-                            } else {
-#pragma unroll
-                                for (int c = 0; c < D / 64; ++c) {
-                                    tma_load_2d(kt + c * 8192, &tmK, 64 * c, y, &full[s]);
-                                    tma_load_2d(kt + C::TILE + c * 8192, &tmV, 64 * c, y, &full[s]);
-                                }
-                            }
-                        }
+                    if (first < 0) {
+                        first = a;
+                    } else {
+                        issue(kTileCache, plane, len, first, a);
+                        first = -1;
                     }
-                    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-                    if (ok) {
-                        ++used;
-                        advance();
-                    }
-                }
-                u += n;
-            }
-            // end of the piece: a slot without a tile
-            if (ok) {
-                if (lane == 0) {
-                    ok = used < p.nstg || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x03u);
-                    if (ok) {
-                        meta[s] = 0;
-                        mbar_arrive(&full[s]);
-                    }
-                }
-                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-                if (ok) {
-                    ++used;
-                    advance();
                 }
             }
+            if (first >= 0 && ok) issue(kTileCache, plane, len, first, -1);
+            if (u1 == units && ok) issue(kTileDraft, plane, len, 0, 0);
+            if (ok) issue(kTileEnd, plane, len, 0, 0);
             pos += u1 - unit;
             unit = 0;
             ++tile;
         }
-        // every copy lands before the block ends, also when a consumer gave up (a stage is always
-        // waited for by its latest use; earlier uses were complete before it was filled again)
+        // every copy lands before the block ends, also when another role gave up (earlier uses of a
+        // stage were complete before it was filled again)
         if (lane == 0) {
             for (int i = 0; i < p.nstg && i < used; ++i) {
                 s = s == 0 ? p.nstg - 1 : s - 1;
                 if (s == p.nstg - 1) par ^= 1u;
-                if (!mbar_wait(&full[s], par, p.status, kTreeDetail | 0x04u)) break;
-            }
-            if (drafts > 0) mbar_wait(&dfull, dpar ^ 1u, p.status, kTreeDetail | 0x05u);
-        }
-        __syncthreads();
-        return;
-    }
-
-    // ---------------------------------------------------- consumers
-    const int mg = warp % MG, kg = warp / MG;
-    const int r = lane >> 2, q4 = lane & 3;
-    const int rows = p.gh * p.T;
-    while (pos < end) {
-        const int b = static_cast<int>(tile / p.rows_per_seq);
-        const int rem = static_cast<int>(tile % p.rows_per_seq);
-        const int hs = rem / p.mt, row_base = (rem % p.mt) * RM;
-        const int units = tree_units(p, tree_len(p, b));
-        const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
-        const int64_t out0 = (static_cast<int64_t>(b) * p.Hq + hs * p.gh) * p.T;  // first output row of the group
-        const int ra = row_base + 16 * mg + r, rb = ra + 8;                       // this thread's rows of the group
-        const __nv_bfloat16* qa = p.Q + (out0 + ra) * D;
-        const __nv_bfloat16* qb = p.Q + (out0 + rb) * D;
-
-        TreeState<D> st;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.f;
-        st.m0 = st.m1 = -INFINITY;
-        st.l0 = st.l1 = 0.f;
-        st.u = 0;
-        st.unit_set = false;
-
-        uint32_t qf[D / 16][4];
-        if (!E4M3 || unit == 0) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t* x = reinterpret_cast<const uint32_t*>(qa + 16 * k) + q4;
-                const uint32_t* y = reinterpret_cast<const uint32_t*>(qb + 16 * k) + q4;
-                qf[k][0] = ra < rows ? __ldg(x) : 0u;
-                qf[k][1] = rb < rows ? __ldg(y) : 0u;
-                qf[k][2] = ra < rows ? __ldg(x + 4) : 0u;
-                qf[k][3] = rb < rows ? __ldg(y + 4) : 0u;
+                if (!mbar_wait(&full[s], par, p.status, kTreeDetail | 0x02u)) break;
             }
         }
-        if (unit == 0) {
-            const uint64_t* mrow = p.mask + static_cast<int64_t>(b) * p.T;
-            const uint64_t live = p.T == 64 ? ~0ull : (1ull << p.T) - 1ull;
-            const uint64_t ma = ra < rows ? __ldg(mrow + ra % p.T) & live : 0ull;
-            const uint64_t mb = rb < rows ? __ldg(mrow + rb % p.T) & live : 0ull;
-            if (ok) ok = mbar_wait(&dfull, dpar, p.status, kTreeDetail | 0x06u);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (ok) {
-                dpar ^= 1u;
-                const uint32_t kb = smem_u32(dk_s), vb = kb + dtile;
-                for (int c = kg; 16 * c < p.T; c += KS) {
-                    const int key0 = 16 * c;
-                    float sc[2][4];
-                    scores_bf16<D>(qf, kb, dsub, key0, sc[0], sc[1]);
+    } else if (warp == 5) {
+        // ------------------------------------------------ MMA
+        if (lane == 0) {
+            const uint32_t q0 = smem_u32(q_s), p0 = smem_u32(p_s);
+            int it = 0;               // tiles so far
+            uint32_t qpar = 0;
+            bool issued = false;
+            int pend_s = -1, pend_kind = 0;
+            bool fresh = true;        // the next P.V begins O
+            auto pv = [&]() {         // P.V of the tile before (number it - 1 when called)
+                const int j = it - 1;
+                ok = mbar_wait(&pfull[j & 1], (j >> 1) & 1, p.status, kTreeDetail | 0x03u);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t pb = p0 + (j % C::NP) * C::PB;
+                const uint32_t vt = smem_u32(ring + pend_s * C::STAGE);
+                if (pend_kind == kTileDraft || !E4M3) {
+                    const bool draft = pend_kind == kTileDraft;
+                    const uint32_t sub = draft ? 8192 : 16384;
+                    const uint64_t a = tree_desc(vt + (draft ? dtile : C::TILE), D == 128 ? sub : 0, 1024, 2);
+                    const uint64_t b = tree_desc(pb, 128, 2048, 0);
+                    const int steps = draft ? p.tp / 16 : 8;
+                    for (int k = 0; k < steps; ++k)
+                        mma_bf16_ss(tm_o, desc_at(a, k * 2048), desc_at(b, k * 256), idesc_bf16_f32(128, R, 1, 1),
+                                    !fresh || k > 0 ? 1u : 0u);
+                } else {
+                    const uint64_t a = D == 128 ? tree_desc(vt + C::TILE, 0, 1024, 2) : tree_desc(vt + C::TILE, 0, 512, 4);
+                    const uint64_t b = tree_desc(pb, 128, 2048, 0);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
+                    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = key0 + 8 * n + 2 * q4 + e;
-                            sc[n][e] = (ma >> key) & 1ull ? sc[n][e] * p.scale_log2 : -INFINITY;
-                            sc[n][2 + e] = (mb >> key) & 1ull ? sc[n][2 + e] * p.scale_log2 : -INFINITY;
+                        for (int t = 0; t < 3; ++t)
+                            mma_f8_ss(tm_o, desc_at(a, k * 32 * D), desc_at(b, t * C::PTERM + k * 512), idesc_f8(R, 1, 1, 1),
+                                      !fresh || k > 0 || t > 0 ? 1u : 0u);
+                    }
+                }
+                fresh = false;
+                mma_commit(&empty[pend_s]);
+                mma_commit(&pvdone[j % C::NP]);
+            };
+            while (pos < end && ok) {
+                const int b = static_cast<int>(tile / p.rows_per_seq);
+                const int units = tree_units(p, tree_len(p, b));
+                const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
+                fresh = true;
+                bool first = true;
+                while (ok) {
+                    ok = mbar_wait(&full[s], par, p.status, kTreeDetail | 0x05u);
+                    if (!ok) break;
+                    const int kind = meta[s].x;
+                    if (kind == kTileEnd) {
+                        if (pend_s >= 0) pv();
+                        pend_s = -1;
+                        if (ok) {
+                            mbar_arrive(&empty[s]);
+                            advance();
+                        }
+                        break;
+                    }
+                    if (first || (E4M3 && kind == kTileDraft)) {  // for the drafted tokens Q comes again, as bf16
+                        ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x06u);
+                        qpar ^= 1u;
+                        first = false;
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
+                    const uint32_t kt = smem_u32(ring + s * C::STAGE);
+                    const uint32_t d = tm + (it & 1) * R;
+                    issued = true;
+                    if (kind == kTileDraft || !E4M3) {
+                        const uint32_t sub = kind == kTileDraft ? 8192 : 16384;
+                        const uint64_t a = tree_desc(kt, 16, 1024, 2), bq = tree_desc(q0, 16, 1024, 2);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_bf16_ss(d, desc_at(a, (k / 4) * sub + (k % 4) * 32), desc_at(bq, (k / 4) * (R * 128) + (k % 4) * 32),
+                                        idesc_bf16_f32(128, R, 0, 0), k > 0 ? 1u : 0u);
+                    } else {
+                        const uint64_t a = D == 128 ? tree_desc(kt, 16, 1024, 2) : tree_desc(kt, 16, 512, 4);
+                        const uint64_t bq = D == 128 ? tree_desc(q0, 16, 1024, 2) : tree_desc(q0, 16, 512, 4);
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, k * 32), idesc_f8(R, 0, 0, 0), k > 0 ? 1u : 0u);
+                            mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, R * D + k * 32), idesc_f8(R, 1, 0, 0), 1u);
                         }
                     }
-                    softmax_step<D, 2>(st, sc);
-                    // an infinity or NaN among the chunk's values would reach masked rows through 0 * x
-                    const int vr = key0 + (lane & 15);
-                    uint32_t top = 0;
+                    mma_commit(&sfull[it & 1]);
+                    if (pend_s >= 0) pv();
+                    pend_s = s;
+                    pend_kind = kind;
+                    ++it;
+                    advance();
+                }
+                pos += u1 - unit;
+                unit = 0;
+                ++tile;
+            }
+            if (issued) {  // nothing of this CTA's still runs when TMEM goes
+                mma_commit(&done);
+                mbar_wait(&done, 0, p.status, kTreeDetail | 0x07u);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ softmax: thread = key of the tile = TMEM lane
+        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;  // TMEM lane base of the warp
+        const int rows = p.gh * p.T;
+        int it = 0;
+        while (pos < end && ok) {
+            const int b = static_cast<int>(tile / p.rows_per_seq);
+            const int rem = static_cast<int>(tile % p.rows_per_seq);
+            const int hs = rem / p.mt, row_base = (rem % p.mt) * R;
+            const int units = tree_units(p, tree_len(p, b));
+            const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
+            const int64_t out0 = (static_cast<int64_t>(b) * p.Hq + hs * p.gh) * p.T;  // first row of the group
+            const int nrows = min(R, rows - row_base);
+            const uint4* qg = reinterpret_cast<const uint4*>(p.Q + (out0 + row_base) * D);
+
+            // Q as bf16: [D / 64][R rows][128 B], 128-byte swizzle
+            auto q_bf16 = [&]() {
+                for (int e = tid; e < R * (D / 8); e += 128) {
+                    const int r = e / (D / 8), c = e % (D / 8);
+                    const uint4 x = r < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(q_s + (c / 8) * (R * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = x;
+                }
+            };
+            // Q as e4m3 + e5m2 terms [R rows][D B], swizzled by the row's size; D/8 lanes hold a row
+            auto q_terms = [&]() {
+                for (int e = tid; e < R * (D / 8); e += 128) {  // R * D / 8 is a multiple of 128
+                    const int r = e / (D / 8), c = e % (D / 8);
+                    const uint4 x = r < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    float v[8], top = 0.f;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const int ch = (lane >> 4) * (D / 16) + i;  // 16-byte chunk of the row
-                        const uint4 x = *reinterpret_cast<const uint4*>(dk_s + dtile + (ch / 8) * dsub + at128(vr, ch % 8));
-                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                                                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+                    for (int k = 0; k < 8; ++k) {
+                        v[k] = __uint_as_float((k & 1) ? (w[k / 2] & 0xFFFF0000u) : (w[k / 2] << 16));
+                        top = fmaxf(top, fabsf(v[k]));
                     }
-                    const bool odd = max(top & 0xFFFFu, top >> 16) >= 0x7F80u;
-                    if (!__any_sync(0xFFFFFFFFu, odd)) {
-                        const uint32_t pa[4] = {pack_bf16x2(sc[0][0], sc[0][1]), pack_bf16x2(sc[0][2], sc[0][3]),
-                                                pack_bf16x2(sc[1][0], sc[1][1]), pack_bf16x2(sc[1][2], sc[1][3])};
-                        pv_bf16<D>(st, pa, vb, dsub, key0);
+#pragma unroll
+                    for (int o = 1; o < D / 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    // 2^(f - 127) brings the maximum to [224, 448): 448 = 1.75 * 2^8
+                    const uint32_t tb = __float_as_uint(top);
+                    const int f = min(253, 127 + 8 + 127 - static_cast<int>(tb >> 23) - ((tb & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+                    const float sc = __uint_as_float(static_cast<uint32_t>(f) << 23);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float a = v[2 * k] * sc, bb = v[2 * k + 1] * sc;
+                        hi[k] = cvt_e4m3x2(a, bb);
+                        const float2 h = e4m3x2_f32(hi[k]);
+                        // an infinity saturates: its remainder keeps it (inf - 448) as a NaN
+                        lo[k] = cvt_e5m2x2(a - h.x, bb - h.y);
+                        if (isinf(a)) lo[k] = (lo[k] & 0xFF00u) | 0x7Fu;
+                        if (isinf(bb)) lo[k] = (lo[k] & 0x00FFu) | 0x7F00u;
+                    }
+                    const int ch = c / 2;  // 16-byte chunk of the row
+                    const uint32_t off = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) + 8 * (c & 1)
+                                                  : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) + 8 * (c & 1);
+                    *reinterpret_cast<uint2*>(q_s + off) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+                    *reinterpret_cast<uint2*>(q_s + R * D + off) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+                    if (c == 0) rf_s[r] = __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
+                }
+            };
+            auto q_ready = [&]() {  // this warp's part of it
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&qfull);
+            };
+            if constexpr (E4M3)
+                q_terms();
+            else
+                q_bf16();
+            if (u1 == units && tid < R) {  // this piece ends with the drafted tokens
+                const int rg = row_base + tid;
+                const uint64_t live = p.T == 64 ? ~0ull : (1ull << p.T) - 1ull;
+                mask_s[tid] = rg < rows ? __ldg(p.mask + static_cast<int64_t>(b) * p.T + rg % p.T) & live : 0ull;
+            }
+            if (tid < 2) dflag[tid] = 0;
+            softmax_sync();  // row factors and masks
+
+            uint64_t l2[R / 2];  // this key's share of the rows' sums
+#pragma unroll
+            for (int i = 0; i < R / 2; ++i) l2[i] = 0ull;
+            bool fresh = true;
+            int u = 0, uexp = 0;   // unit exponent of O, and the V exponent it was set by (e4m3)
+
+            while (true) {
+                // Every slot is one barrier, and a second one when the first says so: a warp whose wait ran
+                // out takes both, so that all warps leave together whatever the others saw in the slot.
+                if (ok) ok = mbar_wait(&full[s], par, p.status, kTreeDetail | 0x08u);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                const int4 mt = ok ? meta[s] : make_int4(kTileEnd, 0, 0, 0);
+                if (mt.x == kTileEnd) {
+                    if (softmax_any(!ok) && softmax_any(!ok)) ok = false;
+                    if (ok) {
+                        if (lane == 0) mbar_arrive(&empty[s]);
+                        advance();
+                    }
+                    break;
+                }
+                const bool draft = mt.x == kTileDraft;
+                // Q is handed over at the first tile, not before it is known that there is one: a piece may
+                // hold no tile at all, and its successor's Q must not be announced before the MMA lane
+                // has seen this one's
+                if (E4M3 && draft) {
+                    q_bf16();  // every S of this piece so far is formed: Q's buffer is free
+                    q_ready();
+                } else if (fresh) {
+                    q_ready();
+                }
+                uint8_t* kt = ring + s * C::STAGE;
+                const bool valid = draft ? tid < p.T : (tid & 63) < (tid < 64 ? mt.y : mt.z);
+                const bool partial = draft || mt.y < 64 || mt.z < 64;
+                float kf = p.scale_log2;
+                int ev = 0;
+                if (E4M3 && !draft && valid) {
+                    kf *= __uint_as_float(static_cast<uint32_t>(exps[s * 256 + tid]) << 23);
+                    ev = exps[s * 256 + 128 + tid];
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok) && mbar_wait(&sfull[it & 1], (it >> 1) & 1, p.status, kTreeDetail | 0x09u);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                tc_fence_after();
+                const uint32_t ts = tm + lanes + (it & 1) * R;
+                const uint64_t kf2 = f2_pack(kf, kf);
+
+                // scores against the kept maximum, log2 units, of columns [c0, c0 + CW)
+                auto load_scores = [&](int c0, uint64_t (&x)[C::CW / 2], bool against) {
+                    uint32_t v[C::CW];
+                    tmem_ldn<C::CW>(ts + c0, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < C::CW / 4; ++i) {
+                        const float4 nm = *reinterpret_cast<const float4*>(nm_s + c0 + 4 * i);
+                        uint64_t a = f2_mul(f2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), kf2);
+                        uint64_t c = f2_mul(f2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), kf2);
+                        uint64_t ma = f2_pack(nm.x, nm.y), mc = f2_pack(nm.z, nm.w);
+                        if (!against) ma = mc = 0ull;
+                        if constexpr (E4M3) {
+                            float4 rf = *reinterpret_cast<const float4*>(rf_s + c0 + 4 * i);
+                            if (draft) rf = make_float4(1.f, 1.f, 1.f, 1.f);  // bf16 rows as they are
+                            a = f2_fma(a, f2_pack(rf.x, rf.y), ma);
+                            c = f2_fma(c, f2_pack(rf.z, rf.w), mc);
+                        } else {
+                            a = f2_add(a, ma);
+                            c = f2_add(c, mc);
+                        }
+                        x[2 * i] = a;
+                        x[2 * i + 1] = c;
+                    }
+                    if (draft) {
+#pragma unroll
+                        for (int i = 0; i < C::CW / 2; ++i) {
+                            float lo, hi;
+                            f2_unpack(x[i], lo, hi);
+                            lo = valid && (mask_s[c0 + 2 * i] >> tid) & 1ull ? lo : -INFINITY;
+                            hi = valid && (mask_s[c0 + 2 * i + 1] >> tid) & 1ull ? hi : -INFINITY;
+                            x[i] = f2_pack(lo, hi);
+                        }
+                    }
+                };
+                float top = -INFINITY;
+                if (!fresh) {
+                    for (int c0 = 0; c0 < R; c0 += C::CW) {
+                        uint64_t x[C::CW / 2];
+                        load_scores(c0, x, true);
+#pragma unroll
+                        for (int i = 0; i < C::CW / 2; ++i) {
+                            float lo, hi;
+                            f2_unpack(x[i], lo, hi);
+                            top = fmax3(top, lo, hi);
+                        }
+                    }
+                }
+                const bool over = valid && (top > C::LAZY || (E4M3 && !draft && ev > uexp));
+                if (softmax_any(!ok || fresh || over)) {
+                    if (softmax_any(!ok)) {
+                        ok = false;
+                        break;
+                    }
+                    // the rows' maxima over this tile, and the largest V exponent
+                    for (int c0 = 0; c0 < R; c0 += C::CW) {
+                        uint64_t x[C::CW / 2];
+                        load_scores(c0, x, false);
+                        float mine = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < C::CW / 2; ++i) {
+                            float lo, hi;
+                            f2_unpack(x[i], lo, hi);
+                            lo = warp_max(valid ? lo : -INFINITY);
+                            hi = warp_max(valid ? hi : -INFINITY);
+                            if (lane == 2 * i) mine = lo;
+                            if (lane == 2 * i + 1) mine = hi;
+                        }
+                        if (lane < C::CW) w_s[warp * R + c0 + lane] = mine;
+                    }
+                    if constexpr (E4M3) {
+                        const uint32_t we = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(ev));
+                        if (lane == 0) wexp[warp] = we;
+                    }
+                    softmax_sync();
+                    if (tid < R) {
+                        const float M = fmaxf(fmaxf(w_s[tid], w_s[R + tid]), fmaxf(w_s[2 * R + tid], w_s[3 * R + tid]));
+                        const float old = fresh ? -INFINITY : m_s[tid];
+                        const float now = fmaxf(old, M);
+                        al_s[tid] = now == old ? 1.f : fast_exp2(old - now);
+                        m_s[tid] = now;
+                        nm_s[tid] = now == -INFINITY ? 0.f : -now;
+                    }
+                    float uf = 1.f;
+                    if (E4M3 && !draft) {
+                        const int e = static_cast<int>(min(254u, max(max(wexp[0], wexp[1]), max(wexp[2], wexp[3]))));
+                        if (fresh || e > uexp) {
+                            uexp = e;
+                            const int un = max(kTreeUMin, e - 127 + static_cast<int>(C::LAZY) - 15);
+                            uf = pow2i(max(-126, u - un));  // u - un <= 0 once O holds anything
+                            u = un;
+                        }
+                    }
+                    softmax_sync();
+                    if (!fresh) {
+                        const int j = it - 1;
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[j % C::NP], (j / C::NP) & 1, p.status,
+                                                               kTreeDetail | 0x0Au));
+                        tc_fence_after();
+                        for (int c0 = 0; c0 < R; c0 += C::CW) {
+                            uint32_t v[C::CW];
+                            tmem_ldn<C::CW>(tm_o + lanes + c0, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < C::CW; ++i)
+                                v[i] = __float_as_uint(__uint_as_float(v[i]) * (al_s[c0 + i] * uf));
+                            tmem_stn<C::CW>(tm_o + lanes + c0, v);
+                        }
+                        tmem_wait_st();
+#pragma unroll
+                        for (int i = 0; i < R / 2; ++i) l2[i] = f2_mul(l2[i], f2_pack(al_s[2 * i], al_s[2 * i + 1]));
+                    }
+                    fresh = false;
+                }
+                // P's buffer: the P.V that read it last is complete
+                if (it >= C::NP && ok) {
+                    const int j = it - C::NP;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[j % C::NP], (j / C::NP) & 1, p.status,
+                                                           kTreeDetail | 0x0Bu));
+                }
+                uint8_t* pb = p_s + (it % C::NP) * C::PB;
+                // a row of exponent 255 stands for NaN (its bytes are zero)
+                const float pf = !E4M3 ? 1.f
+                                 : draft ? pow2i(min(127, max(-126, -u)))
+                                         : __uint_as_float(ev == 255 ? 0x7FFFFFFFu : static_cast<uint32_t>(max(ev - u, 0)) << 23);
+                const uint64_t pf2 = f2_pack(pf, pf);
+#pragma unroll
+                for (int c0 = 0; c0 < R; c0 += C::CW) {
+                    uint64_t x[C::CW / 2];
+                    load_scores(c0, x, true);
+                    float pr[C::CW];
+#pragma unroll
+                    for (int i = 0; i < C::CW / 2; ++i) {
+                        float lo, hi;
+                        f2_unpack(x[i], lo, hi);
+                        pr[2 * i] = fast_exp2(lo);
+                        pr[2 * i + 1] = fast_exp2(hi);
+                    }
+                    if (partial) {
+#pragma unroll
+                        for (int i = 0; i < C::CW; ++i) pr[i] = valid ? pr[i] : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < C::CW / 2; ++i) {
+                        x[i] = f2_pack(pr[2 * i], pr[2 * i + 1]);
+                        l2[c0 / 2 + i] = f2_add(l2[c0 / 2 + i], x[i]);
+                        if constexpr (E4M3) x[i] = f2_mul(x[i], pf2);
+                    }
+                    if (partial && E4M3) {
+#pragma unroll
+                        for (int i = 0; i < C::CW / 2; ++i) x[i] = valid ? x[i] : 0ull;
+                    }
+                    if (E4M3 && !draft) {
+#pragma unroll
+                        for (int g = 0; g < C::CW / 16; ++g) {
+                            uint32_t t1[4], t2[4], t3[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t h[2], a1[2], a2[2], a3[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    float lo, hi;
+                                    f2_unpack(x[8 * g + 2 * k + e], lo, hi);
+                                    h[e] = pack_f16x2(lo, hi);
+                                    a1[e] = h[e] & 0xFF00FF00u;
+                                    h[e] = sub_f16x2(h[e], a1[e]);
+                                    a2[e] = h[e] & 0xFF00FF00u;
+                                    a3[e] = sub_f16x2(h[e], a2[e]) + 0x00800080u;  // rounded, not cut
+                                }
+                                t1[k] = __byte_perm(a1[0], a1[1], 0x7531);
+                                t2[k] = __byte_perm(a2[0], a2[1], 0x7531);
+                                t3[k] = __byte_perm(a3[0], a3[1], 0x7531);
+                            }
+                            uint8_t* dst = pb + (c0 / 16 + g) * 2048 + tid * 16;
+                            *reinterpret_cast<uint4*>(dst) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                            *reinterpret_cast<uint4*>(dst + C::PTERM) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                            *reinterpret_cast<uint4*>(dst + 2 * C::PTERM) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+                        }
                     } else {
-                        // key by key, attended keys only
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
+                        for (int g = 0; g < C::CW / 8; ++g) {
+                            uint32_t w[4];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                for (int q = 0; q < 4; ++q) {
-                                    const int key = key0 + 8 * n + 2 * q + e;
-                                    const float pr = __shfl_sync(0xFFFFFFFFu, sc[n][e], (lane & ~3) | q);
-                                    const float ps = __shfl_sync(0xFFFFFFFFu, sc[n][2 + e], (lane & ~3) | q);
-                                    const bool ua = (ma >> key) & 1ull, ub = (mb >> key) & 1ull;
+                            for (int k = 0; k < 4; ++k) {
+                                float lo, hi;
+                                f2_unpack(x[4 * g + k], lo, hi);
+                                w[k] = pack_bf16x2(lo, hi);
+                            }
+                            *reinterpret_cast<uint4*>(pb + (c0 / 8 + g) * 2048 + tid * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                if (partial && !valid && !draft) {
+                    // what the cache holds past the sequence must not meet P's zeros as a NaN
+                    for (int c = 0; c < C::ROW / 16; ++c) {
+                        uint8_t* v = kt + C::TILE + (E4M3 ? tid * D + 16 * c : (c / 8) * 16384 + tid * 128 + 16 * (c % 8));
+                        *reinterpret_cast<uint4*>(v) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                if (draft && tid < p.tp) {
+                    // a drafted value that is not finite would reach every token through 0 * x: it is taken
+                    // out here and given to the tokens that attend it at the end
+                    uint32_t bad = 0;
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint4* v = reinterpret_cast<uint4*>(kt + dtile + (c / 8) * 8192 + tid * 128 + 16 * (c % 8));
+                        uint32_t w[4] = {v->x, v->y, v->z, v->w};
+                        uint32_t any = 0;
 #pragma unroll
-                                    for (int j = 0; j < D / 8; ++j) {
-                                        const uint32_t x = *reinterpret_cast<const uint32_t*>(
-                                            dk_s + dtile + (j / 8) * dsub + at128(key, j % 8) + 4 * q4);
-                                        const float lo = __uint_as_float(x << 16), hi = __uint_as_float(x & 0xFFFF0000u);
-                                        if (ua) {
-                                            st.o[j][0] = fmaf(pr, lo, st.o[j][0]);
-                                            st.o[j][1] = fmaf(pr, hi, st.o[j][1]);
-                                        }
-                                        if (ub) {
-                                            st.o[j][2] = fmaf(ps, lo, st.o[j][2]);
-                                            st.o[j][3] = fmaf(ps, hi, st.o[j][3]);
-                                        }
-                                    }
+                        for (int k = 0; k < 4; ++k) {
+                            if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u, any = 1;
+                            if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0x0000FFFFu, any = 1;
+                        }
+                        if (!valid) {
+                            *v = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (any) {
+                            *v = make_uint4(w[0], w[1], w[2], w[3]);
+                            bad = 1;
+                        }
+                    }
+                    if (bad) atomicOr(&dflag[tid >> 5], 1u << (tid & 31));
+                }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&pfull[it & 1]);
+                    mbar_arrive(&empty[s]);
+                }
+                ++it;
+                advance();
+            }
+            if (!ok) break;
+
+            // ---- the piece's end: sums over the keys, then O^T (lane = dim) to its rows
+            const bool any_tile = !fresh;
+            for (int c0 = 0; c0 < R; c0 += C::CW) {
+                float v[C::CW];
+#pragma unroll
+                for (int i = 0; i < C::CW / 2; ++i) {
+                    // constant register indices: pick the chunk by selects the compiler folds
+                    uint64_t x = 0ull;
+#pragma unroll
+                    for (int cc = 0; cc < R / C::CW; ++cc)
+                        if (cc * C::CW == c0) x = l2[cc * (C::CW / 2) + i];
+                    f2_unpack(x, v[2 * i], v[2 * i + 1]);
+                }
+                // lane j ends with the sum of column j: halves are exchanged, the kept half is added
+                int n = C::CW;
+                if constexpr (C::CW == 32) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const bool up = lane & 16;
+                        const float give = up ? v[i] : v[i + 16], keep = up ? v[i + 16] : v[i];
+                        v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 16);
+                }
+#pragma unroll
+                for (int o = 8; o >= 1; o >>= 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (i >= o) break;
+                        const bool up = lane & o;
+                        const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+                        v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                    }
+                }
+                if (lane < n) w_s[warp * R + c0 + lane] = v[0];
+            }
+            softmax_sync();
+            const bool whole = unit == 0 && u1 == units;
+            // partial slots: 2c for a piece that goes on with a row tile, 2c + 1 for one that begins it
+            float* part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (unit == 0 ? 1 : 0)) * R * (D + 2);
+            if (tid < R) {
+                const float l = (w_s[tid] + w_s[R + tid]) + (w_s[2 * R + tid] + w_s[3 * R + tid]);
+                const float m = any_tile ? m_s[tid] : -INFINITY;
+                al_s[tid] = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                if (whole) {
+                    if (p.lse != nullptr && tid < nrows)
+                        p.lse[out0 + row_base + tid] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                } else {
+                    part[R * D + 2 * tid] = l == 0.f ? -INFINITY : m;
+                    part[R * D + 2 * tid + 1] = l;
+                }
+            }
+            softmax_sync();
+            if (any_tile) {
+                const int j = it - 1;
+                ok = mbar_wait(&pvdone[j % C::NP], (j / C::NP) & 1, p.status, kTreeDetail | 0x0Cu);
+                tc_fence_after();
+            }
+            const float uf = E4M3 ? pow2i(min(127, max(-126, u))) : 1.f;
+            const uint64_t odd = dflag[0] | (static_cast<uint64_t>(dflag[1]) << 32);
+            const int kvh = p.per_qhead ? hs / p.g : hs;
+            for (int c0 = 0; c0 < R; c0 += C::CW) {
+                if (c0 >= nrows) break;
+                uint32_t v[C::CW];
+                if (any_tile) {
+                    tmem_ldn<C::CW>(tm_o + lanes + c0, v);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C::CW; ++i) v[i] = 0u;
+                }
+                if (tid < D) {
+#pragma unroll
+                    for (int i = 0; i < C::CW; ++i) {
+                        const int r = c0 + i;
+                        if (r < nrows) {
+                            float x = __uint_as_float(v[i]) * (uf * al_s[r]);
+                            if (odd != 0) {
+                                for (uint64_t left = odd & mask_s[r]; left != 0; left &= left - 1) {
+                                    const int jd = __ffsll(static_cast<long long>(left)) - 1;
+                                    const float y = __bfloat162float(
+                                        p.DV[((static_cast<int64_t>(b) * p.Hkv + kvh) * p.T + jd) * D + tid]);
+                                    if (!isfinite(y)) x += y;
                                 }
                             }
+                            if (whole)
+                                p.O[(out0 + row_base + r) * D + tid] = __float2bfloat16_rn(x);
+                            else
+                                part[r * D + tid] = x;
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&dempty);
-                if constexpr (E4M3) to_paired_columns<D>(st);
             }
+            tc_fence_before();
+            if (softmax_any(!ok)) ok = false;  // row parameters are free for the next piece
+            pos += u1 - unit;
+            unit = 0;
+            ++tile;
         }
-
-        // e4m3: the rows of Q as fp16 at a power-of-two scale, dims in the order of the byte tiles
-        float fa = p.scale_log2, fb = p.scale_log2;
-        if constexpr (E4M3) {
-            float ta = 0.f, tb = 0.f;
-            uint2 xa[D / 16], xb[D / 16];
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                xa[k] = ra < rows ? __ldg(reinterpret_cast<const uint2*>(qa + 16 * k) + q4) : make_uint2(0u, 0u);
-                xb[k] = rb < rows ? __ldg(reinterpret_cast<const uint2*>(qb + 16 * k) + q4) : make_uint2(0u, 0u);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t wa = i == 0 ? xa[k].x : xa[k].y, wb = i == 0 ? xb[k].x : xb[k].y;
-                    ta = fmaxf(ta, fmaxf(fabsf(__uint_as_float(wa << 16)), fabsf(__uint_as_float(wa & 0xFFFF0000u))));
-                    tb = fmaxf(tb, fmaxf(fabsf(__uint_as_float(wb << 16)), fabsf(__uint_as_float(wb & 0xFFFF0000u))));
-                }
-            }
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                ta = fmaxf(ta, __shfl_xor_sync(0xFFFFFFFFu, ta, o));
-                tb = fmaxf(tb, __shfl_xor_sync(0xFFFFFFFFu, tb, o));
-            }
-            // exponent field of the factor that brings the maximum to [2^14, 2^15)
-            const int ea = min(253, 268 - static_cast<int>(__float_as_uint(ta) >> 23));
-            const int eb = min(253, 268 - static_cast<int>(__float_as_uint(tb) >> 23));
-            const float ga = __uint_as_float(static_cast<uint32_t>(ea) << 23);
-            const float gb = __uint_as_float(static_cast<uint32_t>(eb) << 23);
-            fa *= __uint_as_float(static_cast<uint32_t>(254 - ea) << 23);
-            fb *= __uint_as_float(static_cast<uint32_t>(254 - eb) << 23);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                qf[k][0] = pack_f16x2(__uint_as_float(xa[k].x << 16) * ga, __uint_as_float(xa[k].x & 0xFFFF0000u) * ga);
-                qf[k][1] = pack_f16x2(__uint_as_float(xb[k].x << 16) * gb, __uint_as_float(xb[k].x & 0xFFFF0000u) * gb);
-                qf[k][2] = pack_f16x2(__uint_as_float(xa[k].y << 16) * ga, __uint_as_float(xa[k].y & 0xFFFF0000u) * ga);
-                qf[k][3] = pack_f16x2(__uint_as_float(xb[k].y << 16) * gb, __uint_as_float(xb[k].y & 0xFFFF0000u) * gb);
-            }
-        }
-
-        while (ok) {
-            ok = mbar_wait(&full[s], par, p.status, kTreeDetail | 0x07u);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            const int lim = meta[s];
-            if (lim == 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
-                advance();
-                break;
-            }
-            uint8_t* kt = ring + s * C::STAGE;
-            uint8_t* es = exps + s * 128;
-            const uint32_t kb = smem_u32(kt), vb = kb + C::TILE;
-            if (lim < 64) {
-                // rows past the sequence hold whatever the cache held: V's must not reach the product as
-                // NaN (0 * NaN), exponents must not set the unit. Warps that share rows write the same 0s.
-                for (int i = 0; i < NCH; ++i) {
-                    const int key0 = 16 * (kg + i * KS);
-                    for (int e = lane; e < 16 * (C::ROW / 16); e += 32) {
-                        const int key = key0 + e / (C::ROW / 16), c = e % (C::ROW / 16);
-                        if (key >= lim) {
-                            const uint32_t o = E4M3 ? at_e4m3<D>(key, c) : (c / 8) * 8192 + at128(key, c % 8);
-                            *reinterpret_cast<uint4*>(kt + C::TILE + o) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                    if (E4M3 && lane < 16 && key0 + lane >= lim) es[key0 + lane] = es[64 + key0 + lane] = 0;
-                }
-                __syncwarp();
-            }
-            float sc[2 * NCH][4];
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int key0 = 16 * (kg + i * KS);
-                if constexpr (E4M3) {
-                    scores_e4m3<D>(qf, kb, key0, sc[2 * i], sc[2 * i + 1]);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint32_t two = *reinterpret_cast<const uint16_t*>(es + key0 + 8 * n + 2 * q4);
-                        const float f0 = __uint_as_float((two & 0xFFu) << 23), f1 = __uint_as_float((two >> 8) << 23);
-                        sc[2 * i + n][0] *= f0 * fa;
-                        sc[2 * i + n][1] *= f1 * fa;
-                        sc[2 * i + n][2] *= f0 * fb;
-                        sc[2 * i + n][3] *= f1 * fb;
-                    }
-                } else {
-                    scores_bf16<D>(qf, kb, 8192, key0, sc[2 * i], sc[2 * i + 1]);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[2 * i + n][e] *= p.scale_log2;
-                    }
-                }
-                if (lim < 64) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const int key = key0 + 8 * n + 2 * q4;
-                        if (key >= lim) sc[2 * i + n][0] = sc[2 * i + n][2] = -INFINITY;
-                        if (key + 1 >= lim) sc[2 * i + n][1] = sc[2 * i + n][3] = -INFINITY;
-                    }
-                }
-            }
-            if constexpr (E4M3) {
-                // the unit exponent: the largest V exponent of this warp's keys so far, less 7
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < NCH; ++i) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(es + 64 + 16 * (kg + i * KS));
-                    top = __vmaxu4(top, __vmaxu4(__vmaxu4(x.x, x.y), __vmaxu4(x.z, x.w)));
-                }
-                top = __vmaxu4(top, top >> 16);
-                top = max(top & 0xFFu, (top >> 8) & 0xFFu);
-                const int u = max(kTreeUMin, min(static_cast<int>(top), 254) - 127 - 7);
-                if (!st.unit_set || u > st.u) {
-                    const float f = pow2i(max(-126, st.u - u));
-                    scale_rows<D>(st, f, f);
-                    st.u = u;
-                    st.unit_set = true;
-                }
-            }
-            softmax_step<D, 2 * NCH>(st, sc);
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int key0 = 16 * (kg + i * KS);
-                uint32_t pa[4];
-                if constexpr (E4M3) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint32_t two = *reinterpret_cast<const uint16_t*>(es + 64 + key0 + 8 * n + 2 * q4);
-                        const int e0 = static_cast<int>(two & 0xFFu), e1 = static_cast<int>(two >> 8);
-                        // a row of exponent 255 keeps its infinity: it is NaN for every token
-                        const float f0 = __uint_as_float(static_cast<uint32_t>(e0 == 255 ? 255 : max(e0 - st.u, 0)) << 23);
-                        const float f1 = __uint_as_float(static_cast<uint32_t>(e1 == 255 ? 255 : max(e1 - st.u, 0)) << 23);
-                        pa[2 * n] = pack_f16x2(sc[2 * i + n][0] * f0, sc[2 * i + n][1] * f1);
-                        pa[2 * n + 1] = pack_f16x2(sc[2 * i + n][2] * f0, sc[2 * i + n][3] * f1);
-                    }
-                    pv_e4m3<D>(st, pa, vb, key0);
-                } else {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        pa[2 * n] = pack_bf16x2(sc[2 * i + n][0], sc[2 * i + n][1]);
-                        pa[2 * n + 1] = pack_bf16x2(sc[2 * i + n][2], sc[2 * i + n][3]);
-                    }
-                    pv_bf16<D>(st, pa, vb, 8192, key0);
-                }
-            }
-            if (lim < 64) fence_proxy_async_smem();  // this warp's zeros, before the next copy into the stage
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
-            advance();
-        }
-
-        // ---- the piece's end
-        if constexpr (E4M3) {
-            if (st.unit_set) {
-                const float f = pow2i(st.u);
-                scale_rows<D>(st, f, f);
-            }
-        }
-        float l0 = st.l0, l1 = st.l1;
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
-            l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
-        }
-        const bool whole = unit == 0 && u1 == units;
-        // partial slots: 2c for a piece that goes on with a row tile, 2c + 1 for one that begins it
-        float* part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (unit == 0 ? 1 : 0)) * RM * (D + 2);
-        // dims of accumulator element (j, e) of a row
-        auto dim_of = [&](int j, int e) {
-            return E4M3 ? 16 * (j / 2) + 4 * q4 + 2 * e + (j & 1) : 8 * j + 2 * q4 + e;
-        };
-        if constexpr (KS == 1) {
-            const int la = 16 * mg + r, lb = la + 8;
-            if (whole) {
-                const float ia = l0 > 0.f || l0 != l0 ? 1.f / l0 : 0.f, ib = l1 > 0.f || l1 != l1 ? 1.f / l1 : 0.f;
-#pragma unroll
-                for (int g = 0; g < D / 16; ++g) {
-                    if constexpr (E4M3) {
-                        const int d = 16 * g + 4 * q4;
-                        if (ra < rows)
-                            *reinterpret_cast<uint2*>(p.O + (out0 + ra) * D + d) =
-                                make_uint2(pack_bf16x2(st.o[2 * g][0] * ia, st.o[2 * g + 1][0] * ia),
-                                           pack_bf16x2(st.o[2 * g][1] * ia, st.o[2 * g + 1][1] * ia));
-                        if (rb < rows)
-                            *reinterpret_cast<uint2*>(p.O + (out0 + rb) * D + d) =
-                                make_uint2(pack_bf16x2(st.o[2 * g][2] * ib, st.o[2 * g + 1][2] * ib),
-                                           pack_bf16x2(st.o[2 * g][3] * ib, st.o[2 * g + 1][3] * ib));
-                    } else {
-#pragma unroll
-                        for (int j = 2 * g; j < 2 * g + 2; ++j) {
-                            const int d = 8 * j + 2 * q4;
-                            if (ra < rows)
-                                *reinterpret_cast<uint32_t*>(p.O + (out0 + ra) * D + d) =
-                                    pack_bf16x2(st.o[j][0] * ia, st.o[j][1] * ia);
-                            if (rb < rows)
-                                *reinterpret_cast<uint32_t*>(p.O + (out0 + rb) * D + d) =
-                                    pack_bf16x2(st.o[j][2] * ib, st.o[j][3] * ib);
-                        }
-                    }
-                }
-                if (p.lse != nullptr && q4 == 0) {
-                    if (ra < rows)
-                        p.lse[out0 + ra] = l0 == 0.f ? -INFINITY : (st.m0 + log2f(l0)) * 0.69314718055994531f;
-                    if (rb < rows)
-                        p.lse[out0 + rb] = l1 == 0.f ? -INFINITY : (st.m1 + log2f(l1)) * 0.69314718055994531f;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        part[la * D + dim_of(j, e)] = st.o[j][e];
-                        part[lb * D + dim_of(j, e)] = st.o[j][2 + e];
-                    }
-                }
-                if (q4 == 0) {
-                    part[RM * D + 2 * la] = st.m0;
-                    part[RM * D + 2 * la + 1] = l0;
-                    part[RM * D + 2 * lb] = st.m1;
-                    part[RM * D + 2 * lb + 1] = l1;
-                }
-            }
-        } else {
-            // the KS warps of a row group meet in shared memory, 16 dims at a time
-            float* cml = comb + KS * RM * 16;   // [kg][row][m, l]
-            const int la = 16 * mg + r, lb = la + 8;
-            if (q4 == 0) {
-                cml[(kg * RM + la) * 2] = st.m0;
-                cml[(kg * RM + la) * 2 + 1] = l0;
-                cml[(kg * RM + lb) * 2] = st.m1;
-                cml[(kg * RM + lb) * 2 + 1] = l1;
-            }
-            for (int g = 0; g < D / 16; ++g) {
-#pragma unroll
-                for (int gg = 0; gg < D / 16; ++gg) {
-                    if (gg != g) continue;  // constant accumulator indices
-#pragma unroll
-                    for (int j = 2 * gg; j < 2 * gg + 2; ++j) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            comb[(kg * RM + la) * 16 + dim_of(j, e) - 16 * gg] = st.o[j][e];
-                            comb[(kg * RM + lb) * 16 + dim_of(j, e) - 16 * gg] = st.o[j][2 + e];
-                        }
-                    }
-                }
-                named_bar_sync(1, W * 32);
-                for (int e = tid; e < RM * 16; e += W * 32) {
-                    const int row = e / 16, d = 16 * g + e % 16;
-                    float M = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) M = fmaxf(M, cml[(k * RM + row) * 2]);
-                    float v = 0.f, l = 0.f;
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        const float mk = cml[(k * RM + row) * 2], lk = cml[(k * RM + row) * 2 + 1];
-                        // a warp without a key for the row has l = 0 (and o = 0) unless it met a NaN
-                        const float w = mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : fast_exp2(mk - M);
-                        v += w * comb[(k * RM + row) * 16 + e % 16];
-                        l += w * lk;
-                    }
-                    const int rg = row_base + row;
-                    if (whole) {
-                        if (rg < rows) {
-                            p.O[(out0 + rg) * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
-                            if (d == 0 && p.lse != nullptr)
-                                p.lse[out0 + rg] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
-                        }
-                    } else {
-                        part[row * D + d] = v;
-                        if (d == 0) {
-                            part[RM * D + 2 * row] = M;
-                            part[RM * D + 2 * row + 1] = l;
-                        }
-                    }
-                }
-                named_bar_sync(1, W * 32);
-            }
-        }
-        pos += u1 - unit;
-        unit = 0;
-        ++tile;
     }
     __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tm, C::COLS);
+    }
 }
 
 // Joins the pieces of the row tiles that crossed runs, in run order: m = max m_i, weights
@@ -969,35 +1039,33 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
 
 // ---------------------------------------------------------------- host side
 
-// Row tile of a group of `rows` rows: 16 rows (the chunks of a unit split over four warps), 32 (over
-// two), 64 or 128; past 64 rows the size that pads least, the larger one on a tie.
+// Rows of one row tile for a selection row of `rows` rows: the smallest of 16, 32, 64, 96 and 128 that
+// holds them, or, past 128 rows, of 96 and 128 the one that pads less (128 on a tie).
 int tree_row_tile(int rows) {
-    if (rows <= 16) return 16;
-    if (rows <= 32) return 32;
-    if (rows <= 64) return 64;
-    const int by64 = (rows + 63) / 64 * 64, by128 = (rows + 127) / 128 * 128;
-    return by128 <= by64 ? 128 : 64;
+    for (int r : {16, 32, 64, 96, 128})
+        if (rows <= r) return r;
+    return (rows + 95) / 96 * 96 < (rows + 127) / 128 * 128 ? 96 : 128;
 }
 
-template <int D, bool E4M3, int MG, int KS>
+// CTAs on one SM: two where the shared memory of both fits.
+int tree_ctas_per_sm(int rm, bool e4m3) { return e4m3 && rm <= 64 ? 2 : 1; }
+
+template <int D, bool E4M3, int R>
 static bool launch_tree(TreeParams p, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dk,
                         const CUtensorMap& dv, cudaStream_t st, int32_t* launches) {
-    using C = TreeCfg<D, E4M3>;
-    // two CTAs share an SM's shared memory (one of 128 rows has it alone)
-    const size_t budget = (MG == 8 ? 224 : 112) * 1024;
-    int nstg = 8;
-    while (nstg > 2 && tree_smem<D, E4M3, MG, KS>(nstg, p.tp) > budget) --nstg;
-    p.nstg = nstg;
-    const size_t smem = tree_smem<D, E4M3, MG, KS>(nstg, p.tp);
+    using C = TreeCfg<D, E4M3, R>;
+    constexpr int budget = (C::CTAS == 2 ? 112 : 225) * 1024;
+    static_assert(C::FIXED + 2 * (C::STAGE + C::EXPS) <= budget, "two stages must fit");
+    p.nstg = (budget - C::FIXED) / (C::STAGE + C::EXPS);
+    if (p.nstg > kTreeMaxStages) p.nstg = kTreeMaxStages;
+    const int smem = C::FIXED + p.nstg * (C::STAGE + C::EXPS);
     static std::atomic<uint64_t> configured{0};
-    if (!configure_smem_once(reinterpret_cast<const void*>(attn_tree_kernel<D, E4M3, MG, KS>), 227 * 1024 - 1024,
-                             configured))
-        return false;
-    attn_tree_kernel<D, E4M3, MG, KS><<<p.runs, (MG * KS + 1) * 32, smem, st>>>(k, v, dk, dv, p);
+    if (!configure_smem_once(reinterpret_cast<const void*>(attn_tree_kernel<D, E4M3, R>), smem, configured)) return false;
+    attn_tree_kernel<D, E4M3, R><<<p.runs, 192, smem, st>>>(k, v, dk, dv, p);
     if (cudaGetLastError() != cudaSuccess) return false;
     ++*launches;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.rows_per_seq, 4 * MG);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.rows_per_seq, R / 4);
     cfg.blockDim = dim3(128);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1005,7 +1073,7 @@ static bool launch_tree(TreeParams p, const CUtensorMap& k, const CUtensorMap& v
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<D>, p, 16 * MG) != cudaSuccess) return false;
+    if (cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<D>, p, R) != cudaSuccess) return false;
     ++*launches;
     return true;
 }
@@ -1014,18 +1082,19 @@ template <int D, bool E4M3>
 static bool launch_tree_rows(const TreeParams& p, int rm, const CUtensorMap& k, const CUtensorMap& v,
                              const CUtensorMap& dk, const CUtensorMap& dv, cudaStream_t st, int32_t* launches) {
     switch (rm) {
-        case 16: return launch_tree<D, E4M3, 1, 4>(p, k, v, dk, dv, st, launches);
-        case 32: return launch_tree<D, E4M3, 2, 2>(p, k, v, dk, dv, st, launches);
-        case 64: return launch_tree<D, E4M3, 4, 1>(p, k, v, dk, dv, st, launches);
-        default: return launch_tree<D, E4M3, 8, 1>(p, k, v, dk, dv, st, launches);
+        case 16: return launch_tree<D, E4M3, 16>(p, k, v, dk, dv, st, launches);
+        case 32: return launch_tree<D, E4M3, 32>(p, k, v, dk, dv, st, launches);
+        case 64: return launch_tree<D, E4M3, 64>(p, k, v, dk, dv, st, launches);
+        case 96: return launch_tree<D, E4M3, 96>(p, k, v, dk, dv, st, launches);
+        default: return launch_tree<D, E4M3, 128>(p, k, v, dk, dv, st, launches);
     }
 }
 
-bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* V, const void* Kc,
-                      const void* Vc, cudaStream_t st, int32_t* launches) {
+bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
+                      cudaStream_t st, int32_t* launches) {
     const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv * p.cap, drows = static_cast<int64_t>(p.B) * p.Hkv * p.T;
     CUtensorMap k, v, dk, dv;
-    if (!make_tmap_2d(&dk, K, drows, D, p.tp) || !make_tmap_2d(&dv, V, drows, D, p.tp)) return false;
+    if (!make_tmap_2d(&dk, K, drows, D, p.tp) || !make_tmap_2d(&dv, p.DV, drows, D, p.tp)) return false;
     if (e4m3) {
         if (!make_tmap_2d_u8(&k, Kc, rows, D, 64) || !make_tmap_2d_u8(&v, Vc, rows, D, 64)) return false;
         return D == 64 ? launch_tree_rows<64, true>(p, rm, k, v, dk, dv, st, launches)

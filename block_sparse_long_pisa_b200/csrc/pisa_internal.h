@@ -256,14 +256,15 @@ struct CachePyramidParams {
     int32_t loff[PISA_MAX_LEVELS];
 };
 
-// Runs (CTAs) of the tree attention: two on each of 148 SMs, one for row tiles of 128 rows. Fixed, so
-// that the workspace and the order of every sum do not depend on the device.
-constexpr int kTreeRuns = 296;
+// Runs (CTAs) of the tree attention per CTA that an SM takes: one for each of 148 SMs. Fixed, so that
+// the workspace and the order of every sum do not depend on the device.
+constexpr int kTreeRuns = 148;
 // Units of 64 keys that a run has on average at least (small jobs take fewer runs).
 constexpr int kTreeMinUnits = 2;
 
 struct TreeParams {
     const __nv_bfloat16* Q;         // [B, Hq, T, D]
+    const __nv_bfloat16* DV;        // drafted values [B, Hkv, T, D]
     const uint64_t* mask;           // [B, T]
     const uint8_t *k_exp, *v_exp;   // e4m3: [B, Hkv, cap]
     const int32_t* len;             // [B]
@@ -310,8 +311,9 @@ bool launch_cache_read(const CacheParams& p, int D, bool e4m3, cudaStream_t st);
 bool launch_cache_pyramid(const CachePyramidParams& p, cudaStream_t st, int32_t* launches);
 // Rows of one row tile for a selection row that `rows` = heads x drafted tokens share.
 int tree_row_tile(int rows);
-bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* V, const void* Kc,
-                      const void* Vc, cudaStream_t st, int32_t* launches);
+int tree_ctas_per_sm(int rm, bool e4m3);
+bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
+                      cudaStream_t st, int32_t* launches);
 bool launch_attn_backward(const BwdParams& p, int32_t batch, cudaStream_t st, int32_t* launches);
 // Backward column pass (dK, dV) on the tensor cores (head dim 64 or 128, 64- or 128-key blocks:
 // every shape the library accepts); false when the shape is another one or on a launch error.

@@ -128,7 +128,7 @@ static pisa_status tree_plan(const pisa_tree_shape* s, TreePlan* t) {
     t->rm = tree_row_tile(t->rows);
     t->mt = (t->rows + t->rm - 1) / t->rm;
     if (static_cast<int64_t>(s->batch) * t->hsel * t->mt >= (int64_t(1) << 31)) return PISA_ERR_UNSUPPORTED;
-    t->runs = t->rm == 128 ? kTreeRuns / 2 : kTreeRuns;
+    t->runs = kTreeRuns * tree_ctas_per_sm(t->rm, s->format == PISA_CACHE_E4M3);
     t->total = kStatusBytes + size_t(2) * t->runs * t->rm * (s->head_dim + 2) * sizeof(float);
     return PISA_OK;
 }
@@ -319,6 +319,7 @@ pisa_status pisa_tree_attention(const pisa_tree_shape* shape, const void* Q, con
     if (injected_launch_failure()) return PISA_ERR_CUDA;
     TreeParams p{};
     p.Q = static_cast<const __nv_bfloat16*>(Q);
+    p.DV = static_cast<const __nv_bfloat16*>(V);
     p.mask = mask;
     p.k_exp = k_exp;
     p.v_exp = v_exp;
@@ -348,7 +349,7 @@ pisa_status pisa_tree_attention(const pisa_tree_shape* shape, const void* Q, con
     p.tp = (shape->drafts + 15) / 16 * 16;
     const float scale = shape->scale > 0.f ? shape->scale : 1.0f / sqrtf(static_cast<float>(shape->head_dim));
     p.scale_log2 = scale * 1.4426950408889634f;
-    return launch_attn_tree(p, shape->head_dim, shape->format == PISA_CACHE_E4M3, t.rm, K, V, Kc, Vc,
+    return launch_attn_tree(p, shape->head_dim, shape->format == PISA_CACHE_E4M3, t.rm, K, Kc, Vc,
                             reinterpret_cast<cudaStream_t>(stream), &g_launches)
                ? PISA_OK
                : PISA_ERR_CUDA;
