@@ -1,7 +1,7 @@
 // Attention of a tree of drafted tokens over a K/V cache (one drafted token is plain decode).
 //
 //   rows   the T drafted tokens of the gh query heads that share a selection row: gh * T rows, cut
-//          into row tiles of R (16 .. 128)
+//          into row tiles of R (16 .. 96)
 //   keys   the cache in units of 64 keys (selected blocks and tail, or all of it, up to the
 //          sequence's length), two units to a tile of 128, and last the drafted tokens themselves,
 //          masked by their ancestor bits
@@ -185,34 +185,37 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t two) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
-// Barrier over the softmax threads; true if `x` holds in any of them.
-__device__ __forceinline__ bool softmax_any(bool x) {
+// Barrier over a softmax warpgroup's threads; true if `x` holds in any of them.
+__device__ __forceinline__ bool softmax_any(uint32_t bar, bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(x))
+        : "r"(static_cast<uint32_t>(x)), "r"(bar)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { named_bar_sync(1, 128); }
+__device__ __forceinline__ void softmax_sync(uint32_t bar) { named_bar_sync(bar, 128); }
 
+// N consecutive TMEM columns (16, 32 or 48) of the warp's lanes; the loads are in flight until
+// tmem_wait_ld.
 template <int N>
-__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
-    if constexpr (N == 32)
+__device__ __forceinline__ void tmem_cols(uint32_t taddr, uint32_t (&v)[N]) {
+    if constexpr (N >= 32) {
+        uint32_t r[32];
         tmem_ld32(taddr, r);
-    else
-        tmem_ld16(taddr, r);
-}
-template <int N>
-__device__ __forceinline__ void tmem_stn(uint32_t taddr, const uint32_t (&r)[N]) {
-    if constexpr (N == 32)
-        tmem_st32(taddr, r);
-    else
-        tmem_st16(taddr, r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = r[i];
+    }
+    if constexpr (N % 32 == 16) {
+        uint32_t r[16];
+        tmem_ld16(taddr + (N - 16), r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[N - 16 + i] = r[i];
+    }
 }
 
 // ---------------------------------------------------------------- layout
@@ -223,21 +226,29 @@ struct TreeCfg {
     static constexpr int TILE = 128 * ROW;               // K (or V) of one tile
     static constexpr int STAGE = 2 * TILE;
     static constexpr int EXPS = E4M3 ? 256 : 0;          // a stage's exponent bytes of K and of V
-    static constexpr int QB = R * 2 * D;                 // Q: bf16, or the e4m3 and the e5m2 terms
+    static constexpr int QB = R * 2 * D;                 // Q: bf16, or its two e4m3 terms
     static constexpr int PTERM = R * 128;                // one 8-bit term of P
-    static constexpr int PB = E4M3 ? 3 * PTERM : 2 * PTERM;
-    // P buffers: one where a second would cost a CTA per SM (e4m3, 64 rows) or a stage (bf16, many rows)
-    static constexpr int NP = (E4M3 ? R == 64 : R > 64) ? 1 : 2;
-    static constexpr int CW = R < 32 ? 16 : 32;          // TMEM columns taken at a time
-    static constexpr int COLS = 3 * R <= 64 ? 64 : 3 * R <= 128 ? 128 : 3 * R <= 256 ? 256 : 512;
+    static constexpr int PB = E4M3 ? 3 * PTERM : 2 * PTERM;  // P: three 8-bit terms, or bf16
+    // terms side by side along N (one pass over K and V for all of them) while TMEM holds them
+    static constexpr bool STACK = E4M3 && R <= 64;
+    static constexpr int SW = STACK ? 2 * R : R;         // TMEM columns of one S
+    static constexpr int OT = STACK ? 3 : 1;             // accumulators of O
+    static constexpr int COLS = 2 * SW + OT * R <= 64 ? 64 : 2 * SW + OT * R <= 128 ? 128
+                                                         : 2 * SW + OT * R <= 256  ? 256
+                                                                                   : 512;
+    static constexpr int NWG = R >= 64 ? 2 : 1;          // softmax warpgroups: each takes RW columns
+    static constexpr int RW = R / NWG;
+    static constexpr int CW = 16;                        // columns of O taken at a time
+    static constexpr int NP = !E4M3 && R > 64 ? 1 : 2;   // P buffers: one where a second would cost a stage
     static constexpr float LAZY = E4M3 ? 4.f : 8.f;      // log2 units a score may exceed the kept maximum by
     // dynamic shared memory without the ring: Q, P, masks, row parameters (8 floats a row)
     static constexpr int FIXED = 1024 + QB + NP * PB + R * 8 + R * 32;
-    static constexpr int CTAS = E4M3 && R <= 64 ? 2 : 1;  // CTAs an SM's shared memory takes
+    static constexpr int CTAS = E4M3 && R <= 32 ? 2 : 1;  // CTAs an SM's shared memory and TMEM take
+    static constexpr int THREADS = 128 * NWG + 64;
 };
 
 template <int D, bool E4M3, int R>
-__global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
+__global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3, R>::CTAS)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
                      const TreeParams p) {
@@ -255,7 +266,7 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
     uint8_t* exps = reinterpret_cast<uint8_t*>(w_s + 4 * R);  // [stage][K 128, V 128]
     __shared__ __align__(8) uint64_t full[kTreeMaxStages], empty[kTreeMaxStages], sfull[2], pfull[2], pvdone[2], qfull, done;
     __shared__ int4 meta[kTreeMaxStages];  // kind, keys that count in the two halves
-    __shared__ uint32_t tmem_slot, dflag[2], wexp[4];
+    __shared__ uint32_t tmem_slot, dflag[2], wexp[8];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const TreeJob job = tree_job(p);
@@ -268,23 +279,23 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
     if (tid == 0) {
         for (int i = 0; i < p.nstg; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 5);  // the softmax warps, and P.V (or the MMA lane itself)
+            mbar_init(&empty[i], 4 * C::NWG + 1);  // the softmax warps, and P.V (or the MMA lane itself)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 4);
+            mbar_init(&pfull[i], 4 * C::NWG);
             mbar_init(&pvdone[i], 1);
         }
-        mbar_init(&qfull, 4);
+        mbar_init(&qfull, 4 * C::NWG);
         mbar_init(&done, 1);
         fence_barrier_init();
     }
-    if (warp == 5) tmem_alloc(&tmem_slot, C::COLS);
+    if (warp == 4 * C::NWG + 1) tmem_alloc(&tmem_slot, C::COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = tmem_slot;
-    const uint32_t tm_o = tm + 2 * R;
+    const uint32_t tm_o = tm + 2 * C::SW;
 
     int s = 0;            // ring stage, and the parity of its current use
     uint32_t par = 0;
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
     };
     const int dtile = D * 128;  // drafted K (or V) in a stage: [D / 64][64 rows][128 B]
 
-    if (warp == 4) {
+    if (warp == 4 * C::NWG) {
         // ------------------------------------------------ producer
         int used = 0;   // ring slots handed out
         if (lane == 0) {
@@ -410,52 +421,57 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
                 if (!mbar_wait(&full[s], par, p.status, kTreeDetail | 0x02u)) break;
             }
         }
-    } else if (warp == 5) {
+    } else if (warp == 4 * C::NWG + 1) {
         // ------------------------------------------------ MMA
         if (lane == 0) {
             const uint32_t q0 = smem_u32(q_s), p0 = smem_u32(p_s);
-            int it = 0;               // tiles so far
+            int it = 0, pt = 0;       // slots so far (S buffers), and tiles among them (P buffers)
             uint32_t qpar = 0;
             bool issued = false;
             int pend_s = -1, pend_kind = 0;
             bool fresh = true;        // the next P.V begins O
-            auto pv = [&]() {         // P.V of the tile before (number it - 1 when called)
-                const int j = it - 1;
-                ok = mbar_wait(&pfull[j & 1], (j >> 1) & 1, p.status, kTreeDetail | 0x03u);
+            auto pv = [&]() {         // P.V of the tile before
+                ok = mbar_wait(&pfull[pt & 1], (pt >> 1) & 1, p.status, kTreeDetail | 0x03u);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t pb = p0 + (j % C::NP) * C::PB;
+                const uint32_t pb = p0 + (pt % C::NP) * C::PB;
                 const uint32_t vt = smem_u32(ring + pend_s * C::STAGE);
+                const uint64_t b = tree_desc(pb, 128, 2048, 0);
                 if (pend_kind == kTileDraft || !E4M3) {
                     const bool draft = pend_kind == kTileDraft;
                     const uint32_t sub = draft ? 8192 : 16384;
                     const uint64_t a = tree_desc(vt + (draft ? dtile : C::TILE), D == 128 ? sub : 0, 1024, 2);
-                    const uint64_t b = tree_desc(pb, 128, 2048, 0);
                     const int steps = draft ? p.tp / 16 : 8;
                     for (int k = 0; k < steps; ++k)
                         mma_bf16_ss(tm_o, desc_at(a, k * 2048), desc_at(b, k * 256), idesc_bf16_f32(128, R, 1, 1),
                                     !fresh || k > 0 ? 1u : 0u);
                 } else {
                     const uint64_t a = D == 128 ? tree_desc(vt + C::TILE, 0, 1024, 2) : tree_desc(vt + C::TILE, 0, 512, 4);
-                    const uint64_t b = tree_desc(pb, 128, 2048, 0);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
+                        if constexpr (C::STACK) {
+                            mma_f8_ss(tm_o, desc_at(a, k * 32 * D), desc_at(b, k * 512), idesc_f8(3 * R, 1, 1, 1),
+                                      !fresh || k > 0 ? 1u : 0u);
+                        } else {
 #pragma unroll
-                        for (int t = 0; t < 3; ++t)
-                            mma_f8_ss(tm_o, desc_at(a, k * 32 * D), desc_at(b, t * C::PTERM + k * 512), idesc_f8(R, 1, 1, 1),
-                                      !fresh || k > 0 || t > 0 ? 1u : 0u);
+                            for (int t = 0; t < 3; ++t)
+                                mma_f8_ss(tm_o, desc_at(a, k * 32 * D), desc_at(b, t * C::PTERM + k * 512),
+                                          idesc_f8(R, 1, 1, 1), !fresh || k > 0 || t > 0 ? 1u : 0u);
+                        }
                     }
                 }
                 fresh = false;
                 mma_commit(&empty[pend_s]);
-                mma_commit(&pvdone[j % C::NP]);
+                mma_commit(&pvdone[pt % C::NP]);
+                ++pt;
             };
             while (pos < end && ok) {
                 const int b = static_cast<int>(tile / p.rows_per_seq);
                 const int units = tree_units(p, tree_len(p, b));
                 const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
+                ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x04u);
+                qpar ^= 1u;
                 fresh = true;
-                bool first = true;
                 while (ok) {
                     ok = mbar_wait(&full[s], par, p.status, kTreeDetail | 0x05u);
                     if (!ok) break;
@@ -464,20 +480,30 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
                         if (pend_s >= 0) pv();
                         pend_s = -1;
                         if (ok) {
+                            // with every product of the piece complete, the softmax may read O
+                            issued = true;
+                            mma_commit(&sfull[it & 1]);
                             mbar_arrive(&empty[s]);
+                            ++it;
                             advance();
                         }
                         break;
                     }
-                    if (first || (E4M3 && kind == kTileDraft)) {  // for the drafted tokens Q comes again, as bf16
+                    if (E4M3 && kind == kTileDraft) {
+                        // Q comes again, as bf16: a slot without scores tells the softmax so
+                        if (pend_s >= 0) pv();
+                        pend_s = -1;
+                        if (!ok) break;
+                        issued = true;
+                        mma_commit(&sfull[it & 1]);
+                        ++it;
                         ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x06u);
                         qpar ^= 1u;
-                        first = false;
                         if (!ok) break;
                     }
                     tc_fence_after();
                     const uint32_t kt = smem_u32(ring + s * C::STAGE);
-                    const uint32_t d = tm + (it & 1) * R;
+                    const uint32_t d = tm + (it & 1) * C::SW;
                     issued = true;
                     if (kind == kTileDraft || !E4M3) {
                         const uint32_t sub = kind == kTileDraft ? 8192 : 16384;
@@ -491,8 +517,12 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
                         const uint64_t bq = D == 128 ? tree_desc(q0, 16, 1024, 2) : tree_desc(q0, 16, 512, 4);
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k) {
-                            mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, k * 32), idesc_f8(R, 0, 0, 0), k > 0 ? 1u : 0u);
-                            mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, R * D + k * 32), idesc_f8(R, 1, 0, 0), 1u);
+                            if constexpr (C::STACK) {
+                                mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, k * 32), idesc_f8(2 * R, 0, 0, 0), k > 0 ? 1u : 0u);
+                            } else {
+                                mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, k * 32), idesc_f8(R, 0, 0, 0), k > 0 ? 1u : 0u);
+                                mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, R * D + k * 32), idesc_f8(R, 1, 0, 0), 1u);
+                            }
                         }
                     }
                     mma_commit(&sfull[it & 1]);
@@ -514,32 +544,38 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
         __syncwarp();
     } else {
         // ------------------------------------------------ softmax: thread = key of the tile = TMEM lane
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;  // TMEM lane base of the warp
+        // With two warpgroups each takes RW of the rows, on its own: its maxima, its unit, its columns of
+        // O, its barrier.
+        const int wg = warp / 4, key = tid & 127, cb = wg * C::RW;
+        const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;  // TMEM lane base of the warp
+        const uint32_t bar = 1 + wg;
         const int rows = p.gh * p.T;
-        int it = 0;
+        float *rf = rf_s + cb, *nms = nm_s + cb, *ms = m_s + cb, *als = al_s + cb, *ws = w_s + 4 * cb;
+        const uint64_t* masks = mask_s + cb;
+        int it = 0, pt = 0;
         while (pos < end && ok) {
             const int b = static_cast<int>(tile / p.rows_per_seq);
             const int rem = static_cast<int>(tile % p.rows_per_seq);
-            const int hs = rem / p.mt, row_base = (rem % p.mt) * R;
+            const int hs = rem / p.mt, row_base = (rem % p.mt) * R + cb;
             const int units = tree_units(p, tree_len(p, b));
             const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
             const int64_t out0 = (static_cast<int64_t>(b) * p.Hq + hs * p.gh) * p.T;  // first row of the group
-            const int nrows = min(R, rows - row_base);
+            const int nrows = max(0, min(C::RW, rows - row_base));
             const uint4* qg = reinterpret_cast<const uint4*>(p.Q + (out0 + row_base) * D);
 
             // Q as bf16: [D / 64][R rows][128 B], 128-byte swizzle
             auto q_bf16 = [&]() {
-                for (int e = tid; e < R * (D / 8); e += 128) {
-                    const int r = e / (D / 8), c = e % (D / 8);
-                    const uint4 x = r < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
+                for (int e = key; e < C::RW * (D / 8); e += 128) {
+                    const int r = e / (D / 8) + cb, c = e % (D / 8);
+                    const uint4 x = r - cb < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4*>(q_s + (c / 8) * (R * 128) + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = x;
                 }
             };
-            // Q as e4m3 + e5m2 terms [R rows][D B], swizzled by the row's size; D/8 lanes hold a row
+            // Q as two 8-bit terms [R rows][D B], swizzled by the row's size; D/8 lanes hold a row
             auto q_terms = [&]() {
-                for (int e = tid; e < R * (D / 8); e += 128) {  // R * D / 8 is a multiple of 128
-                    const int r = e / (D / 8), c = e % (D / 8);
-                    const uint4 x = r < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
+                for (int e = key; e < C::RW * (D / 8); e += 128) {  // RW * D / 8 is a multiple of 128
+                    const int r = e / (D / 8) + cb, c = e % (D / 8);
+                    const uint4 x = r - cb < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                     float v[8], top = 0.f;
 #pragma unroll
@@ -559,8 +595,9 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
                         const float a = v[2 * k] * sc, bb = v[2 * k + 1] * sc;
                         hi[k] = cvt_e4m3x2(a, bb);
                         const float2 h = e4m3x2_f32(hi[k]);
-                        // an infinity saturates: its remainder keeps it (inf - 448) as a NaN
-                        lo[k] = cvt_e5m2x2(a - h.x, bb - h.y);
+                        // the remainder; stacked terms have sums of their own, so it can be kept 16 times larger
+                        lo[k] = C::STACK ? cvt_e4m3x2((a - h.x) * 16.f, (bb - h.y) * 16.f) : cvt_e5m2x2(a - h.x, bb - h.y);
+                        // an infinity saturates the first term: the second makes the score a NaN
                         if (isinf(a)) lo[k] = (lo[k] & 0xFF00u) | 0x7Fu;
                         if (isinf(bb)) lo[k] = (lo[k] & 0x00FFu) | 0x7F00u;
                     }
@@ -581,145 +618,159 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
                 q_terms();
             else
                 q_bf16();
-            if (u1 == units && tid < R) {  // this piece ends with the drafted tokens
-                const int rg = row_base + tid;
+            if (u1 == units && key < C::RW) {  // this piece ends with the drafted tokens
+                const int rg = row_base + key;
                 const uint64_t live = p.T == 64 ? ~0ull : (1ull << p.T) - 1ull;
-                mask_s[tid] = rg < rows ? __ldg(p.mask + static_cast<int64_t>(b) * p.T + rg % p.T) & live : 0ull;
+                mask_s[cb + key] = rg < rows ? __ldg(p.mask + static_cast<int64_t>(b) * p.T + rg % p.T) & live : 0ull;
             }
-            if (tid < 2) dflag[tid] = 0;
-            softmax_sync();  // row factors and masks
+            // Q of this piece may be announced: the MMA lane saw the piece before to its end (the slot that
+            // ends a piece comes through it)
+            q_ready();
+            if (key < C::RW) nms[key] = 0.f;
+            softmax_sync(bar);  // row factors and masks
 
-            uint64_t l2[R / 2];  // this key's share of the rows' sums
+            uint64_t l2[C::RW / 2];  // this key's share of the rows' sums
 #pragma unroll
-            for (int i = 0; i < R / 2; ++i) l2[i] = 0ull;
-            bool fresh = true;
+            for (int i = 0; i < C::RW / 2; ++i) l2[i] = 0ull;
+            bool fresh = true, cached = false;  // no tile yet; a tile of the cache so far
             int u = 0, uexp = 0;   // unit exponent of O, and the V exponent it was set by (e4m3)
 
             while (true) {
                 // Every slot is one barrier, and a second one when the first says so: a warp whose wait ran
                 // out takes both, so that all warps leave together whatever the others saw in the slot.
-                if (ok) ok = mbar_wait(&full[s], par, p.status, kTreeDetail | 0x08u);
+                if (ok) ok = mbar_wait(&sfull[it & 1], (it >> 1) & 1, p.status, kTreeDetail | 0x08u);
                 ok = __all_sync(0xFFFFFFFFu, ok);
+                tc_fence_after();
                 const int4 mt = ok ? meta[s] : make_int4(kTileEnd, 0, 0, 0);
+                if (E4M3 && mt.x == kTileDraft) {
+                    // this slot only says that the drafted tokens come: every S so far is formed, Q's buffer
+                    // is free for the bf16 rows; the next slot has the scores
+                    q_bf16();
+                    q_ready();
+                    ++it;
+                    ok = mbar_wait(&sfull[it & 1], (it >> 1) & 1, p.status, kTreeDetail | 0x09u);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    tc_fence_after();
+                }
                 if (mt.x == kTileEnd) {
-                    if (softmax_any(!ok) && softmax_any(!ok)) ok = false;
+                    if (softmax_any(bar, !ok) && softmax_any(bar, !ok)) ok = false;
                     if (ok) {
                         if (lane == 0) mbar_arrive(&empty[s]);
+                        ++it;
                         advance();
                     }
                     break;
                 }
                 const bool draft = mt.x == kTileDraft;
-                // Q is handed over at the first tile, not before it is known that there is one: a piece may
-                // hold no tile at all, and its successor's Q must not be announced before the MMA lane
-                // has seen this one's
-                if (E4M3 && draft) {
-                    q_bf16();  // every S of this piece so far is formed: Q's buffer is free
-                    q_ready();
-                } else if (fresh) {
-                    q_ready();
-                }
                 uint8_t* kt = ring + s * C::STAGE;
-                const bool valid = draft ? tid < p.T : (tid & 63) < (tid < 64 ? mt.y : mt.z);
+                const bool valid = draft ? key < p.T : (key & 63) < (key < 64 ? mt.y : mt.z);
                 const bool partial = draft || mt.y < 64 || mt.z < 64;
                 float kf = p.scale_log2;
                 int ev = 0;
                 if (E4M3 && !draft && valid) {
-                    kf *= __uint_as_float(static_cast<uint32_t>(exps[s * 256 + tid]) << 23);
-                    ev = exps[s * 256 + 128 + tid];
+                    kf *= __uint_as_float(static_cast<uint32_t>(exps[s * 256 + key]) << 23);
+                    ev = exps[s * 256 + 128 + key];
                 }
-                ok = __all_sync(0xFFFFFFFFu, ok) && mbar_wait(&sfull[it & 1], (it >> 1) & 1, p.status, kTreeDetail | 0x09u);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                tc_fence_after();
-                const uint32_t ts = tm + lanes + (it & 1) * R;
-                const uint64_t kf2 = f2_pack(kf, kf);
-
-                // scores against the kept maximum, log2 units, of columns [c0, c0 + CW)
-                auto load_scores = [&](int c0, uint64_t (&x)[C::CW / 2], bool against) {
-                    uint32_t v[C::CW];
-                    tmem_ldn<C::CW>(ts + c0, v);
-                    tmem_wait_ld();
+                if (draft && wg == 0 && key < 2) dflag[key] = 0;
+                // scores against the kept maximum, log2 units: x = acc * kf (* the row's factor) - m
+                const uint32_t ts = tm + lanes + (it & 1) * C::SW + cb;
+                uint64_t x[C::RW / 2];
+                {
+                    uint32_t v[C::RW];
+                    tmem_cols<C::RW>(ts, v);
+                    if (C::STACK && !draft) {  // the second term of Q is 16 times too large
+                        uint32_t w[C::RW];
+                        tmem_cols<C::RW>(ts + R, w);
+                        tmem_wait_ld();
+                        const uint64_t f = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
-                    for (int i = 0; i < C::CW / 4; ++i) {
-                        const float4 nm = *reinterpret_cast<const float4*>(nm_s + c0 + 4 * i);
-                        uint64_t a = f2_mul(f2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), kf2);
-                        uint64_t c = f2_mul(f2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), kf2);
-                        uint64_t ma = f2_pack(nm.x, nm.y), mc = f2_pack(nm.z, nm.w);
-                        if (!against) ma = mc = 0ull;
-                        if constexpr (E4M3) {
-                            float4 rf = *reinterpret_cast<const float4*>(rf_s + c0 + 4 * i);
-                            if (draft) rf = make_float4(1.f, 1.f, 1.f, 1.f);  // bf16 rows as they are
-                            a = f2_fma(a, f2_pack(rf.x, rf.y), ma);
-                            c = f2_fma(c, f2_pack(rf.z, rf.w), mc);
-                        } else {
-                            a = f2_add(a, ma);
-                            c = f2_add(c, mc);
-                        }
-                        x[2 * i] = a;
-                        x[2 * i + 1] = c;
+                        for (int i = 0; i < C::RW / 2; ++i)
+                            x[i] = f2_fma(f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), f,
+                                          f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
+                    } else {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < C::RW / 2; ++i)
+                            x[i] = f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                     }
+                }
+                const uint64_t kf2 = f2_pack(kf, kf);
+#pragma unroll
+                for (int i = 0; i < C::RW / 4; ++i) {
+                    const float4 nm = *reinterpret_cast<const float4*>(nms + 4 * i);
+                    if constexpr (E4M3) {
+                        float4 f = *reinterpret_cast<const float4*>(rf + 4 * i);
+                        if (draft) f = make_float4(1.f, 1.f, 1.f, 1.f);  // bf16 rows as they are
+                        x[2 * i] = f2_fma(f2_mul(x[2 * i], kf2), f2_pack(f.x, f.y), f2_pack(nm.x, nm.y));
+                        x[2 * i + 1] = f2_fma(f2_mul(x[2 * i + 1], kf2), f2_pack(f.z, f.w), f2_pack(nm.z, nm.w));
+                    } else {
+                        x[2 * i] = f2_fma(x[2 * i], kf2, f2_pack(nm.x, nm.y));
+                        x[2 * i + 1] = f2_fma(x[2 * i + 1], kf2, f2_pack(nm.z, nm.w));
+                    }
+                }
+                if (partial) {
+                    const uint64_t none = f2_pack(-INFINITY, -INFINITY);
                     if (draft) {
 #pragma unroll
-                        for (int i = 0; i < C::CW / 2; ++i) {
+                        for (int i = 0; i < C::RW / 2; ++i) {
                             float lo, hi;
                             f2_unpack(x[i], lo, hi);
-                            lo = valid && (mask_s[c0 + 2 * i] >> tid) & 1ull ? lo : -INFINITY;
-                            hi = valid && (mask_s[c0 + 2 * i + 1] >> tid) & 1ull ? hi : -INFINITY;
+                            lo = valid && (masks[2 * i] >> key) & 1ull ? lo : -INFINITY;
+                            hi = valid && (masks[2 * i + 1] >> key) & 1ull ? hi : -INFINITY;
                             x[i] = f2_pack(lo, hi);
                         }
-                    }
-                };
-                float top = -INFINITY;
-                if (!fresh) {
-                    for (int c0 = 0; c0 < R; c0 += C::CW) {
-                        uint64_t x[C::CW / 2];
-                        load_scores(c0, x, true);
+                    } else {
 #pragma unroll
-                        for (int i = 0; i < C::CW / 2; ++i) {
-                            float lo, hi;
-                            f2_unpack(x[i], lo, hi);
-                            top = fmax3(top, lo, hi);
-                        }
+                        for (int i = 0; i < C::RW / 2; ++i) x[i] = valid ? x[i] : none;
                     }
                 }
-                const bool over = valid && (top > C::LAZY || (E4M3 && !draft && ev > uexp));
-                if (softmax_any(!ok || fresh || over)) {
-                    if (softmax_any(!ok)) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < C::RW / 2; ++i) {
+                    float lo, hi;
+                    f2_unpack(x[i], lo, hi);
+                    top = fmax3(top, lo, hi);
+                }
+                const bool over = top > C::LAZY || (E4M3 && ev > uexp);
+                if (softmax_any(bar, !ok || fresh || over)) {
+                    if (softmax_any(bar, !ok)) {
                         ok = false;
                         break;
                     }
-                    // the rows' maxima over this tile, and the largest V exponent
-                    for (int c0 = 0; c0 < R; c0 += C::CW) {
-                        uint64_t x[C::CW / 2];
-                        load_scores(c0, x, false);
-                        float mine = -INFINITY;
+                    // the rows' maxima over this tile (less the kept ones), and the largest V exponent
+                    float mine = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < C::CW / 2; ++i) {
-                            float lo, hi;
-                            f2_unpack(x[i], lo, hi);
-                            lo = warp_max(valid ? lo : -INFINITY);
-                            hi = warp_max(valid ? hi : -INFINITY);
-                            if (lane == 2 * i) mine = lo;
-                            if (lane == 2 * i + 1) mine = hi;
+                    for (int i = 0; i < C::RW / 2; ++i) {
+                        float lo, hi;
+                        f2_unpack(x[i], lo, hi);
+                        lo = warp_max(lo);
+                        hi = warp_max(hi);
+                        if (lane == (2 * i) % 32) mine = lo;
+                        if (lane == (2 * i) % 32 + 1) mine = hi;
+                        if (2 * i + 2 == C::RW || (2 * i + 2) % 32 == 0) {
+                            const int c = (2 * i) / 32 * 32 + lane;
+                            if (c < C::RW) ws[(warp % 4) * C::RW + c] = mine;
                         }
-                        if (lane < C::CW) w_s[warp * R + c0 + lane] = mine;
                     }
                     if constexpr (E4M3) {
                         const uint32_t we = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(ev));
                         if (lane == 0) wexp[warp] = we;
                     }
-                    softmax_sync();
-                    if (tid < R) {
-                        const float M = fmaxf(fmaxf(w_s[tid], w_s[R + tid]), fmaxf(w_s[2 * R + tid], w_s[3 * R + tid]));
-                        const float old = fresh ? -INFINITY : m_s[tid];
-                        const float now = fmaxf(old, M);
-                        al_s[tid] = now == old ? 1.f : fast_exp2(old - now);
-                        m_s[tid] = now;
-                        nm_s[tid] = now == -INFINITY ? 0.f : -now;
+                    softmax_sync(bar);
+                    if (key < C::RW) {
+                        const float M = fmaxf(fmaxf(ws[key], ws[C::RW + key]), fmaxf(ws[2 * C::RW + key], ws[3 * C::RW + key]));
+                        const float was = -nms[key];  // the reference that x was taken against
+                        const float old = fresh ? -INFINITY : ms[key];
+                        const float now = fmaxf(old, was + M);
+                        als[key] = now == old ? 1.f : fast_exp2(old - now);
+                        ms[key] = now;
+                        nms[key] = now == -INFINITY ? 0.f : -now;
+                        ws[key] = was + nms[key];     // what brings x to the new reference
                     }
                     float uf = 1.f;
                     if (E4M3 && !draft) {
-                        const int e = static_cast<int>(min(254u, max(max(wexp[0], wexp[1]), max(wexp[2], wexp[3]))));
+                        const uint32_t* we = wexp + 4 * wg;
+                        const int e = static_cast<int>(min(254u, max(max(we[0], we[1]), max(we[2], we[3]))));
                         if (fresh || e > uexp) {
                             uexp = e;
                             const int un = max(kTreeUMin, e - 127 + static_cast<int>(C::LAZY) - 15);
@@ -727,118 +778,115 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
                             u = un;
                         }
                     }
-                    softmax_sync();
+                    softmax_sync(bar);
+#pragma unroll
+                    for (int i = 0; i < C::RW / 4; ++i) {
+                        const float4 d = *reinterpret_cast<const float4*>(ws + 4 * i);
+                        x[2 * i] = f2_add(x[2 * i], f2_pack(d.x, d.y));
+                        x[2 * i + 1] = f2_add(x[2 * i + 1], f2_pack(d.z, d.w));
+                    }
                     if (!fresh) {
-                        const int j = it - 1;
+                        const int j = pt - 1;
                         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[j % C::NP], (j / C::NP) & 1, p.status,
                                                                kTreeDetail | 0x0Au));
                         tc_fence_after();
-                        for (int c0 = 0; c0 < R; c0 += C::CW) {
-                            uint32_t v[C::CW];
-                            tmem_ldn<C::CW>(tm_o + lanes + c0, v);
-                            tmem_wait_ld();
+#pragma unroll 1
+                        for (int t = 0; t < (cached ? C::OT : 1); ++t) {
+#pragma unroll 1
+                            for (int c0 = 0; c0 < C::RW; c0 += C::CW) {
+                                const uint32_t to = tm_o + lanes + t * R + cb + c0;
+                                uint32_t v[C::CW];
+                                tmem_ld16(to, v);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < C::CW; ++i)
-                                v[i] = __float_as_uint(__uint_as_float(v[i]) * (al_s[c0 + i] * uf));
-                            tmem_stn<C::CW>(tm_o + lanes + c0, v);
+                                for (int i = 0; i < C::CW; ++i)
+                                    v[i] = __float_as_uint(__uint_as_float(v[i]) * (als[c0 + i] * uf));
+                                tmem_st16(to, v);
+                            }
                         }
                         tmem_wait_st();
 #pragma unroll
-                        for (int i = 0; i < R / 2; ++i) l2[i] = f2_mul(l2[i], f2_pack(al_s[2 * i], al_s[2 * i + 1]));
+                        for (int i = 0; i < C::RW / 4; ++i) {
+                            const float4 a = *reinterpret_cast<const float4*>(als + 4 * i);
+                            l2[2 * i] = f2_mul(l2[2 * i], f2_pack(a.x, a.y));
+                            l2[2 * i + 1] = f2_mul(l2[2 * i + 1], f2_pack(a.z, a.w));
+                        }
                     }
                     fresh = false;
                 }
-                // P's buffer: the P.V that read it last is complete
-                if (it >= C::NP && ok) {
-                    const int j = it - C::NP;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[j % C::NP], (j / C::NP) & 1, p.status,
-                                                           kTreeDetail | 0x0Bu));
+                // P's buffer: this tile's S is complete, and with it every product issued before it, the P.V
+                // of two tiles before among them; a single buffer waits for the last one
+                if (C::NP == 1 && pt > 0 && ok)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[0], (pt - 1) & 1, p.status, kTreeDetail | 0x0Bu));
+                uint8_t* pb = p_s + (pt % C::NP) * C::PB;
+#pragma unroll
+                for (int i = 0; i < C::RW / 2; ++i) {
+                    float lo, hi;
+                    f2_unpack(x[i], lo, hi);
+                    x[i] = f2_pack(fast_exp2(lo), fast_exp2(hi));
+                    l2[i] = f2_add(l2[i], x[i]);
                 }
-                uint8_t* pb = p_s + (it % C::NP) * C::PB;
-                // a row of exponent 255 stands for NaN (its bytes are zero)
-                const float pf = !E4M3 ? 1.f
-                                 : draft ? pow2i(min(127, max(-126, -u)))
-                                         : __uint_as_float(ev == 255 ? 0x7FFFFFFFu : static_cast<uint32_t>(max(ev - u, 0)) << 23);
-                const uint64_t pf2 = f2_pack(pf, pf);
+                if constexpr (E4M3) {
+                    // a row of exponent 255 stands for NaN (its bytes are zero); a row that does not count has
+                    // P = 0 and a factor of 2^-126
+                    const float pf = draft ? pow2i(min(127, max(-126, -u)))
+                                           : __uint_as_float(ev == 255 ? 0x7FFFFFFFu : static_cast<uint32_t>(max(ev - u, 1)) << 23);
+                    const uint64_t pf2 = f2_pack(pf, pf);
 #pragma unroll
-                for (int c0 = 0; c0 < R; c0 += C::CW) {
-                    uint64_t x[C::CW / 2];
-                    load_scores(c0, x, true);
-                    float pr[C::CW];
+                    for (int i = 0; i < C::RW / 2; ++i) x[i] = f2_mul(x[i], pf2);
+                }
+                if (E4M3 && !draft) {
 #pragma unroll
-                    for (int i = 0; i < C::CW / 2; ++i) {
-                        float lo, hi;
-                        f2_unpack(x[i], lo, hi);
-                        pr[2 * i] = fast_exp2(lo);
-                        pr[2 * i + 1] = fast_exp2(hi);
-                    }
-                    if (partial) {
+                    for (int g = 0; g < C::RW / 16; ++g) {
+                        uint32_t t1[4], t2[4], t3[4];
 #pragma unroll
-                        for (int i = 0; i < C::CW; ++i) pr[i] = valid ? pr[i] : 0.f;
-                    }
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t h[2], a1[2], a2[2], a3[2];
 #pragma unroll
-                    for (int i = 0; i < C::CW / 2; ++i) {
-                        x[i] = f2_pack(pr[2 * i], pr[2 * i + 1]);
-                        l2[c0 / 2 + i] = f2_add(l2[c0 / 2 + i], x[i]);
-                        if constexpr (E4M3) x[i] = f2_mul(x[i], pf2);
-                    }
-                    if (partial && E4M3) {
-#pragma unroll
-                        for (int i = 0; i < C::CW / 2; ++i) x[i] = valid ? x[i] : 0ull;
-                    }
-                    if (E4M3 && !draft) {
-#pragma unroll
-                        for (int g = 0; g < C::CW / 16; ++g) {
-                            uint32_t t1[4], t2[4], t3[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t h[2], a1[2], a2[2], a3[2];
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    float lo, hi;
-                                    f2_unpack(x[8 * g + 2 * k + e], lo, hi);
-                                    h[e] = pack_f16x2(lo, hi);
-                                    a1[e] = h[e] & 0xFF00FF00u;
-                                    h[e] = sub_f16x2(h[e], a1[e]);
-                                    a2[e] = h[e] & 0xFF00FF00u;
-                                    a3[e] = sub_f16x2(h[e], a2[e]) + 0x00800080u;  // rounded, not cut
-                                }
-                                t1[k] = __byte_perm(a1[0], a1[1], 0x7531);
-                                t2[k] = __byte_perm(a2[0], a2[1], 0x7531);
-                                t3[k] = __byte_perm(a3[0], a3[1], 0x7531);
-                            }
-                            uint8_t* dst = pb + (c0 / 16 + g) * 2048 + tid * 16;
-                            *reinterpret_cast<uint4*>(dst) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-                            *reinterpret_cast<uint4*>(dst + C::PTERM) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-                            *reinterpret_cast<uint4*>(dst + 2 * C::PTERM) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int g = 0; g < C::CW / 8; ++g) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                            for (int e = 0; e < 2; ++e) {
                                 float lo, hi;
-                                f2_unpack(x[4 * g + k], lo, hi);
-                                w[k] = pack_bf16x2(lo, hi);
+                                f2_unpack(x[8 * g + 2 * k + e], lo, hi);
+                                h[e] = pack_f16x2(lo, hi);
+                                a1[e] = h[e] & 0xFF00FF00u;
+                                h[e] = sub_f16x2(h[e], a1[e]);
+                                a2[e] = h[e] & 0xFF00FF00u;
+                                a3[e] = sub_f16x2(h[e], a2[e]) + 0x00800080u;  // rounded, not cut
                             }
-                            *reinterpret_cast<uint4*>(pb + (c0 / 8 + g) * 2048 + tid * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                            t1[k] = __byte_perm(a1[0], a1[1], 0x7531);
+                            t2[k] = __byte_perm(a2[0], a2[1], 0x7531);
+                            t3[k] = __byte_perm(a3[0], a3[1], 0x7531);
                         }
+                        uint8_t* dst = pb + (cb / 16 + g) * 2048 + key * 16;
+                        *reinterpret_cast<uint4*>(dst) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                        *reinterpret_cast<uint4*>(dst + C::PTERM) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                        *reinterpret_cast<uint4*>(dst + 2 * C::PTERM) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int g = 0; g < C::RW / 8; ++g) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float lo, hi;
+                            f2_unpack(x[4 * g + k], lo, hi);
+                            w[k] = pack_bf16x2(lo, hi);
+                        }
+                        *reinterpret_cast<uint4*>(pb + (cb / 8 + g) * 2048 + key * 16) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                if (partial && !valid && !draft) {
+                if (wg == 0 && partial && !valid && !draft) {
                     // what the cache holds past the sequence must not meet P's zeros as a NaN
                     for (int c = 0; c < C::ROW / 16; ++c) {
-                        uint8_t* v = kt + C::TILE + (E4M3 ? tid * D + 16 * c : (c / 8) * 16384 + tid * 128 + 16 * (c % 8));
+                        uint8_t* v = kt + C::TILE + (E4M3 ? key * D + 16 * c : (c / 8) * 16384 + key * 128 + 16 * (c % 8));
                         *reinterpret_cast<uint4*>(v) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
-                if (draft && tid < p.tp) {
+                if (wg == 0 && draft && key < p.tp) {
                     // a drafted value that is not finite would reach every token through 0 * x: it is taken
                     // out here and given to the tokens that attend it at the end
                     uint32_t bad = 0;
                     for (int c = 0; c < D / 8; ++c) {
-                        uint4* v = reinterpret_cast<uint4*>(kt + dtile + (c / 8) * 8192 + tid * 128 + 16 * (c % 8));
+                        uint4* v = reinterpret_cast<uint4*>(kt + dtile + (c / 8) * 8192 + key * 128 + 16 * (c % 8));
                         uint32_t w[4] = {v->x, v->y, v->z, v->w};
                         uint32_t any = 0;
 #pragma unroll
@@ -853,46 +901,33 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
                             bad = 1;
                         }
                     }
-                    if (bad) atomicOr(&dflag[tid >> 5], 1u << (tid & 31));
+                    if (bad) atomicOr(&dflag[key >> 5], 1u << (key & 31));
                 }
+                cached = cached || !draft;
                 tc_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&pfull[it & 1]);
+                    mbar_arrive(&pfull[pt & 1]);
                     mbar_arrive(&empty[s]);
                 }
                 ++it;
+                ++pt;
                 advance();
             }
             if (!ok) break;
 
-            // ---- the piece's end: sums over the keys, then O^T (lane = dim) to its rows
+            // ---- the piece's end (every product is complete): sums over the keys, then O^T (lane = dim) to
+            // its rows
             const bool any_tile = !fresh;
-            for (int c0 = 0; c0 < R; c0 += C::CW) {
-                float v[C::CW];
 #pragma unroll
-                for (int i = 0; i < C::CW / 2; ++i) {
-                    // constant register indices: pick the chunk by selects the compiler folds
-                    uint64_t x = 0ull;
+            for (int c0 = 0; c0 < C::RW; c0 += 16) {
+                float v[16];
 #pragma unroll
-                    for (int cc = 0; cc < R / C::CW; ++cc)
-                        if (cc * C::CW == c0) x = l2[cc * (C::CW / 2) + i];
-                    f2_unpack(x, v[2 * i], v[2 * i + 1]);
-                }
-                // lane j ends with the sum of column j: halves are exchanged, the kept half is added
-                int n = C::CW;
-                if constexpr (C::CW == 32) {
+                for (int i = 0; i < 8; ++i) f2_unpack(l2[c0 / 2 + i], v[2 * i], v[2 * i + 1]);
+                // lanes j and j + 16 end with the sum of column j: halves are exchanged, the kept half is added
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const bool up = lane & 16;
-                        const float give = up ? v[i] : v[i + 16], keep = up ? v[i + 16] : v[i];
-                        v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 16);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 16);
-                }
+                for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 16);
 #pragma unroll
                 for (int o = 8; o >= 1; o >>= 1) {
 #pragma unroll
@@ -903,74 +938,81 @@ __global__ void __launch_bounds__(192, TreeCfg<D, E4M3, R>::CTAS)
                         v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
                     }
                 }
-                if (lane < n) w_s[warp * R + c0 + lane] = v[0];
+                if (lane < 16) ws[(warp % 4) * C::RW + c0 + lane] = v[0];
             }
-            softmax_sync();
+            softmax_sync(bar);
             const bool whole = unit == 0 && u1 == units;
             // partial slots: 2c for a piece that goes on with a row tile, 2c + 1 for one that begins it
             float* part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (unit == 0 ? 1 : 0)) * R * (D + 2);
-            if (tid < R) {
-                const float l = (w_s[tid] + w_s[R + tid]) + (w_s[2 * R + tid] + w_s[3 * R + tid]);
-                const float m = any_tile ? m_s[tid] : -INFINITY;
-                al_s[tid] = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            if (key < C::RW) {
+                const float l = (ws[key] + ws[C::RW + key]) + (ws[2 * C::RW + key] + ws[3 * C::RW + key]);
+                const float m = any_tile ? ms[key] : -INFINITY;
+                als[key] = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                 if (whole) {
-                    if (p.lse != nullptr && tid < nrows)
-                        p.lse[out0 + row_base + tid] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                    if (p.lse != nullptr && key < nrows)
+                        p.lse[out0 + row_base + key] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                 } else {
-                    part[R * D + 2 * tid] = l == 0.f ? -INFINITY : m;
-                    part[R * D + 2 * tid + 1] = l;
+                    part[R * D + 2 * (cb + key)] = l == 0.f ? -INFINITY : m;
+                    part[R * D + 2 * (cb + key) + 1] = l;
                 }
             }
-            softmax_sync();
-            if (any_tile) {
-                const int j = it - 1;
-                ok = mbar_wait(&pvdone[j % C::NP], (j / C::NP) & 1, p.status, kTreeDetail | 0x0Cu);
-                tc_fence_after();
-            }
+            softmax_sync(bar);
             const float uf = E4M3 ? pow2i(min(127, max(-126, u))) : 1.f;
-            const uint64_t odd = dflag[0] | (static_cast<uint64_t>(dflag[1]) << 32);
+            const uint64_t odd = u1 == units ? dflag[0] | (static_cast<uint64_t>(dflag[1]) << 32) : 0ull;
             const int kvh = p.per_qhead ? hs / p.g : hs;
-            for (int c0 = 0; c0 < R; c0 += C::CW) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < C::RW; c0 += C::CW) {
                 if (c0 >= nrows) break;
                 uint32_t v[C::CW];
                 if (any_tile) {
-                    tmem_ldn<C::CW>(tm_o + lanes + c0, v);
+                    tmem_ld16(tm_o + lanes + cb + c0, v);
                     tmem_wait_ld();
+                    if (C::OT > 1 && cached) {
+#pragma unroll
+                        for (int t = 1; t < C::OT; ++t) {
+                            uint32_t w[C::CW];
+                            tmem_ld16(tm_o + lanes + t * R + cb + c0, w);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < C::CW; ++i)
+                                v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < C::CW; ++i) v[i] = 0u;
                 }
-                if (tid < D) {
+                if (key < D) {
 #pragma unroll
                     for (int i = 0; i < C::CW; ++i) {
                         const int r = c0 + i;
                         if (r < nrows) {
-                            float x = __uint_as_float(v[i]) * (uf * al_s[r]);
+                            float o = __uint_as_float(v[i]) * (uf * als[r]);
                             if (odd != 0) {
-                                for (uint64_t left = odd & mask_s[r]; left != 0; left &= left - 1) {
+                                for (uint64_t left = odd & masks[r]; left != 0; left &= left - 1) {
                                     const int jd = __ffsll(static_cast<long long>(left)) - 1;
                                     const float y = __bfloat162float(
-                                        p.DV[((static_cast<int64_t>(b) * p.Hkv + kvh) * p.T + jd) * D + tid]);
-                                    if (!isfinite(y)) x += y;
+                                        p.DV[((static_cast<int64_t>(b) * p.Hkv + kvh) * p.T + jd) * D + key]);
+                                    if (!isfinite(y)) o += y;
                                 }
                             }
                             if (whole)
-                                p.O[(out0 + row_base + r) * D + tid] = __float2bfloat16_rn(x);
+                                p.O[(out0 + row_base + r) * D + key] = __float2bfloat16_rn(o);
                             else
-                                part[r * D + tid] = x;
+                                part[(cb + r) * D + key] = o;
                         }
                     }
                 }
             }
             tc_fence_before();
-            if (softmax_any(!ok)) ok = false;  // row parameters are free for the next piece
+            softmax_sync(bar);  // row parameters are free for the next piece
             pos += u1 - unit;
             unit = 0;
             ++tile;
         }
     }
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 4 * C::NWG + 1) {
         tc_fence_after();
         tmem_dealloc(tm, C::COLS);
     }
@@ -1039,16 +1081,16 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
 
 // ---------------------------------------------------------------- host side
 
-// Rows of one row tile for a selection row of `rows` rows: the smallest of 16, 32, 64, 96 and 128 that
-// holds them, or, past 128 rows, of 96 and 128 the one that pads less (128 on a tie).
+// Rows of one row tile for a selection row of `rows` rows: the smallest of 16, 32, 64 and 96 that holds
+// them, or, past 96 rows, of 64 and 96 the one that pads less (96 on a tie).
 int tree_row_tile(int rows) {
-    for (int r : {16, 32, 64, 96, 128})
+    for (int r : {16, 32, 64, 96})
         if (rows <= r) return r;
-    return (rows + 95) / 96 * 96 < (rows + 127) / 128 * 128 ? 96 : 128;
+    return (rows + 63) / 64 * 64 < (rows + 95) / 96 * 96 ? 64 : 96;
 }
 
 // CTAs on one SM: two where the shared memory of both fits.
-int tree_ctas_per_sm(int rm, bool e4m3) { return e4m3 && rm <= 64 ? 2 : 1; }
+int tree_ctas_per_sm(int rm, bool e4m3) { return e4m3 && rm <= 32 ? 2 : 1; }
 
 template <int D, bool E4M3, int R>
 static bool launch_tree(TreeParams p, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dk,
@@ -1061,7 +1103,7 @@ static bool launch_tree(TreeParams p, const CUtensorMap& k, const CUtensorMap& v
     const int smem = C::FIXED + p.nstg * (C::STAGE + C::EXPS);
     static std::atomic<uint64_t> configured{0};
     if (!configure_smem_once(reinterpret_cast<const void*>(attn_tree_kernel<D, E4M3, R>), smem, configured)) return false;
-    attn_tree_kernel<D, E4M3, R><<<p.runs, 192, smem, st>>>(k, v, dk, dv, p);
+    attn_tree_kernel<D, E4M3, R><<<p.runs, C::THREADS, smem, st>>>(k, v, dk, dv, p);
     if (cudaGetLastError() != cudaSuccess) return false;
     ++*launches;
     cudaLaunchConfig_t cfg{};
@@ -1085,8 +1127,7 @@ static bool launch_tree_rows(const TreeParams& p, int rm, const CUtensorMap& k, 
         case 16: return launch_tree<D, E4M3, 16>(p, k, v, dk, dv, st, launches);
         case 32: return launch_tree<D, E4M3, 32>(p, k, v, dk, dv, st, launches);
         case 64: return launch_tree<D, E4M3, 64>(p, k, v, dk, dv, st, launches);
-        case 96: return launch_tree<D, E4M3, 96>(p, k, v, dk, dv, st, launches);
-        default: return launch_tree<D, E4M3, 128>(p, k, v, dk, dv, st, launches);
+        default: return launch_tree<D, E4M3, 96>(p, k, v, dk, dv, st, launches);
     }
 }
 
