@@ -53,7 +53,8 @@ namespace pisa {
 
 constexpr uint32_t kTreeDetail = kKernTree << 8;
 constexpr int kTreeUMin = -100;  // smallest unit exponent of O (e4m3)
-constexpr int kTreeMaxStages = 8;
+constexpr int kTreeMaxSlots = 4;  // of the K ring and of the V ring
+constexpr int kTreeMeta = 8;      // entries (tiles and piece ends) whose description is kept
 enum : int { kTileEnd = 0, kTileCache = 1, kTileDraft = 2 };
 
 // ---------------------------------------------------------------- the runs
@@ -198,6 +199,18 @@ __device__ __forceinline__ bool softmax_any(uint32_t bar, bool x) {
         : "memory");
     return r != 0;
 }
+// Whether the barrier's phase of this parity has completed (no wait).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ void softmax_sync(uint32_t bar) { named_bar_sync(bar, 128); }
 
 // N consecutive TMEM columns (16, 32 or 48) of the warp's lanes; the loads are in flight until
@@ -223,9 +236,8 @@ __device__ __forceinline__ void tmem_cols(uint32_t taddr, uint32_t (&v)[N]) {
 template <int D, bool E4M3, int R>
 struct TreeCfg {
     static constexpr int ROW = E4M3 ? D : 2 * D;         // bytes of a cache row
-    static constexpr int TILE = 128 * ROW;               // K (or V) of one tile
-    static constexpr int STAGE = 2 * TILE;
-    static constexpr int EXPS = E4M3 ? 256 : 0;          // a stage's exponent bytes of K and of V
+    static constexpr int TILE = 128 * ROW;               // K (or V) of one tile: one slot of a ring
+    static constexpr int EXPS = E4M3 ? 256 : 0;          // a tile's exponent bytes of K and of V
     static constexpr int QB = R * 2 * D;                 // Q: bf16, or its two e4m3 terms
     static constexpr int PTERM = R * 128;                // one 8-bit term of P
     static constexpr int PB = E4M3 ? 3 * PTERM : 2 * PTERM;  // P: three 8-bit terms, or bf16
@@ -236,13 +248,13 @@ struct TreeCfg {
     static constexpr int COLS = 2 * SW + OT * R <= 64 ? 64 : 2 * SW + OT * R <= 128 ? 128
                                                          : 2 * SW + OT * R <= 256  ? 256
                                                                                    : 512;
-    static constexpr int NWG = R >= 64 ? 2 : 1;          // softmax warpgroups: each takes RW columns
+    static constexpr int NWG = R >= 64 ? R / 32 : 1;     // softmax warpgroups: each takes RW columns
     static constexpr int RW = R / NWG;
     static constexpr int CW = 16;                        // columns of O taken at a time
-    static constexpr int NP = !E4M3 && R > 64 ? 1 : 2;   // P buffers: one where a second would cost a stage
+    static constexpr int NP = 2;                         // P buffers
     static constexpr float LAZY = E4M3 ? 4.f : 8.f;      // log2 units a score may exceed the kept maximum by
-    // dynamic shared memory without the ring: Q, P, masks, row parameters (8 floats a row)
-    static constexpr int FIXED = 1024 + QB + NP * PB + R * 8 + R * 32;
+    // dynamic shared memory without the rings: Q, P, masks, row parameters (8 floats a row), exponents
+    static constexpr int FIXED = 1024 + QB + NP * PB + R * 8 + R * 32 + kTreeMeta * EXPS;
     static constexpr int CTAS = E4M3 && R <= 32 ? 2 : 1;  // CTAs an SM's shared memory and TMEM take
     static constexpr int THREADS = 128 * NWG + 64;
 };
@@ -255,7 +267,8 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
     using C = TreeCfg<D, E4M3, R>;
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* q_s = ring + p.nstg * C::STAGE;
+    uint8_t* vring = ring + p.nk * C::TILE;
+    uint8_t* q_s = vring + p.nv * C::TILE;
     uint8_t* p_s = q_s + C::QB;
     uint64_t* mask_s = reinterpret_cast<uint64_t*>(p_s + C::NP * C::PB);  // [R]
     float* rf_s = reinterpret_cast<float*>(mask_s + R);  // score factor of a row (e4m3: 2^-(Q's exponent))
@@ -263,10 +276,11 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
     float* m_s = nm_s + R;                               // kept maximum, log2 units
     float* al_s = m_s + R;                               // factor of O and l in a rescale; 1/l at the end
     float* w_s = al_s + R;                               // [4 warps][R]
-    uint8_t* exps = reinterpret_cast<uint8_t*>(w_s + 4 * R);  // [stage][K 128, V 128]
-    __shared__ __align__(8) uint64_t full[kTreeMaxStages], empty[kTreeMaxStages], sfull[2], pfull[2], pvdone[2], qfull, done;
-    __shared__ int4 meta[kTreeMaxStages];  // kind, keys that count in the two halves
-    __shared__ uint32_t tmem_slot, dflag[2], wexp[8];
+    uint8_t* exps = reinterpret_cast<uint8_t*>(w_s + 4 * R);  // [entry][K 128, V 128]
+    __shared__ __align__(8) uint64_t kfull[kTreeMaxSlots], kempty[kTreeMaxSlots], vfull[kTreeMaxSlots],
+        vempty[kTreeMaxSlots], sfull[2], pfull[2], pvdone[2], qfull, done;
+    __shared__ int4 meta[kTreeMeta];  // kind, keys that count in the two halves
+    __shared__ uint32_t tmem_slot, dflag[2], wexp[4 * C::NWG];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const TreeJob job = tree_job(p);
@@ -277,9 +291,13 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
     int unit;
     tree_find(p, pos, tile, unit);
     if (tid == 0) {
-        for (int i = 0; i < p.nstg; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 4 * C::NWG + 1);  // the softmax warps, and P.V (or the MMA lane itself)
+        for (int i = 0; i < p.nk; ++i) {
+            mbar_init(&kfull[i], 1);
+            mbar_init(&kempty[i], 1);
+        }
+        for (int i = 0; i < p.nv; ++i) {
+            mbar_init(&vfull[i], 1);
+            mbar_init(&vempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
@@ -297,72 +315,93 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
     const uint32_t tm = tmem_slot;
     const uint32_t tm_o = tm + 2 * C::SW;
 
-    int s = 0;            // ring stage, and the parity of its current use
-    uint32_t par = 0;
     bool ok = true;       // cleared by a wait that ran out: nothing more is waited for
-    auto advance = [&]() {
-        if (++s == p.nstg) {
-            s = 0;
-            par ^= 1u;
+    // A place in a ring: slot, parity of its current use, and uses so far.
+    struct At {
+        int s = 0, n = 0;
+        uint32_t par = 0;
+        __device__ __forceinline__ void next(int slots) {
+            ++n;
+            if (++s == slots) {
+                s = 0;
+                par ^= 1u;
+            }
         }
     };
-    const int dtile = D * 128;  // drafted K (or V) in a stage: [D / 64][64 rows][128 B]
+    At k, v;              // K ring (tiles and piece ends), V ring (tiles)
 
     if (warp == 4 * C::NWG) {
         // ------------------------------------------------ producer
-        int used = 0;   // ring slots handed out
         if (lane == 0) {
             prefetch_tmap(&tmK);
             prefetch_tmap(&tmV);
             prefetch_tmap(&tmDK);
             prefetch_tmap(&tmDV);
         }
-        // one slot: kind, and for a tile the first keys of its halves (second -1: absent)
+        // one entry: a tile's K and then its V, or the end of a piece; of a tile of the cache the first
+        // keys of its halves (second -1: absent)
         auto issue = [&](int kind, int64_t plane, int len, int a0, int a1) {
             if (lane == 0) {
-                ok = used < p.nstg || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x01u);
+                ok = k.n < p.nk || mbar_wait(&kempty[k.s], k.par ^ 1u, p.status, kTreeDetail | 0x01u);
                 if (ok) {
-                    uint8_t* kt = ring + s * C::STAGE;
+                    uint8_t* kt = ring + k.s * C::TILE;
+                    uint64_t* kb = &kfull[k.s];
+                    const int e = k.n % kTreeMeta;
+                    const int halves = a1 >= 0 ? 2 : 1;
+                    const int dbytes = p.tp * 2 * D, dy = static_cast<int>(plane * p.T);
                     if (kind == kTileEnd) {
-                        meta[s] = make_int4(kind, 0, 0, 0);
-                        mbar_arrive(&full[s]);
+                        meta[e] = make_int4(kind, 0, 0, 0);
+                        mbar_arrive(kb);
                     } else if (kind == kTileDraft) {
-                        meta[s] = make_int4(kind, 0, 0, 0);
-                        mbar_arrive_expect_tx(&full[s], 2 * p.tp * 2 * D);
-                        const int y = static_cast<int>(plane * p.T);
+                        meta[e] = make_int4(kind, 0, 0, 0);
+                        mbar_arrive_expect_tx(kb, dbytes);
 #pragma unroll
-                        for (int c = 0; c < D / 64; ++c) {
-                            tma_load_2d(kt + c * 8192, &tmDK, 64 * c, y, &full[s]);
-                            tma_load_2d(kt + dtile + c * 8192, &tmDV, 64 * c, y, &full[s]);
-                        }
+                        for (int c = 0; c < D / 64; ++c) tma_load_2d(kt + c * 8192, &tmDK, 64 * c, dy, kb);
                     } else {
-                        const int halves = a1 >= 0 ? 2 : 1;
-                        meta[s] = make_int4(kind, min(64, len - a0), a1 >= 0 ? min(64, len - a1) : 0, 0);
-                        mbar_arrive_expect_tx(&full[s], halves * (C::STAGE + C::EXPS) / 2);
+                        meta[e] = make_int4(kind, min(64, len - a0), a1 >= 0 ? min(64, len - a1) : 0, 0);
+                        mbar_arrive_expect_tx(kb, halves * (C::TILE + C::EXPS) / 2);
                         for (int h = 0; h < halves; ++h) {
                             const int64_t row = plane * p.cap + (h == 0 ? a0 : a1);
-                            const int y = static_cast<int>(row);
                             if constexpr (E4M3) {
-                                tma_load_2d(kt + h * 64 * D, &tmK, 0, y, &full[s]);
-                                tma_load_2d(kt + C::TILE + h * 64 * D, &tmV, 0, y, &full[s]);
-                                bulk_load(exps + s * 256 + h * 64, p.k_exp + row, 64, &full[s]);
-                                bulk_load(exps + s * 256 + 128 + h * 64, p.v_exp + row, 64, &full[s]);
+                                tma_load_2d(kt + h * 64 * D, &tmK, 0, static_cast<int>(row), kb);
+                                bulk_load(exps + e * 256 + h * 64, p.k_exp + row, 64, kb);
+                                bulk_load(exps + e * 256 + 128 + h * 64, p.v_exp + row, 64, kb);
                             } else {
 #pragma unroll
-                                for (int c = 0; c < D / 64; ++c) {
-                                    tma_load_2d(kt + c * 16384 + h * 8192, &tmK, 64 * c, y, &full[s]);
-                                    tma_load_2d(kt + C::TILE + c * 16384 + h * 8192, &tmV, 64 * c, y, &full[s]);
+                                for (int c = 0; c < D / 64; ++c)
+                                    tma_load_2d(kt + c * 16384 + h * 8192, &tmK, 64 * c, static_cast<int>(row), kb);
+                            }
+                        }
+                    }
+                    k.next(p.nk);
+                    if (kind != kTileEnd) {
+                        ok = v.n < p.nv || mbar_wait(&vempty[v.s], v.par ^ 1u, p.status, kTreeDetail | 0x02u);
+                        if (ok) {
+                            uint8_t* vt = vring + v.s * C::TILE;
+                            uint64_t* vb = &vfull[v.s];
+                            if (kind == kTileDraft) {
+                                mbar_arrive_expect_tx(vb, dbytes);
+#pragma unroll
+                                for (int c = 0; c < D / 64; ++c) tma_load_2d(vt + c * 8192, &tmDV, 64 * c, dy, vb);
+                            } else {
+                                mbar_arrive_expect_tx(vb, halves * C::TILE / 2);
+                                for (int h = 0; h < halves; ++h) {
+                                    const int y = static_cast<int>(plane * p.cap + (h == 0 ? a0 : a1));
+                                    if constexpr (E4M3) {
+                                        tma_load_2d(vt + h * 64 * D, &tmV, 0, y, vb);
+                                    } else {
+#pragma unroll
+                                        for (int c = 0; c < D / 64; ++c)
+                                            tma_load_2d(vt + c * 16384 + h * 8192, &tmV, 64 * c, y, vb);
+                                    }
                                 }
                             }
+                            v.next(p.nv);
                         }
                     }
                 }
             }
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-            if (ok) {
-                ++used;
-                advance();
-            }
         };
         while (pos < end && ok) {
             const int b = static_cast<int>(tile / p.rows_per_seq);
@@ -412,125 +451,172 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
             unit = 0;
             ++tile;
         }
-        // every copy lands before the block ends, also when another role gave up (earlier uses of a
-        // stage were complete before it was filled again)
+        // every copy lands before the block ends, also when another role gave up (earlier uses of a slot
+        // were complete before it was filled again)
         if (lane == 0) {
-            for (int i = 0; i < p.nstg && i < used; ++i) {
-                s = s == 0 ? p.nstg - 1 : s - 1;
-                if (s == p.nstg - 1) par ^= 1u;
-                if (!mbar_wait(&full[s], par, p.status, kTreeDetail | 0x02u)) break;
+            for (int i = 0; i < p.nk && i < k.n; ++i) {
+                k.s = k.s == 0 ? p.nk - 1 : k.s - 1;
+                if (k.s == p.nk - 1) k.par ^= 1u;
+                if (!mbar_wait(&kfull[k.s], k.par, p.status, kTreeDetail | 0x03u)) break;
+            }
+            for (int i = 0; i < p.nv && i < v.n; ++i) {
+                v.s = v.s == 0 ? p.nv - 1 : v.s - 1;
+                if (v.s == p.nv - 1) v.par ^= 1u;
+                if (!mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x04u)) break;
             }
         }
     } else if (warp == 4 * C::NWG + 1) {
         // ------------------------------------------------ MMA
         if (lane == 0) {
             const uint32_t q0 = smem_u32(q_s), p0 = smem_u32(p_s);
-            int it = 0, pt = 0;       // slots so far (S buffers), and tiles among them (P buffers)
+            int it = 0, pt = 0;       // S slots so far, and tiles whose P.V was issued
+            int npend = 0;            // tiles whose S was issued and P.V was not (two at most: S has two buffers)
+            uint32_t drafts = 0;      // bit 0: the older of them is the drafted tokens, bit 1: the younger
             uint32_t qpar = 0;
             bool issued = false;
-            int pend_s = -1, pend_kind = 0;
             bool fresh = true;        // the next P.V begins O
-            auto pv = [&]() {         // P.V of the tile before
-                ok = mbar_wait(&pfull[pt & 1], (pt >> 1) & 1, p.status, kTreeDetail | 0x03u);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t pb = p0 + (pt % C::NP) * C::PB;
-                const uint32_t vt = smem_u32(ring + pend_s * C::STAGE);
-                const uint64_t b = tree_desc(pb, 128, 2048, 0);
-                if (pend_kind == kTileDraft || !E4M3) {
-                    const bool draft = pend_kind == kTileDraft;
-                    const uint32_t sub = draft ? 8192 : 16384;
-                    const uint64_t a = tree_desc(vt + (draft ? dtile : C::TILE), D == 128 ? sub : 0, 1024, 2);
-                    const int steps = draft ? p.tp / 16 : 8;
-                    for (int k = 0; k < steps; ++k)
-                        mma_bf16_ss(tm_o, desc_at(a, k * 2048), desc_at(b, k * 256), idesc_bf16_f32(128, R, 1, 1),
-                                    !fresh || k > 0 ? 1u : 0u);
+
+            // K step k of P.V of the oldest pending tile
+            auto pv_step = [&](int n, uint64_t a, uint64_t b) {
+                if constexpr (!E4M3) {
+                    mma_bf16_ss(tm_o, desc_at(a, n * 2048), desc_at(b, n * 256), idesc_bf16_f32(128, R, 1, 1),
+                                !fresh || n > 0 ? 1u : 0u);
+                } else if constexpr (C::STACK) {
+                    mma_f8_ss(tm_o, desc_at(a, n * 32 * D), desc_at(b, n * 512), idesc_f8(3 * R, 1, 1, 1),
+                              !fresh || n > 0 ? 1u : 0u);
                 } else {
-                    const uint64_t a = D == 128 ? tree_desc(vt + C::TILE, 0, 1024, 2) : tree_desc(vt + C::TILE, 0, 512, 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if constexpr (C::STACK) {
-                            mma_f8_ss(tm_o, desc_at(a, k * 32 * D), desc_at(b, k * 512), idesc_f8(3 * R, 1, 1, 1),
-                                      !fresh || k > 0 ? 1u : 0u);
-                        } else {
-#pragma unroll
-                            for (int t = 0; t < 3; ++t)
-                                mma_f8_ss(tm_o, desc_at(a, k * 32 * D), desc_at(b, t * C::PTERM + k * 512),
-                                          idesc_f8(R, 1, 1, 1), !fresh || k > 0 || t > 0 ? 1u : 0u);
-                        }
-                    }
+                    for (int t = 0; t < 3; ++t)
+                        mma_f8_ss(tm_o, desc_at(a, n * 32 * D), desc_at(b, t * C::PTERM + n * 512), idesc_f8(R, 1, 1, 1),
+                                  !fresh || n > 0 || t > 0 ? 1u : 0u);
                 }
+            };
+            constexpr int PVS = E4M3 ? 4 : 8, QKS = E4M3 ? D / 32 : D / 16;
+            auto qk_step = [&](int n, uint32_t d, uint64_t a, uint64_t b) {
+                if constexpr (!E4M3) {
+                    mma_bf16_ss(d, desc_at(a, (n / 4) * 16384 + (n % 4) * 32), desc_at(b, (n / 4) * (R * 128) + (n % 4) * 32),
+                                idesc_bf16_f32(128, R, 0, 0), n > 0 ? 1u : 0u);
+                } else if constexpr (C::STACK) {
+                    mma_f8_ss(d, desc_at(a, n * 32), desc_at(b, n * 32), idesc_f8(2 * R, 0, 0, 0), n > 0 ? 1u : 0u);
+                } else {
+                    mma_f8_ss(d, desc_at(a, n * 32), desc_at(b, n * 32), idesc_f8(R, 0, 0, 0), n > 0 ? 1u : 0u);
+                    mma_f8_ss(d, desc_at(a, n * 32), desc_at(b, R * D + n * 32), idesc_f8(R, 1, 0, 0), 1u);
+                }
+            };
+            auto v_desc = [&]() {
+                const uint32_t vt = smem_u32(vring + v.s * C::TILE);
+                if constexpr (E4M3)
+                    return D == 128 ? tree_desc(vt, 0, 1024, 2) : tree_desc(vt, 0, 512, 4);
+                else
+                    return tree_desc(vt, D == 128 ? 16384 : 0, 1024, 2);
+            };
+            auto p_desc = [&]() { return tree_desc(p0 + (pt % C::NP) * C::PB, 128, 2048, 0); };
+            auto p_wait = [&]() {     // P and V of the oldest pending tile are there
+                ok = mbar_wait(&pfull[pt & 1], (pt >> 1) & 1, p.status, kTreeDetail | 0x05u) &&
+                     mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x06u);
+                tc_fence_after();
+            };
+            auto pv_done = [&]() {
                 fresh = false;
-                mma_commit(&empty[pend_s]);
+                mma_commit(&vempty[v.s]);
                 mma_commit(&pvdone[pt % C::NP]);
+                v.next(p.nv);
                 ++pt;
+                --npend;
+                drafts >>= 1;
+            };
+            auto pv_alone = [&]() {
+                const uint64_t b = p_desc();
+                if (drafts & 1u) {
+                    const uint64_t a = tree_desc(smem_u32(vring + v.s * C::TILE), D == 128 ? 8192 : 0, 1024, 2);
+                    for (int n = 0; n < p.tp / 16; ++n)
+                        mma_bf16_ss(tm_o, desc_at(a, n * 2048), desc_at(b, n * 256), idesc_bf16_f32(128, R, 1, 1),
+                                    !fresh || n > 0 ? 1u : 0u);
+                } else {
+                    const uint64_t a = v_desc();
+#pragma unroll
+                    for (int n = 0; n < PVS; ++n) pv_step(n, a, b);
+                }
+                pv_done();
+            };
+            auto flush = [&]() {
+                while (npend > 0 && ok) {
+                    p_wait();
+                    if (ok) pv_alone();
+                }
             };
             while (pos < end && ok) {
                 const int b = static_cast<int>(tile / p.rows_per_seq);
                 const int units = tree_units(p, tree_len(p, b));
                 const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
-                ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x04u);
+                ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x07u);
                 qpar ^= 1u;
                 fresh = true;
                 while (ok) {
-                    ok = mbar_wait(&full[s], par, p.status, kTreeDetail | 0x05u);
+                    // the next S goes where the older pending tile's was: its P.V comes first, or, if the next
+                    // K is there, step by step with it (two chains of dependent products side by side)
+                    bool both = false;
+                    if (npend == 2) {
+                        p_wait();
+                        if (!ok) break;
+                        both = (drafts & 1u) == 0 && mbar_test(&kfull[k.s], k.par);
+                        if (!both) pv_alone();
+                    }
+                    ok = mbar_wait(&kfull[k.s], k.par, p.status, kTreeDetail | 0x08u);
                     if (!ok) break;
-                    const int kind = meta[s].x;
+                    const int kind = meta[k.n % kTreeMeta].x;
+                    if (both && kind != kTileCache) {
+                        pv_alone();
+                        both = false;
+                    }
+                    issued = true;
                     if (kind == kTileEnd) {
-                        if (pend_s >= 0) pv();
-                        pend_s = -1;
+                        flush();
                         if (ok) {
                             // with every product of the piece complete, the softmax may read O
-                            issued = true;
                             mma_commit(&sfull[it & 1]);
-                            mbar_arrive(&empty[s]);
+                            mbar_arrive(&kempty[k.s]);
                             ++it;
-                            advance();
+                            k.next(p.nk);
                         }
                         break;
                     }
                     if (E4M3 && kind == kTileDraft) {
                         // Q comes again, as bf16: a slot without scores tells the softmax so
-                        if (pend_s >= 0) pv();
-                        pend_s = -1;
+                        flush();
                         if (!ok) break;
-                        issued = true;
                         mma_commit(&sfull[it & 1]);
                         ++it;
-                        ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x06u);
+                        ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x09u);
                         qpar ^= 1u;
                         if (!ok) break;
                     }
                     tc_fence_after();
-                    const uint32_t kt = smem_u32(ring + s * C::STAGE);
+                    const uint32_t kt = smem_u32(ring + k.s * C::TILE);
                     const uint32_t d = tm + (it & 1) * C::SW;
-                    issued = true;
-                    if (kind == kTileDraft || !E4M3) {
-                        const uint32_t sub = kind == kTileDraft ? 8192 : 16384;
+                    if (kind == kTileDraft) {
                         const uint64_t a = tree_desc(kt, 16, 1024, 2), bq = tree_desc(q0, 16, 1024, 2);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            mma_bf16_ss(d, desc_at(a, (k / 4) * sub + (k % 4) * 32), desc_at(bq, (k / 4) * (R * 128) + (k % 4) * 32),
-                                        idesc_bf16_f32(128, R, 0, 0), k > 0 ? 1u : 0u);
+                        for (int n = 0; n < D / 16; ++n)
+                            mma_bf16_ss(d, desc_at(a, (n / 4) * 8192 + (n % 4) * 32), desc_at(bq, (n / 4) * (R * 128) + (n % 4) * 32),
+                                        idesc_bf16_f32(128, R, 0, 0), n > 0 ? 1u : 0u);
                     } else {
-                        const uint64_t a = D == 128 ? tree_desc(kt, 16, 1024, 2) : tree_desc(kt, 16, 512, 4);
-                        const uint64_t bq = D == 128 ? tree_desc(q0, 16, 1024, 2) : tree_desc(q0, 16, 512, 4);
+                        const uint64_t a = E4M3 && D == 64 ? tree_desc(kt, 16, 512, 4) : tree_desc(kt, 16, 1024, 2);
+                        const uint64_t bq = E4M3 && D == 64 ? tree_desc(q0, 16, 512, 4) : tree_desc(q0, 16, 1024, 2);
+                        const uint64_t va = v_desc(), pb = p_desc();
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            if constexpr (C::STACK) {
-                                mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, k * 32), idesc_f8(2 * R, 0, 0, 0), k > 0 ? 1u : 0u);
-                            } else {
-                                mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, k * 32), idesc_f8(R, 0, 0, 0), k > 0 ? 1u : 0u);
-                                mma_f8_ss(d, desc_at(a, k * 32), desc_at(bq, R * D + k * 32), idesc_f8(R, 1, 0, 0), 1u);
-                            }
+                        for (int n = 0; n < PVS; ++n) {
+                            if (both) pv_step(n, va, pb);
+                            if (n < QKS) qk_step(n, d, a, bq);
                         }
                     }
                     mma_commit(&sfull[it & 1]);
-                    if (pend_s >= 0) pv();
-                    pend_s = s;
-                    pend_kind = kind;
+                    mma_commit(&kempty[k.s]);
+                    if (both) pv_done();
+                    if (kind == kTileDraft) drafts |= 1u << npend;
+                    ++npend;
                     ++it;
-                    advance();
+                    k.next(p.nk);
                 }
                 pos += u1 - unit;
                 unit = 0;
@@ -538,7 +624,7 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
             }
             if (issued) {  // nothing of this CTA's still runs when TMEM goes
                 mma_commit(&done);
-                mbar_wait(&done, 0, p.status, kTreeDetail | 0x07u);
+                mbar_wait(&done, 0, p.status, kTreeDetail | 0x0Au);
             }
         }
         __syncwarp();
@@ -638,38 +724,36 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
             while (true) {
                 // Every slot is one barrier, and a second one when the first says so: a warp whose wait ran
                 // out takes both, so that all warps leave together whatever the others saw in the slot.
-                if (ok) ok = mbar_wait(&sfull[it & 1], (it >> 1) & 1, p.status, kTreeDetail | 0x08u);
+                if (ok) ok = mbar_wait(&sfull[it & 1], (it >> 1) & 1, p.status, kTreeDetail | 0x0Bu);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 tc_fence_after();
-                const int4 mt = ok ? meta[s] : make_int4(kTileEnd, 0, 0, 0);
+                const int me = k.n % kTreeMeta;
+                const int4 mt = ok ? meta[me] : make_int4(kTileEnd, 0, 0, 0);
                 if (E4M3 && mt.x == kTileDraft) {
                     // this slot only says that the drafted tokens come: every S so far is formed, Q's buffer
                     // is free for the bf16 rows; the next slot has the scores
                     q_bf16();
                     q_ready();
                     ++it;
-                    ok = mbar_wait(&sfull[it & 1], (it >> 1) & 1, p.status, kTreeDetail | 0x09u);
+                    ok = mbar_wait(&sfull[it & 1], (it >> 1) & 1, p.status, kTreeDetail | 0x0Cu);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     tc_fence_after();
                 }
                 if (mt.x == kTileEnd) {
                     if (softmax_any(bar, !ok) && softmax_any(bar, !ok)) ok = false;
-                    if (ok) {
-                        if (lane == 0) mbar_arrive(&empty[s]);
-                        ++it;
-                        advance();
-                    }
+                    ++it;
+                    k.next(p.nk);
                     break;
                 }
                 const bool draft = mt.x == kTileDraft;
-                uint8_t* kt = ring + s * C::STAGE;
+                uint8_t* vt = vring + v.s * C::TILE;
                 const bool valid = draft ? key < p.T : (key & 63) < (key < 64 ? mt.y : mt.z);
                 const bool partial = draft || mt.y < 64 || mt.z < 64;
                 float kf = p.scale_log2;
                 int ev = 0;
                 if (E4M3 && !draft && valid) {
-                    kf *= __uint_as_float(static_cast<uint32_t>(exps[s * 256 + key]) << 23);
-                    ev = exps[s * 256 + 128 + key];
+                    kf *= __uint_as_float(static_cast<uint32_t>(exps[me * 256 + key]) << 23);
+                    ev = exps[me * 256 + 128 + key];
                 }
                 if (draft && wg == 0 && key < 2) dflag[key] = 0;
                 // scores against the kept maximum, log2 units: x = acc * kf (* the row's factor) - m
@@ -788,7 +872,7 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                     if (!fresh) {
                         const int j = pt - 1;
                         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[j % C::NP], (j / C::NP) & 1, p.status,
-                                                               kTreeDetail | 0x0Au));
+                                                               kTreeDetail | 0x0Du));
                         tc_fence_after();
 #pragma unroll 1
                         for (int t = 0; t < (cached ? C::OT : 1); ++t) {
@@ -814,10 +898,8 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                     }
                     fresh = false;
                 }
-                // P's buffer: this tile's S is complete, and with it every product issued before it, the P.V
-                // of two tiles before among them; a single buffer waits for the last one
-                if (C::NP == 1 && pt > 0 && ok)
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[0], (pt - 1) & 1, p.status, kTreeDetail | 0x0Bu));
+                // P's buffer is free: this tile's S is complete, and with it every product issued before it, the
+                // P.V of two tiles before among them
                 uint8_t* pb = p_s + (pt % C::NP) * C::PB;
 #pragma unroll
                 for (int i = 0; i < C::RW / 2; ++i) {
@@ -877,8 +959,8 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                 if (wg == 0 && partial && !valid && !draft) {
                     // what the cache holds past the sequence must not meet P's zeros as a NaN
                     for (int c = 0; c < C::ROW / 16; ++c) {
-                        uint8_t* v = kt + C::TILE + (E4M3 ? key * D + 16 * c : (c / 8) * 16384 + key * 128 + 16 * (c % 8));
-                        *reinterpret_cast<uint4*>(v) = make_uint4(0u, 0u, 0u, 0u);
+                        uint8_t* z = vt + (E4M3 ? key * D + 16 * c : (c / 8) * 16384 + key * 128 + 16 * (c % 8));
+                        *reinterpret_cast<uint4*>(z) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
                 if (wg == 0 && draft && key < p.tp) {
@@ -886,8 +968,8 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                     // out here and given to the tokens that attend it at the end
                     uint32_t bad = 0;
                     for (int c = 0; c < D / 8; ++c) {
-                        uint4* v = reinterpret_cast<uint4*>(kt + dtile + (c / 8) * 8192 + key * 128 + 16 * (c % 8));
-                        uint32_t w[4] = {v->x, v->y, v->z, v->w};
+                        uint4* z = reinterpret_cast<uint4*>(vt + (c / 8) * 8192 + key * 128 + 16 * (c % 8));
+                        uint32_t w[4] = {z->x, z->y, z->z, z->w};
                         uint32_t any = 0;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -895,9 +977,9 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                             if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0x0000FFFFu, any = 1;
                         }
                         if (!valid) {
-                            *v = make_uint4(0u, 0u, 0u, 0u);
+                            *z = make_uint4(0u, 0u, 0u, 0u);
                         } else if (any) {
-                            *v = make_uint4(w[0], w[1], w[2], w[3]);
+                            *z = make_uint4(w[0], w[1], w[2], w[3]);
                             bad = 1;
                         }
                     }
@@ -907,13 +989,11 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                 tc_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&pfull[pt & 1]);
-                    mbar_arrive(&empty[s]);
-                }
+                if (lane == 0) mbar_arrive(&pfull[pt & 1]);
                 ++it;
                 ++pt;
-                advance();
+                k.next(p.nk);
+                v.next(p.nv);
             }
             if (!ok) break;
 
@@ -1097,10 +1177,12 @@ static bool launch_tree(TreeParams p, const CUtensorMap& k, const CUtensorMap& v
                         const CUtensorMap& dv, cudaStream_t st, int32_t* launches) {
     using C = TreeCfg<D, E4M3, R>;
     constexpr int budget = (C::CTAS == 2 ? 112 : 225) * 1024;
-    static_assert(C::FIXED + 2 * (C::STAGE + C::EXPS) <= budget, "two stages must fit");
-    p.nstg = (budget - C::FIXED) / (C::STAGE + C::EXPS);
-    if (p.nstg > kTreeMaxStages) p.nstg = kTreeMaxStages;
-    const int smem = C::FIXED + p.nstg * (C::STAGE + C::EXPS);
+    constexpr int fit = (budget - C::FIXED) / C::TILE;
+    constexpr int slots = fit < 2 * kTreeMaxSlots ? fit : 2 * kTreeMaxSlots;
+    static_assert(slots >= 4, "two slots of K and of V must fit");
+    p.nk = slots / 2;
+    p.nv = slots - p.nk;
+    const int smem = C::FIXED + slots * C::TILE;
     static std::atomic<uint64_t> configured{0};
     if (!configure_smem_once(reinterpret_cast<const void*>(attn_tree_kernel<D, E4M3, R>), smem, configured)) return false;
     attn_tree_kernel<D, E4M3, R><<<p.runs, C::THREADS, smem, st>>>(k, v, dk, dv, p);

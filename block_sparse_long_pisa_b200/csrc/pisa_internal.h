@@ -278,7 +278,7 @@ struct TreeParams {
     int32_t mt, rows_per_seq;       // row tiles per selection row, and per sequence (Hsel * mt)
     int32_t runs, min_units;        // runs (CTAs) at most, and units one run has at least on average
     int32_t tp;                     // drafted tokens rounded up to 16
-    int32_t nstg;                   // ring stages (set by the launcher)
+    int32_t nk, nv;                 // slots of the K and of the V ring (set by the launcher)
     float scale_log2;
 };
 
