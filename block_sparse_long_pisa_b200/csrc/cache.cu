@@ -19,7 +19,7 @@
 namespace pisa {
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheRows = 4;  // rows one lane group has in flight
+constexpr int kCacheRows = 4;  // rows of one lane group, all in flight together
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t r;
@@ -37,82 +37,83 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t two) {
 // NaN that such a row stands for.
 __device__ __forceinline__ float exp_value(uint32_t e) { return __uint_as_float(e << 23); }
 
-// The sequence's first cache position and row count; false when the range does not fit the cache.
-__device__ __forceinline__ bool cache_range(const CacheParams& p, int b, int64_t& start, int& count) {
-    start = p.start != nullptr ? p.start[b] : 0;
-    count = p.count != nullptr ? p.count[b] : p.tokens;
-    return count >= 0 && count <= p.tokens && start >= 0 && start + count <= p.cap;
-}
-
-// Row r of the call -> sequence, head, token (tokens fastest).
-struct RowAt {
-    int b, h, t;
-    __device__ __forceinline__ RowAt(const CacheParams& p, uint32_t r) {  // B * H * tokens < 2^31
-        const uint32_t q = r / static_cast<uint32_t>(p.tokens);
-        t = static_cast<int>(r - q * static_cast<uint32_t>(p.tokens));
-        b = static_cast<int>(q / static_cast<uint32_t>(p.H));
-        h = static_cast<int>(q - static_cast<uint32_t>(b) * static_cast<uint32_t>(p.H));
+// A lane group's segment: kCacheRows consecutive tokens of one plane, clipped to the tokens that count;
+// segments of a plane lie side by side. One division and one look at start and count per segment.
+struct Segment {
+    int b, h, t0, n;       // sequence, head, first token, tokens that count (0: nothing to do)
+    int64_t at;            // cache row of the first token
+    __device__ __forceinline__ Segment(const CacheParams& p, uint32_t seg, uint32_t detail, bool reports) {
+        const uint32_t per_plane = (static_cast<uint32_t>(p.tokens) + kCacheRows - 1) / kCacheRows;
+        const uint32_t plane = seg / per_plane;
+        b = h = t0 = n = 0;
+        at = 0;
+        if (plane >= static_cast<uint32_t>(p.B) * p.H) return;
+        b = static_cast<int>(plane / static_cast<uint32_t>(p.H));
+        h = static_cast<int>(plane - static_cast<uint32_t>(b) * p.H);
+        t0 = static_cast<int>(seg - plane * per_plane) * kCacheRows;
+        const int64_t start = p.start != nullptr ? __ldg(p.start + b) : 0;
+        const int count = p.count != nullptr ? __ldg(p.count + b) : p.tokens;
+        if (count < 0 || count > p.tokens || start < 0 || start + count > p.cap) {
+            // the sequence is left alone
+            if (reports && h == 0 && t0 == 0) record_error(p.status, PISA_ERR_BAD_INDEX, detail);
+            return;
+        }
+        n = max(0, min(kCacheRows, count - t0));
+        at = static_cast<int64_t>(plane) * p.cap + start + t0;
     }
 };
 
-// grid: (row blocks, K or V). Each lane group takes kCacheRows rows, a block's groups side by side.
+// grid: (segment blocks, K or V).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheParams p) {
     constexpr int LPR = D / 8, G = kCacheThreads / LPR;
     const int lane8 = threadIdx.x % LPR, group = threadIdx.x / LPR;
     const bool is_v = blockIdx.y != 0;
-    const uint32_t rows = static_cast<uint32_t>(p.B) * p.H * p.tokens;
-    const uint32_t r0 = blockIdx.x * (G * kCacheRows) + group;
-    const __nv_bfloat16* src = is_v ? p.V : p.K;
-    const int64_t s0 = is_v ? p.vs[0] : p.ks[0], s1 = is_v ? p.vs[1] : p.ks[1], s2 = is_v ? p.vs[2] : p.ks[2];
+    const Segment w(p, blockIdx.x * G + group, (kKernCache << 8) | 0xB0u, lane8 == 0 && !is_v);
+    const int64_t* st = is_v ? p.vs : p.ks;
+    const int64_t step = st[2];
+    const __nv_bfloat16* src = (is_v ? p.V : p.K) + w.b * st[0] + w.h * st[1] + w.t0 * step + 8 * lane8;
     uint4 v[kCacheRows];
-    int64_t at[kCacheRows];
 #pragma unroll
     for (int u = 0; u < kCacheRows; ++u) {
-        const uint32_t r = r0 + u * G;
-        at[u] = -1;
         v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= rows) continue;
-        const RowAt w(p, r);
-        int64_t start;
-        int count;
-        if (!cache_range(p, w.b, start, count)) {
-            if (lane8 == 0 && w.h == 0 && w.t == 0 && !is_v)
-                record_error(p.status, PISA_ERR_BAD_INDEX, (kKernCache << 8) | 0xB0u);
-            continue;
-        }
-        if (w.t >= count) continue;
-        at[u] = (static_cast<int64_t>(w.b) * p.H + w.h) * p.cap + start + w.t;
-        v[u] = __ldg(reinterpret_cast<const uint4*>(src + w.b * s0 + w.h * s1 + w.t * s2 + 8 * lane8));
+        if (u < w.n) v[u] = __ldg(reinterpret_cast<const uint4*>(src + u * step));
     }
+    if constexpr (!E4M3) {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.Vc : p.Kc) + w.at * D + 8 * lane8;
 #pragma unroll
-    for (int u = 0; u < kCacheRows; ++u) {
-        if constexpr (!E4M3) {
-            if (at[u] >= 0)
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.Vc : p.Kc) + at[u] * D + 8 * lane8) =
-                    v[u];
-        } else {
-            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-            uint32_t top = 0;  // largest magnitude of the even and of the odd values
+        for (int u = 0; u < kCacheRows; ++u)
+            if (u < w.n) *reinterpret_cast<uint4*>(dst + u * D) = v[u];
+    } else {
+        uint8_t* dst = static_cast<uint8_t*>(is_v ? p.Vc : p.Kc) + w.at * D + 8 * lane8;
+        uint8_t* dexp = (is_v ? p.ve : p.ke) + w.at;
+        uint32_t top[kCacheRows];  // largest magnitude of the even and of the odd values
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+        for (int u = 0; u < kCacheRows; ++u)
+            top[u] = __vmaxu2(__vmaxu2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
+                              __vmaxu2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu));
 #pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            top = max(top & 0xFFFFu, top >> 16);
+        for (int o = 1; o < LPR; o <<= 1) {
+#pragma unroll
+            for (int u = 0; u < kCacheRows; ++u) top[u] = __vmaxu2(top[u], __shfl_xor_sync(0xFFFFFFFFu, top[u], o));
+        }
+#pragma unroll
+        for (int u = 0; u < kCacheRows; ++u) {
+            const uint32_t t = max(top[u] & 0xFFFFu, top[u] >> 16);
             // 1.m * 2^(E - 127) <= 1.75 * 2^8 * 2^(e - 127)
-            const int E = static_cast<int>(top >> 7);
+            const int E = static_cast<int>(t >> 7);
             const bool bad = E == 255;
-            const int e = bad ? 255 : max(1, E - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0));
+            const int e = bad ? 255 : max(1, E - 8 + ((t & 0x7Fu) > 0x60u ? 1 : 0));
             const float f = __uint_as_float(static_cast<uint32_t>(bad ? 127 : 254 - e) << 23);
+            const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
             uint32_t q[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                q[k] = e4m3x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
-            if (at[u] >= 0) {
-                uint8_t* dst = static_cast<uint8_t*>(is_v ? p.Vc : p.Kc) + at[u] * D + 8 * lane8;
-                *reinterpret_cast<uint2*>(dst) =
+                q[k] = e4m3x2(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xFFFF0000u) * f);
+            if (u < w.n) {
+                *reinterpret_cast<uint2*>(dst + u * D) =
                     bad ? make_uint2(0u, 0u) : make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-                if (lane8 == 0) (is_v ? p.ve : p.ke)[at[u]] = static_cast<uint8_t>(e);
+                if (lane8 == 0) dexp[u] = static_cast<uint8_t>(e);
             }
         }
     }
@@ -123,54 +124,43 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CachePa
     constexpr int LPR = D / 8, G = kCacheThreads / LPR;
     const int lane8 = threadIdx.x % LPR, group = threadIdx.x / LPR;
     const bool is_v = blockIdx.y != 0;
-    const uint32_t rows = static_cast<uint32_t>(p.B) * p.H * p.tokens;
-    const uint32_t r0 = blockIdx.x * (G * kCacheRows) + group;
-    __nv_bfloat16* out = is_v ? p.Vo : p.Ko;
-    uint4 v[kCacheRows];
-    uint32_t e[kCacheRows];
-    bool ok[kCacheRows];
+    const Segment w(p, blockIdx.x * G + group, (kKernCache << 8) | 0xB1u, lane8 == 0 && !is_v);
+    __nv_bfloat16* out =
+        (is_v ? p.Vo : p.Ko) + ((static_cast<int64_t>(w.b) * p.H + w.h) * p.tokens + w.t0) * D + 8 * lane8;
+    if constexpr (!E4M3) {
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.Vc : p.Kc) + w.at * D + 8 * lane8;
+        uint4 v[kCacheRows];
 #pragma unroll
-    for (int u = 0; u < kCacheRows; ++u) {
-        const uint32_t r = r0 + u * G;
-        ok[u] = false;
-        if (r >= rows) continue;
-        const RowAt w(p, r);
-        int64_t start;
-        int count;
-        if (!cache_range(p, w.b, start, count)) {
-            if (lane8 == 0 && w.h == 0 && w.t == 0 && !is_v)
-                record_error(p.status, PISA_ERR_BAD_INDEX, (kKernCache << 8) | 0xB1u);
-            continue;
-        }
-        if (w.t >= count) continue;
-        ok[u] = true;
-        const int64_t at = (static_cast<int64_t>(w.b) * p.H + w.h) * p.cap + start + w.t;
-        if constexpr (E4M3) {
-            const uint2 two = __ldg(reinterpret_cast<const uint2*>(
-                static_cast<const uint8_t*>(is_v ? p.Vc : p.Kc) + at * D + 8 * lane8));
-            v[u].x = two.x;
-            v[u].y = two.y;
-            e[u] = __ldg((is_v ? p.ve : p.ke) + at);
-        } else {
-            v[u] = __ldg(reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(is_v ? p.Vc : p.Kc) + at * D + 8 * lane8));
-        }
-    }
+        for (int u = 0; u < kCacheRows; ++u)
+            if (u < w.n) v[u] = __ldg(reinterpret_cast<const uint4*>(src + u * D));
 #pragma unroll
-    for (int u = 0; u < kCacheRows; ++u) {
-        if (!ok[u]) continue;
-        if constexpr (E4M3) {
+        for (int u = 0; u < kCacheRows; ++u)
+            if (u < w.n) *reinterpret_cast<uint4*>(out + u * D) = v[u];
+    } else {
+        const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.Vc : p.Kc) + w.at * D + 8 * lane8;
+        const uint8_t* sexp = (is_v ? p.ve : p.ke) + w.at;
+        uint2 v[kCacheRows];
+        uint32_t e[kCacheRows];
+#pragma unroll
+        for (int u = 0; u < kCacheRows; ++u) {
+            if (u < w.n) {
+                v[u] = __ldg(reinterpret_cast<const uint2*>(src + u * D));
+                e[u] = __ldg(sexp + u);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kCacheRows; ++u) {
+            if (u >= w.n) break;
             const float f = exp_value(e[u]);
-            const uint32_t w[2] = {v[u].x, v[u].y};
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 x = e4m3x2_values((w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
-                o[k] = pack_bf16x2(x.x * f, x.y * f);
+                const uint32_t x = k < 2 ? v[u].x : v[u].y;
+                const float2 y = e4m3x2_values((k & 1) ? x >> 16 : x & 0xFFFFu);
+                o[k] = pack_bf16x2(y.x * f, y.y * f);
             }
-            v[u] = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(out + u * D) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r0 + u * G) * D + 8 * lane8) = v[u];
     }
 }
 
@@ -218,7 +208,56 @@ __device__ __forceinline__ void e4m3_block_mean(const uint8_t* K, const uint8_t*
     }
 }
 
-// Level 0 of many new blocks: one warp per block.
+// Subtrees of S = f^m key blocks (S <= 16, or f): a CTA forms the level-0 means of its blocks that are
+// new (one warp per block), takes the older ones as they stand, and forms the m levels above them in
+// shared memory; nodes over older blocks alone come out as they were. Grid: planes x the subtrees
+// that hold a new block.
+template <int D>
+__global__ void __launch_bounds__(256) cache_subtree_kernel(const CachePyramidParams p, int S, int m, int sub_lo,
+                                                            int subtrees) {
+    extern __shared__ __align__(16) float rows[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t plane = blockIdx.x / subtrees;
+    const int64_t j0 = static_cast<int64_t>(sub_lo + blockIdx.x % subtrees) * S;
+    float* out = p.pyr + plane * p.plane_rows * D;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = warp; r < S && j0 + r < p.n0; r += 8) {
+        const int64_t j = j0 + r;
+        float* row = rows + r * D;
+        if (j >= p.b_lo) {
+            const int64_t at = plane * p.N + j * p.blk;
+            e4m3_block_mean<D>(p.K + at * D, p.e + at, p.blk, row);
+            __syncwarp();
+            for (int c = lane; c < D / 4; c += 32)
+                reinterpret_cast<float4*>(out + j * D)[c] = reinterpret_cast<const float4*>(row)[c];
+        } else {
+            for (int c = lane; c < D / 4; c += 32)
+                reinterpret_cast<float4*>(row)[c] = reinterpret_cast<const float4*>(out + j * D)[c];
+        }
+    }
+    int64_t width = 1;
+    int span = S;
+    const float* below = rows;
+    for (int l = 1; l <= m; ++l) {
+        __syncthreads();
+        const int up = span / p.factor;
+        float* cur = rows + (below - rows) + span * D;
+        const int64_t c0 = j0 / (width * p.factor), first = j0 / width;
+        for (int e = threadIdx.x; e < up * (D / 4); e += 256) {
+            const int64_t c = c0 + e / (D / 4);
+            const int q = e % (D / 4);
+            if (c >= p.lsize[l] || c * width * p.factor >= p.n0) continue;
+            const float4 v = node_mean4(below + 4 * q, first, D, c, p.factor, p.lsize[l - 1], width, p.n0);
+            *reinterpret_cast<float4*>(cur + (c - c0) * D + 4 * q) = v;
+            *reinterpret_cast<float4*>(out + (p.loff[l] + c) * D + 4 * q) = v;
+        }
+        below = cur;
+        span = up;
+        width *= p.factor;
+    }
+}
+
+// Level 0 of many new blocks without subtrees (a single level, or a factor above 64): one warp per block.
 template <int D>
 __global__ void __launch_bounds__(128) cache_block_mean_kernel(const CachePyramidParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -231,10 +270,11 @@ __global__ void __launch_bounds__(128) cache_block_mean_kernel(const CachePyrami
     e4m3_block_mean<D>(p.K + row * D, p.e + row, p.blk, p.pyr + (plane * p.plane_rows + j) * D);
 }
 
-// The nodes over the blocks [b_lo, b_hi) of one plane per CTA, level after level; with LEVEL0 (few
-// new blocks) the CTA's warps form the level-0 means first, and the whole append is one launch.
+// The nodes of levels l0 .. L - 1 over the blocks [b_lo, b_hi) of one plane per CTA, level after level;
+// with LEVEL0 (few new blocks) the CTA's warps form the level-0 means first, and the whole append is
+// one launch.
 template <int D, bool LEVEL0>
-__global__ void __launch_bounds__(256) cache_pyramid_kernel(const CachePyramidParams p) {
+__global__ void __launch_bounds__(256) cache_pyramid_kernel(const CachePyramidParams p, int l0) {
     const int64_t plane = blockIdx.x;
     float* out = p.pyr + plane * p.plane_rows * D;
     if constexpr (LEVEL0) {
@@ -246,7 +286,8 @@ __global__ void __launch_bounds__(256) cache_pyramid_kernel(const CachePyramidPa
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the level-0 grid is complete
     }
     int64_t width = 1;
-    for (int l = 1; l < p.L; ++l) {
+    for (int l = 1; l < l0; ++l) width *= p.factor;
+    for (int l = l0; l < p.L; ++l) {
         __syncthreads();
         const int64_t wl = width * p.factor;
         const int c_lo = static_cast<int>(p.b_lo / wl);
@@ -263,9 +304,9 @@ __global__ void __launch_bounds__(256) cache_pyramid_kernel(const CachePyramidPa
 
 template <int D>
 static bool launch_cache_rows(const CacheParams& p, bool e4m3, bool write, cudaStream_t st) {
-    constexpr int per_block = kCacheThreads / (D / 8) * kCacheRows;
-    const int64_t rows = static_cast<int64_t>(p.B) * p.H * p.tokens;
-    const int64_t blocks = (rows + per_block - 1) / per_block;
+    constexpr int G = kCacheThreads / (D / 8);
+    const int64_t segments = static_cast<int64_t>(p.B) * p.H * ((p.tokens + kCacheRows - 1) / kCacheRows);
+    const int64_t blocks = (segments + G - 1) / G;
     if (blocks > INT32_MAX) return false;
     const dim3 grid(static_cast<unsigned>(blocks), 2);
     if (write) {
@@ -297,16 +338,34 @@ constexpr int kCachePyramidOneLaunch = 8;
 template <int D>
 static bool launch_cache_pyramid_d(const CachePyramidParams& p, cudaStream_t st, int32_t* launches) {
     if (p.b_hi - p.b_lo <= kCachePyramidOneLaunch) {
-        cache_pyramid_kernel<D, true><<<p.planes, 256, 0, st>>>(p);
+        cache_pyramid_kernel<D, true><<<p.planes, 256, 0, st>>>(p, 1);
         if (cudaGetLastError() != cudaSuccess) return false;
         ++*launches;
         return true;
     }
-    const int64_t warps = static_cast<int64_t>(p.planes) * (p.b_hi - p.b_lo);
-    cache_block_mean_kernel<D><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(p);
+    int l0 = 1;  // first level that the second launch forms
+    if (p.L >= 2 && p.factor <= 64) {
+        int S = p.factor, m = 1;
+        while (m + 1 <= p.L - 1 && S * p.factor <= 16) {
+            S *= p.factor;
+            ++m;
+        }
+        int rows = 0, span = S;
+        for (int l = 0; l <= m; ++l, span /= p.factor) rows += span;
+        const int sub_lo = p.b_lo / S, subtrees = (p.b_hi - 1) / S + 1 - sub_lo;
+        const int64_t blocks = static_cast<int64_t>(p.planes) * subtrees;
+        if (blocks > INT32_MAX) return false;
+        cache_subtree_kernel<D><<<static_cast<unsigned>(blocks), 256, rows * D * sizeof(float), st>>>(p, S, m, sub_lo,
+                                                                                                      subtrees);
+        l0 = m + 1;
+    } else {
+        const int64_t warps = static_cast<int64_t>(p.planes) * (p.b_hi - p.b_lo);
+        if ((warps + 3) / 4 > INT32_MAX) return false;
+        cache_block_mean_kernel<D><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(p);
+    }
     if (cudaGetLastError() != cudaSuccess) return false;
     ++*launches;
-    if (p.L < 2) return true;
+    if (l0 >= p.L) return true;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.planes));
     cfg.blockDim = dim3(256);
@@ -316,7 +375,7 @@ static bool launch_cache_pyramid_d(const CachePyramidParams& p, cudaStream_t st,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, cache_pyramid_kernel<D, false>, p) != cudaSuccess) return false;
+    if (cudaLaunchKernelEx(&cfg, cache_pyramid_kernel<D, false>, p, l0) != cudaSuccess) return false;
     ++*launches;
     return true;
 }

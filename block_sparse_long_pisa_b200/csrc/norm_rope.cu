@@ -30,21 +30,31 @@ namespace pisa {
 
 constexpr int kNrThreads = 256;
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+// 8 bf16 of a row as four packed fp32 pairs, and back (one rounding).
+__device__ __forceinline__ void unpack8(const uint4& v, uint64_t (&f)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        f[2 * k] = bf_lo(w[k]);
-        f[2 * k + 1] = bf_hi(w[k]);
-    }
+    for (int k = 0; k < 4; ++k) f[k] = f2_pack(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
 }
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float lo, hi;
+        f2_unpack(f[k], lo, hi);
+        w[k] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint64_t nr_mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t nr_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 __device__ __forceinline__ uint4 load_row(const __nv_bfloat16* p) {
@@ -113,11 +123,16 @@ __device__ __forceinline__ void load_turn(const float2* tab, const LaneMap<D>& l
     }
 }
 
-// The mates' values of this lane's 8 dims.
-__device__ __forceinline__ void mate_values(const uint4& v, int mate, bool inter, float (&m)[8]) {
-    if (inter) {
-        unpack8(make_uint4(__funnelshift_l(v.x, v.x, 16), __funnelshift_l(v.y, v.y, 16),
-                           __funnelshift_l(v.z, v.z, 16), __funnelshift_l(v.w, v.w, 16)), m);
+// The mates' values of this lane's 8 dims: interleaved pairs are the lane's own, changed places.
+template <bool INTER>
+__device__ __forceinline__ void mate_values(const uint4& v, const uint64_t (&own)[4], int mate, uint64_t (&m)[4]) {
+    if constexpr (INTER) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float lo, hi;
+            f2_unpack(own[k], lo, hi);
+            m[k] = f2_pack(hi, lo);
+        }
     } else {
         unpack8(shfl4(v, mate), m);
     }
@@ -139,7 +154,7 @@ __device__ __forceinline__ void fill_table(const NormRopeParams& p, int64_t tok0
 }
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRopeParams p) {
     extern __shared__ __align__(16) float2 tab[];
     constexpr int LPR = D / 8;
     constexpr int G = kNrThreads / LPR;  // lane groups of the block
@@ -147,217 +162,250 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
     const LaneMap<D> lm(p.R, INTER);
     const int group = threadIdx.x / LPR;
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tb;
-    const int tt = group % p.tb;
-    const int64_t tok = tok0 + tt;
-    const bool live = tok < p.ntokens;
-    const int hstep = G / p.tb;
+    const int tt = group % p.tb, off = group / p.tb, hstep = G / p.tb;
+    const bool live = tok0 + tt < p.ntokens;
+    const int64_t tok = live ? tok0 + tt : 0;
     const int h0 = static_cast<int>(blockIdx.y) * p.hb, h1 = min(h0 + p.hb, p.Hq + p.Hkv);
-    const int64_t b = live ? tok / p.T : 0, t = live ? tok % p.T : 0;
-    const int64_t xq0 = b * p.xq[0] + t * p.xq[1] + 8 * lm.lane8, xk0 = b * p.xk[0] + t * p.xk[1] + 8 * lm.lane8;
-    auto src = [&](int h) -> const __nv_bfloat16* {
-        return h < p.Hq ? p.Xq + xq0 + h * p.xq[2] : p.Xk + xk0 + (h - p.Hq) * p.xk[2];
-    };
-    const int hfirst = h0 + group / p.tb;
-    // the first rows travel while the angles are formed
+    const int64_t b = tok / p.T, t = tok % p.T;
+    const __nv_bfloat16* src = nullptr;   // this lane's dims of its next row to load
+    __nv_bfloat16* dst = nullptr;         // and of its next row to store
+    int64_t sstep = 0, dstep = 0;
+    int n = 0, todo = 0;                  // rows of the section that are left to load, and its rounds
     uint4 v[U];
+    // heads [lo, hi) of one side: the first U rows travel
+    auto begin = [&](bool is_k) {
+        const int lo = is_k ? max(h0 - p.Hq, 0) : h0, hi = is_k ? h1 - p.Hq : min(h1, p.Hq);
+        const int64_t* st = is_k ? p.xk : p.xq;
+        const int64_t H = is_k ? p.Hkv : p.Hq;
+        src = (is_k ? p.Xk : p.Xq) + b * st[0] + t * st[1] + (lo + off) * st[2] + 8 * lm.lane8;
+        dst = (is_k ? p.K : p.Q) + ((b * H + lo + off) * p.T + t) * D + 8 * lm.lane8;
+        sstep = hstep * st[2];
+        dstep = static_cast<int64_t>(hstep) * p.T * D;
+        n = live ? (hi - lo - off + hstep - 1) / hstep : 0;
+        todo = hi > lo ? (hi - lo + hstep - 1) / hstep : 0;  // the same for every group of the block
+        if (hi - lo - off <= 0) n = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (live && hfirst + u * hstep < h1) v[u] = load_row(src(hfirst + u * hstep));
+        for (int u = 0; u < U; ++u) {
+            if (u < n) v[u] = load_row(src);
+            src += sstep;
+        }
+    };
+    const bool has_q = h0 < p.Hq;
+    begin(!has_q);  // before the angles are formed
     fill_table(p, tok0, p.tb, tab);
     __syncthreads();
     Turn tn;
     load_turn<D>(tab + (live ? tt : 0) * (p.R / 2), lm, p.R, INTER, tn);
-
-    float a[8], bb[8];
-    bool for_k = false;
-    auto fold = [&](const float* w) {
-        const int md = INTER ? 0 : (lm.mate - static_cast<int>(threadIdx.x & 31)) * 8;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int d = 8 * lm.lane8 + k;
-            const int m = INTER ? (lm.turns ? (d ^ 1) : d) : d + md;
-            a[k] = tn.c[k] * (w != nullptr ? __ldg(w + d) : 1.f);
-            bb[k] = tn.s[k] * (w != nullptr ? __ldg(w + m) : 1.f);
+    for (int side = has_q ? 0 : 1; side < 2; ++side) {
+        if (side == 1 && has_q) {
+            if (h1 <= p.Hq) break;
+            begin(true);
         }
-    };
-    fold(p.wq);
-    // every lane of a warp walks the same number of rows: the shuffles need all of them
-    for (int h = h0; h < h1; h += U * hstep) {
+        // y = r (x a + x_mate c)
+        const float* w = side == 0 ? p.wq : p.wk;
+        const int md = INTER ? 0 : (lm.mate - static_cast<int>(threadIdx.x & 31)) * 8;
+        uint64_t a[4], c[4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int hh = h + u * hstep + group / p.tb;
-            const bool ok = live && hh < h1;
-            if (ok && hh >= p.Hq && !for_k) {
-                fold(p.wk);
-                for_k = true;
+        for (int k = 0; k < 4; ++k) {
+            float wa[2] = {1.f, 1.f}, wm[2] = {1.f, 1.f};
+            if (w != nullptr) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int d = 8 * lm.lane8 + 2 * k + e;
+                    wa[e] = __ldg(w + d);
+                    wm[e] = __ldg(w + (INTER ? d ^ 1 : d + md));
+                }
             }
-            if (!ok) v[u] = make_uint4(0u, 0u, 0u, 0u);
-            float x[8], m[8], y[8];
-            unpack8(v[u], x);
-            mate_values(v[u], lm.mate, INTER, m);
-            float ss = 0.f;
+            a[k] = f2_pack(tn.c[2 * k] * wa[0], tn.c[2 * k + 1] * wa[1]);
+            c[k] = f2_pack(tn.s[2 * k] * wm[0], tn.s[2 * k + 1] * wm[1]);
+        }
+        // every lane of a warp walks the same number of rows: the shuffles need all of them
+        for (int i = 0; i < todo; i += U) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
-            const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
-            // past the rotated dims b is 0: the mate (the lane itself) must not bring in a NaN twice,
-            // which is harmless, its own value being one already
+            for (int u = 0; u < U; ++u) {
+                const bool ok = i + u < n;
+                if (!ok) v[u] = make_uint4(0u, 0u, 0u, 0u);
+                uint64_t x[4], m[4];
+                unpack8(v[u], x);
+                mate_values<INTER>(v[u], x, lm.mate, m);
+                uint64_t s2 = nr_mul2(x[0], x[0]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = r * fmaf(m[k], bb[k], x[k] * a[k]);
-            if (ok) {
-                __nv_bfloat16* dst = hh < p.Hq ? p.Q + ((b * p.Hq + hh) * p.T + t) * D
-                                               : p.K + ((b * p.Hkv + (hh - p.Hq)) * p.T + t) * D;
-                *reinterpret_cast<uint4*>(dst + 8 * lm.lane8) = pack8(y);
+                for (int k = 1; k < 4; ++k) s2 = nr_fma2(x[k], x[k], s2);
+                float s0, s1;
+                f2_unpack(s2, s0, s1);
+                const float r = rsqrtf(row_sum<D>(s0 + s1) * (1.f / D) + p.eps);
+                const uint64_t r2 = f2_pack(r, r);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = nr_mul2(nr_fma2(m[k], c[k], nr_mul2(x[k], a[k])), r2);
+                if (ok) *reinterpret_cast<uint4*>(dst) = pack8(x);
+                dst += dstep;
+                if (i + u + U < n) v[u] = load_row(src);
+                src += sstep;
             }
-            const int hn = hh + U * hstep;
-            if (live && hn < h1) v[u] = load_row(src(hn));
         }
     }
 }
 
+// One side (queries or keys) per block: blocks [0, p.qblocks) walk the query tiles, the others the
+// key tiles, so a thread has one side's weights and sums.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_backward_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, 2) norm_rope_backward_kernel(const NormRopeParams p) {
     extern __shared__ __align__(16) float2 tab[];
     __shared__ float red[kNrThreads * 8];
     constexpr int LPR = D / 8;
     constexpr int G = kNrThreads / LPR;
-    constexpr int U = 2;
+    constexpr int U = 4;
     const LaneMap<D> lm(p.R, INTER);
     const int group = threadIdx.x / LPR;
-    const int tt = group % p.tb;
-    const int hstep = G / p.tb;
-    const int hsplits = (p.Hq + p.Hkv + p.hb - 1) / p.hb;
-    float wq[8], wk[8], gq[8], gk[8];
+    const int tt = group % p.tb, off = group / p.tb, hstep = G / p.tb;
+    const bool is_k = static_cast<int>(blockIdx.x) >= p.qblocks;
+    const int H = is_k ? p.Hkv : p.Hq;
+    const int hb = is_k ? p.hbk : p.hb, hsplits = (H + hb - 1) / hb;
+    const int64_t tiles = (p.ntokens + p.tb - 1) / p.tb * hsplits;
+    const int64_t* st = is_k ? p.xk : p.xq;
+    const int64_t* gt = is_k ? p.dxk : p.dxq;
+    const float* w = is_k ? p.wk : p.wq;
+    uint64_t wl[4], g2[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        wq[k] = p.wq != nullptr ? __ldg(p.wq + 8 * lm.lane8 + k) : 1.f;
-        wk[k] = p.wk != nullptr ? __ldg(p.wk + 8 * lm.lane8 + k) : 1.f;
-        gq[k] = gk[k] = 0.f;
+    for (int k = 0; k < 4; ++k) {
+        const int d = 8 * lm.lane8 + 2 * k;
+        wl[k] = w != nullptr ? f2_pack(__ldg(w + d), __ldg(w + d + 1)) : f2_pack(1.f, 1.f);
+        g2[k] = 0ull;
     }
-    for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    const int first = static_cast<int>(blockIdx.x) - (is_k ? p.qblocks : 0);
+    const int step = is_k ? static_cast<int>(gridDim.x) - p.qblocks : p.qblocks;
+    int64_t table_of = -1;
+    for (int64_t tile = first; tile < tiles; tile += step) {
         const int64_t tok0 = (tile / hsplits) * p.tb;
-        const int64_t tok = tok0 + tt;
-        const bool live = tok < p.ntokens;
-        const int h0 = static_cast<int>(tile % hsplits) * p.hb, h1 = min(h0 + p.hb, p.Hq + p.Hkv);
-        const int64_t b = live ? tok / p.T : 0, t = live ? tok % p.T : 0;
-        const int64_t c0 = 8 * lm.lane8;
-        auto load = [&](int h, uint4& x, uint4& g) {
-            if (h < p.Hq) {
-                x = load_row(p.Xq + b * p.xq[0] + t * p.xq[1] + h * p.xq[2] + c0);
-                g = load_row(p.dQ + ((b * p.Hq + h) * p.T + t) * D + c0);
-            } else {
-                const int hk = h - p.Hq;
-                x = load_row(p.Xk + b * p.xk[0] + t * p.xk[1] + hk * p.xk[2] + c0);
-                g = load_row(p.dK + ((b * p.Hkv + hk) * p.T + t) * D + c0);
-            }
-        };
+        const bool live = tok0 + tt < p.ntokens;
+        const int64_t tok = live ? tok0 + tt : 0;
+        const int h0 = static_cast<int>(tile % hsplits) * hb, h1 = min(h0 + hb, H);
+        const int64_t b = tok / p.T, t = tok % p.T;
+        const __nv_bfloat16* xs = (is_k ? p.Xk : p.Xq) + b * st[0] + t * st[1] + (h0 + off) * st[2] + 8 * lm.lane8;
+        const __nv_bfloat16* gs = (is_k ? p.dK : p.dQ) + ((b * H + h0 + off) * p.T + t) * D + 8 * lm.lane8;
+        __nv_bfloat16* dst = (is_k ? p.dXk : p.dXq) + b * gt[0] + t * gt[1] + (h0 + off) * gt[2] + 8 * lm.lane8;
+        const int64_t sstep = hstep * st[2], gstep = static_cast<int64_t>(hstep) * p.T * D, dstep = hstep * gt[2];
+        const int n = live && h1 - h0 > off ? (h1 - h0 - off + hstep - 1) / hstep : 0;
+        const int todo = (h1 - h0 + hstep - 1) / hstep;
         uint4 xv[U], gv[U];
-        const int hfirst = h0 + group / p.tb;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (live && hfirst + u * hstep < h1) load(hfirst + u * hstep, xv[u], gv[u]);
-        __syncthreads();  // the previous tile's table has been read
-        fill_table(p, tok0, p.tb, tab);
-        __syncthreads();
+        for (int u = 0; u < U; ++u) {
+            if (u < n) {
+                xv[u] = load_row(xs);
+                gv[u] = load_row(gs);
+            }
+            xs += sstep;
+            gs += gstep;
+        }
+        if (tok0 != table_of) {
+            __syncthreads();  // the previous tile's table has been read
+            fill_table(p, tok0, p.tb, tab);
+            __syncthreads();
+            table_of = tok0;
+        }
         Turn tn;
         load_turn<D>(tab + (live ? tt : 0) * (p.R / 2), lm, p.R, INTER, tn);
-        for (int h = h0; h < h1; h += U * hstep) {
+        for (int i = 0; i < todo; i += U) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int hh = h + u * hstep + group / p.tb;
-                const bool ok = live && hh < h1;
-                const bool is_q = hh < p.Hq;
+                const bool ok = i + u < n;
                 if (!ok) xv[u] = gv[u] = make_uint4(0u, 0u, 0u, 0u);
-                float x[8], g[8], m[8], dn[8];
+                uint64_t x[4], g[4], m[4];
                 unpack8(xv[u], x);
                 unpack8(gv[u], g);
-                mate_values(gv[u], lm.mate, INTER, m);
-                float ss = 0.f, dot = 0.f;
+                mate_values<INTER>(gv[u], g, lm.mate, m);
+                uint64_t s2 = 0ull, d2 = 0ull;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    g[k] = fmaf(m[k], -tn.s[k], g[k] * tn.c[k]);  // du: the turn taken back
-                    dn[k] = g[k] * (is_q ? wq[k] : wk[k]);
-                    ss = fmaf(x[k], x[k], ss);
-                    dot = fmaf(dn[k], x[k], dot);
+                for (int k = 0; k < 4; ++k) {
+                    // du: the turn taken back; then dn = du w
+                    g[k] = nr_fma2(m[k], f2_pack(-tn.s[2 * k], -tn.s[2 * k + 1]),
+                                   nr_mul2(g[k], f2_pack(tn.c[2 * k], tn.c[2 * k + 1])));
+                    m[k] = nr_mul2(g[k], wl[k]);
+                    s2 = nr_fma2(x[k], x[k], s2);
+                    d2 = nr_fma2(m[k], x[k], d2);
                 }
-                ss = row_sum<D>(ss);
-                dot = row_sum<D>(dot);
-                const float r = rsqrtf(ss * (1.f / D) + p.eps);
-                const float f = r * r * dot * (1.f / D);
-                if (ok) {
-                    float dx[8];
+                float s0, s1, d0, d1;
+                f2_unpack(s2, s0, s1);
+                f2_unpack(d2, d0, d1);
+                const float ss = row_sum<D>(s0 + s1), dot = row_sum<D>(d0 + d1);
+                // a row that does not count adds nothing (with eps = 0 its own r would be infinite)
+                const float r = ok ? rsqrtf(ss * (1.f / D) + p.eps) : 0.f;
+                const float f = -r * r * dot * (1.f / D);
+                const uint64_t r2 = f2_pack(r, r), f2 = f2_pack(f, f);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        dx[k] = r * fmaf(-f, x[k], dn[k]);
-                        const float xr = x[k] * r;
-                        if (is_q)
-                            gq[k] = fmaf(g[k], xr, gq[k]);
-                        else
-                            gk[k] = fmaf(g[k], xr, gk[k]);
-                    }
-                    __nv_bfloat16* dst = is_q ? p.dXq + b * p.dxq[0] + t * p.dxq[1] + hh * p.dxq[2]
-                                              : p.dXk + b * p.dxk[0] + t * p.dxk[1] + (hh - p.Hq) * p.dxk[2];
-                    *reinterpret_cast<uint4*>(dst + c0) = pack8(dx);
+                for (int k = 0; k < 4; ++k) {
+                    m[k] = nr_mul2(nr_fma2(x[k], f2, m[k]), r2);
+                    g2[k] = nr_fma2(g[k], nr_mul2(x[k], r2), g2[k]);
                 }
-                const int hn = hh + U * hstep;
-                if (live && hn < h1) load(hn, xv[u], gv[u]);
+                if (ok) *reinterpret_cast<uint4*>(dst) = pack8(m);
+                dst += dstep;
+                if (i + u + U < n) {
+                    xv[u] = load_row(xs);
+                    gv[u] = load_row(gs);
+                }
+                xs += sstep;
+                gs += gstep;
             }
         }
     }
-    // the block's groups, then one row of partial sums per block: [block][q, k][D]
+    // the block's groups: one row of partial sums per block
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) red[group * D + 8 * lm.lane8 + k] = side == 0 ? gq[k] : gk[k];
-        __syncthreads();
-        for (int d = threadIdx.x; d < D; d += kNrThreads) {
-            float s = 0.f;
+    for (int k = 0; k < 4; ++k) {
+        float lo, hi;
+        f2_unpack(g2[k], lo, hi);
+        red[group * D + 8 * lm.lane8 + 2 * k] = lo;
+        red[group * D + 8 * lm.lane8 + 2 * k + 1] = hi;
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += kNrThreads) {
+        float s = 0.f;
 #pragma unroll 4
-            for (int gg = 0; gg < G; ++gg) s += red[gg * D + d];
-            p.part[(static_cast<int64_t>(blockIdx.x) * 2 + side) * D + d] = s;
-        }
+        for (int gg = 0; gg < G; ++gg) s += red[gg * D + d];
+        p.part[static_cast<int64_t>(blockIdx.x) * D + d] = s;
     }
 }
 
-// dwq and dwk from the blocks' partial sums: 32 columns per block, 32 threads per column.
-__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int blocks, int D, float* dwq,
+// dwq and dwk from the blocks' partial sums [blocks][D]: 32 columns per block (blockIdx.y: the side),
+// 32 threads per column.
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int qblocks, int blocks, int D, float* dwq,
                                                             float* dwk) {
     __shared__ float red[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), ty = threadIdx.x >> 5;
+    const int lo = blockIdx.y == 0 ? 0 : qblocks, hi = blockIdx.y == 0 ? qblocks : blocks;
     float s = 0.f;
-    for (int i = ty; i < blocks; i += 32) s += part[static_cast<int64_t>(i) * 2 * D + col];
+    for (int i = lo + ty; i < hi; i += 32) s += part[static_cast<int64_t>(i) * D + col];
     red[ty][threadIdx.x & 31] = s;
     __syncthreads();
     if (ty == 0) {
         float v = 0.f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v += red[i][threadIdx.x];
-        float* dst = col < D ? dwq : dwk;
-        if (dst != nullptr) dst[col % D] = v;
+        float* dst = blockIdx.y == 0 ? dwq : dwk;
+        if (dst != nullptr) dst[col] = v;
     }
 }
 
 // Tokens per tile and heads per tile: full tiles (one token per lane group, all heads) unless that
 // leaves SMs idle; then fewer tokens, then fewer heads, down to one row per lane group.
-void norm_rope_tiles(NormRopeParams* p, int D) {
-    const int G = kNrThreads / (D / 8), H = p->Hq + p->Hkv;
+static int64_t norm_rope_tiles(NormRopeParams* p, int D, int H) {
+    const int G = kNrThreads / (D / 8);
     p->tb = G;
     p->hb = H;
     while (true) {
         const int64_t blocks = (p->ntokens + p->tb - 1) / p->tb * ((H + p->hb - 1) / p->hb);
-        if (blocks >= kNormRopeBlocks) break;
+        if (blocks >= kNormRopeBlocks) return blocks;
         if (p->tb > 1)
             p->tb /= 2;
         else if (p->hb > G)
             p->hb = (p->hb + 1) / 2;
         else
-            break;
+            return blocks;
     }
-    p->tiles = (p->ntokens + p->tb - 1) / p->tb * ((H + p->hb - 1) / p->hb);
 }
 
 bool launch_norm_rope(NormRopeParams p, int D, bool inter, cudaStream_t st) {
-    norm_rope_tiles(&p, D);
+    norm_rope_tiles(&p, D, p.Hq + p.Hkv);
     const int64_t bx = (p.ntokens + p.tb - 1) / p.tb;
     if (bx > INT32_MAX) return false;
     const dim3 grid(static_cast<unsigned>(bx), (p.Hq + p.Hkv + p.hb - 1) / p.hb);
@@ -378,8 +426,22 @@ bool launch_norm_rope(NormRopeParams p, int D, bool inter, cudaStream_t st) {
 
 bool launch_norm_rope_backward(NormRopeParams p, int D, bool inter, float* dwq, float* dwk, cudaStream_t st,
                                int32_t* launches) {
-    norm_rope_tiles(&p, D);
-    const int grid = static_cast<int>(p.tiles < kNormRopeBlocks ? p.tiles : kNormRopeBlocks);
+    // the tile shape of all heads together; the blocks are shared out by the sides' rows
+    const int H = p.Hq + p.Hkv;
+    const int64_t all = norm_rope_tiles(&p, D, H);
+    p.hbk = p.hb < p.Hkv ? p.hb : p.Hkv;
+    p.hb = p.hb < p.Hq ? p.hb : p.Hq;
+    const int64_t tt = (p.ntokens + p.tb - 1) / p.tb;
+    const int64_t qtiles = tt * ((p.Hq + p.hb - 1) / p.hb), ktiles = tt * ((p.Hkv + p.hbk - 1) / p.hbk);
+    const int64_t most = all < kNormRopeBlocks ? all + 1 : kNormRopeBlocks;
+    int64_t qb = (most * p.Hq + H - 1) / H;
+    if (qb >= most) qb = most - 1;
+    if (qb < 1) qb = 1;
+    int64_t kb = most - qb < 1 ? 1 : most - qb;
+    if (qb > qtiles) qb = qtiles;
+    if (kb > ktiles) kb = ktiles;
+    p.qblocks = static_cast<int>(qb);
+    const int grid = static_cast<int>(qb + kb);
     const size_t smem = static_cast<size_t>(p.tb) * (p.R / 2) * sizeof(float2);
     if (D == 64) {
         if (inter)
@@ -395,8 +457,19 @@ bool launch_norm_rope_backward(NormRopeParams p, int D, bool inter, float* dwq, 
     if (cudaGetLastError() != cudaSuccess) return false;
     ++*launches;
     if (dwq == nullptr && dwk == nullptr) return true;
-    norm_rope_dw_kernel<<<2 * D / 32, 1024, 0, st>>>(p.part, grid, D, dwq, dwk);
-    if (cudaGetLastError() != cudaSuccess) return false;
+    // launched while the rows are still being worked on: it waits for them itself
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(D / 32), 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(p.part), p.qblocks, grid, D, dwq, dwk) !=
+        cudaSuccess)
+        return false;
     ++*launches;
     return true;
 }

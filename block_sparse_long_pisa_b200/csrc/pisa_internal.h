@@ -228,10 +228,13 @@ struct NormRopeParams {
     __nv_bfloat16 *dXq, *dXk;       // backward: strided outputs
     const float *wq, *wk, *inv_freq;
     const int32_t* pos;             // [B, T]
-    float* part;                    // backward: [blocks, 2, D]
+    float* part;                    // backward: [blocks, D]
     int64_t xq[3], xk[3], dxq[3], dxk[3];  // element strides: batch, token, head
-    int64_t ntokens, tiles;         // B * T; tiles set by the launcher
-    int32_t T, Hq, Hkv, R, tb, hb;  // tb, hb: tokens and heads of a tile (set by the launcher)
+    int64_t ntokens;                // B * T
+    int32_t T, Hq, Hkv, R;
+    // set by the launcher: tokens and heads of a tile; backward: heads of a key tile, and the blocks
+    // (the first ones) that take query tiles
+    int32_t tb, hb, hbk, qblocks;
     float eps;
 };
 
@@ -302,7 +305,6 @@ pisa_status launch_attn_prefill(const Plan& pl, const void* Q, const void* K, co
 bool launch_attn_prefill_dual(int D, int blk, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                               const AttnParams& p, dim3 grid, cudaStream_t st);
 bool launch_attn_decode(const Plan& pl, const DecodeParams& p, cudaStream_t st, int32_t* launches);
-void norm_rope_tiles(NormRopeParams* p, int D);
 bool launch_norm_rope(NormRopeParams p, int D, bool inter, cudaStream_t st);
 bool launch_norm_rope_backward(NormRopeParams p, int D, bool inter, float* dwq, float* dwk, cudaStream_t st,
                                int32_t* launches);

@@ -79,7 +79,7 @@ static NormRopeParams norm_rope_params(const pisa_norm_rope_shape* s, const void
 }
 
 static size_t norm_rope_ws(const pisa_norm_rope_shape* s) {
-    return static_cast<size_t>(kNormRopeBlocks) * 2 * s->head_dim * sizeof(float);
+    return static_cast<size_t>(kNormRopeBlocks) * s->head_dim * sizeof(float);
 }
 
 static pisa_status check_cache(const pisa_cache_shape* s) {

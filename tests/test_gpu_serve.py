@@ -127,6 +127,20 @@ def test_norm_rope_backward(pisa, case):
         assert torch.equal(again[2], out[2]) and torch.equal(again[3], out[3])
 
 
+def test_norm_rope_without_eps(pisa):
+    """eps = 0: rows that do not exist (the last tile's) add nothing to the weights' gradient."""
+    rng = np.random.default_rng(4)
+    B, T, Hq, Hkv, D = 1, 37, 3, 1, 64
+    xq, xk, dq, dk = bf16(rng, B, T, Hq, D), bf16(rng, B, T, Hkv, D), bf16(rng, B, Hq, T, D), bf16(rng, B, Hkv, T, D)
+    s = pisa.NormRopeShape(B, T, Hq, Hkv, D, D, 0, 0.0)
+    pos, fr = np.arange(T)[None].astype(np.int32), np.float32(1.0) / (1 + np.arange(32, dtype=np.float32))
+    w = f32(np.ones(D))
+    _, _, dwq, dwk = pisa.qk_norm_rope_backward(s, xq, xk, i32(pos), f32(fr), dq, dk, w, w)
+    for dw, x, dy in ((dwq, xq, dq), (dwk, xk, dk)):
+        _, rw, size = so.norm_rope_backward(host(x), None, pos, fr, D, 0, 0.0, host(dy))
+        assert (np.abs(host(dw) - rw) <= 2.0 ** -19 * size).all()
+
+
 def test_norm_rope_rows_that_are_not_finite_stay_alone(pisa):
     """A NaN or an infinity in one row leaves every other row as it was; a zero row gives zeros."""
     import torch

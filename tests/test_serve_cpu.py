@@ -201,7 +201,7 @@ def test_workspace_sizes_depend_on_the_shape_alone():
     for drafts, rm, runs in ((1, 16, 296), (8, 16, 296), (16, 32, 296), (32, 64, 148), (48, 96, 148), (64, 64, 148)):
         s = pisa.TreeShape(**{**TREE, "drafts": drafts})
         assert pisa.tree_workspace_size(s) == 256 + 2 * runs * rm * 66 * 4
-    assert pisa.norm_rope_workspace_size(pisa.NormRopeShape(2, 3, 4, 2, 64, 64)) == 592 * 2 * 64 * 4
+    assert pisa.norm_rope_workspace_size(pisa.NormRopeShape(2, 3, 4, 2, 64, 64)) == 592 * 64 * 4
 
 
 # ----------------------------------------------------------------------------- pins of the oracle
