@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import math
 import os
 
@@ -205,9 +206,15 @@ def last_launch_count() -> int:
 
 # ----------------------------------------------------------------------------- torch-facing calls
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> int | None:
@@ -451,45 +458,57 @@ class Session:
 
 # ----------------------------------------------------------------------------- around the attention
 
-def _device_of(named, stream):
-    """The one CUDA device that all tensors of `named` ((tensor, name), tensor None = absent) are on,
-    and the raw stream: `stream`, which must be that device's, or the device's current one."""
+# These calls take a few microseconds on the GPU when they serve one token, so their checks are kept
+# short: plain comparisons, the error spelled out only when one fails.
+
+def _current_stream(index: int) -> int:
+    """The raw current stream of a device (torch's own shortcut to it where it has one: a tenth of the
+    microsecond that a Stream object costs)."""
     torch = _torch()
-    dev = None
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _launch(where, call, stream, named, args):
+    """call(*args, stream) with the device of the tensors current. `named`: (tensor or None, name); all
+    must be on one CUDA device. `stream` must be that device's; None is its current one."""
+    torch = _torch()
+    dev = -1
     for t, name in named:
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()
+        if d == dev:
+            continue
+        if d < 0:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if dev >= 0:
+            raise ValueError(f"{name} must be on cuda:{dev}, got cuda:{d}")
+        dev = d
     if stream is None:
-        return dev, torch.cuda.current_stream(dev).cuda_stream
-    if stream.device != dev:
-        raise ValueError(f"the stream must be one of {dev}, got {stream.device}")
-    return dev, stream.cuda_stream
-
-
-def _on(dev, call, *args) -> int:
-    """The call's status with `dev` current (kernels launch on the current device)."""
-    torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        return call(*args)
-    with torch.cuda.device(dev):
-        return call(*args)
+        raw = _current_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream must be one of cuda:{dev}, got {stream.device}")
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev:   # kernels launch on the current device
+        status = call(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, raw)
+    if status != OK:
+        raise PisaError(status, where)
 
 
 def _like(t, dtype, shape, name):
-    """A contiguous tensor of this type and shape (its device is checked by _device_of)."""
+    """A contiguous tensor of this type and shape (its device is checked by _launch)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows_like(t, dtype, shape, name):
@@ -497,12 +516,12 @@ def _rows_like(t, dtype, shape, name):
     dims of one, whose stride says nothing)."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[3] != 1:
+    a, b, c, last = t.stride()
+    if last != 1:
         raise ValueError(f"{name} must have adjacent elements in its last dimension")
-    return _i64x3(*[0 if n == 1 else x for n, x in zip(shape[:3], st[:3])])
+    return (a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, c if shape[2] > 1 else 0)
 
 
 def _status_word(ws):
@@ -525,10 +544,14 @@ class NormRopeShape:
     interleaved: int = 0
     eps: float = 1e-6
 
-    def c(self, xq=None, xk=None, dxq=None, dxk=None) -> PisaNormRopeShape:
-        z = _i64x3()
-        return PisaNormRopeShape(self.batch, self.tokens, self.heads_q, self.heads_kv, self.head_dim, self.rotary_dim,
-                                 int(self.interleaved), float(self.eps), xq or z, xk or z, dxq or z, dxk or z)
+    def c(self, xq=(0, 0, 0), xk=(0, 0, 0), dxq=(0, 0, 0), dxk=(0, 0, 0)) -> PisaNormRopeShape:
+        return _norm_rope_struct(self, xq, xk, dxq, dxk)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_rope_struct(s, xq, xk, dxq, dxk):
+    return PisaNormRopeShape(s.batch, s.tokens, s.heads_q, s.heads_kv, s.head_dim, s.rotary_dim, int(s.interleaved),
+                             float(s.eps), _i64x3(*xq), _i64x3(*xk), _i64x3(*dxq), _i64x3(*dxk))
 
 
 def norm_rope_workspace_size(shape: NormRopeShape) -> int:
@@ -567,18 +590,13 @@ def qk_norm_rope(shape: NormRopeShape, Xq, Xk, pos, inv_freq, wq=None, wk=None, 
     torch = _torch()
     s = shape
     sq, sk = _norm_rope_args(s, Xq, Xk, pos, inv_freq, wq, wk)
-    if Q is None:
-        Q = torch.empty((s.batch, s.heads_q, s.tokens, s.head_dim), dtype=torch.bfloat16, device=Xq.device)
-    else:
-        _like(Q, torch.bfloat16, (s.batch, s.heads_q, s.tokens, s.head_dim), "Q")
-    if K is None:
-        K = torch.empty((s.batch, s.heads_kv, s.tokens, s.head_dim), dtype=torch.bfloat16, device=Xq.device)
-    else:
-        _like(K, torch.bfloat16, (s.batch, s.heads_kv, s.tokens, s.head_dim), "K")
-    dev, st = _device_of(((Xq, "Xq"), (Xk, "Xk"), (pos, "pos"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"),
-                          (Q, "Q"), (K, "K")), stream)
-    _check(_on(dev, _lib.pisa_qk_norm_rope, s.c(sq, sk), Xq.data_ptr(), Xk.data_ptr(), _ptr(wq), _ptr(wk),
-               _ptr(inv_freq), _ptr(pos), Q.data_ptr(), K.data_ptr(), st), "pisa_qk_norm_rope")
+    qs, ks = (s.batch, s.heads_q, s.tokens, s.head_dim), (s.batch, s.heads_kv, s.tokens, s.head_dim)
+    Q = Xq.new_empty(qs) if Q is None else _like(Q, torch.bfloat16, qs, "Q")
+    K = Xq.new_empty(ks) if K is None else _like(K, torch.bfloat16, ks, "K")
+    _launch("pisa_qk_norm_rope", _lib.pisa_qk_norm_rope, stream,
+            ((Xq, "Xq"), (Xk, "Xk"), (pos, "pos"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"), (Q, "Q"), (K, "K")),
+            (s.c(sq, sk), Xq.data_ptr(), Xk.data_ptr(), _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(pos), Q.data_ptr(),
+             K.data_ptr()))
     return Q, K
 
 
@@ -593,22 +611,20 @@ def qk_norm_rope_backward(shape: NormRopeShape, Xq, Xk, pos, inv_freq, dQ, dK, w
     sq, sk = _norm_rope_args(s, Xq, Xk, pos, inv_freq, wq, wk)
     _like(dQ, torch.bfloat16, (B, s.heads_q, T, D), "dQ")
     _like(dK, torch.bfloat16, (B, s.heads_kv, T, D), "dK")
-    dev = Xq.device
-    if dXq is None:
-        dXq = torch.empty((B, T, s.heads_q, D), dtype=torch.bfloat16, device=dev)
-    if dXk is None:
-        dXk = torch.empty((B, T, s.heads_kv, D), dtype=torch.bfloat16, device=dev)
+    dXq = Xq.new_empty((B, T, s.heads_q, D)) if dXq is None else dXq
+    dXk = Xq.new_empty((B, T, s.heads_kv, D)) if dXk is None else dXk
     gq = _rows_like(dXq, torch.bfloat16, (B, T, s.heads_q, D), "dXq")
     gk = _rows_like(dXk, torch.bfloat16, (B, T, s.heads_kv, D), "dXk")
-    dwq = torch.empty(D, dtype=torch.float32, device=dev) if wq is not None else None
-    dwk = torch.empty(D, dtype=torch.float32, device=dev) if wk is not None else None
+    dwq = wq.new_empty(D) if wq is not None else None
+    dwk = wk.new_empty(D) if wk is not None else None
     if ws is None:
-        ws = new_norm_rope_workspace(s, dev)
-    dev, st = _device_of(((Xq, "Xq"), (Xk, "Xk"), (pos, "pos"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"),
-                          (dQ, "dQ"), (dK, "dK"), (dXq, "dXq"), (dXk, "dXk"), (ws, "ws")), stream)
-    _check(_on(dev, _lib.pisa_qk_norm_rope_backward, s.c(sq, sk, gq, gk), Xq.data_ptr(), Xk.data_ptr(), _ptr(wq),
-               _ptr(wk), _ptr(inv_freq), _ptr(pos), dQ.data_ptr(), dK.data_ptr(), dXq.data_ptr(), dXk.data_ptr(),
-               _ptr(dwq), _ptr(dwk), ws.data_ptr(), ws.numel() * ws.element_size(), st), "pisa_qk_norm_rope_backward")
+        ws = new_norm_rope_workspace(s, Xq.device)
+    _launch("pisa_qk_norm_rope_backward", _lib.pisa_qk_norm_rope_backward, stream,
+            ((Xq, "Xq"), (Xk, "Xk"), (pos, "pos"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"), (dQ, "dQ"),
+             (dK, "dK"), (dXq, "dXq"), (dXk, "dXk"), (ws, "ws")),
+            (s.c(sq, sk, gq, gk), Xq.data_ptr(), Xk.data_ptr(), _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(pos),
+             dQ.data_ptr(), dK.data_ptr(), dXq.data_ptr(), dXk.data_ptr(), _ptr(dwq), _ptr(dwk), ws.data_ptr(),
+             ws.numel() * ws.element_size()))
     return dXq, dXk, dwq, dwk
 
 
@@ -650,8 +666,10 @@ class Cache:
         self.shape, self.k, self.v, self.k_exp, self.v_exp = s, k, v, k_exp, v_exp
         self.device = k.device
         self._c = s.c()
-        self._named = ((k, "k"), (v, "v"), (k_exp, "k_exp"), (v_exp, "v_exp"))
-        _device_of(self._named, None) if k.is_cuda else None
+        self._ptrs = tuple(_ptr(t) for t in (k, v, k_exp, v_exp))
+        for t, name in ((v, "v"), (k_exp, "k_exp"), (v_exp, "v_exp")):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{name} must be on {k.device}, got {t.device}")
 
     def _both(self):
         if self.v is None:
@@ -694,10 +712,10 @@ def cache_write(cache: Cache, K, V, ws, start=None, count=None, stream=None) -> 
     sk, sv = _rows_like(K, torch.bfloat16, rows, "K"), _rows_like(V, torch.bfloat16, rows, "V")
     _ranges(s.batch, start, count)
     _status_word(ws)
-    dev, st = _device_of(((cache.k, "cache"), (K, "K"), (V, "V"), (start, "start"), (count, "count"), (ws, "ws")), stream)
-    _check(_on(dev, _lib.pisa_cache_write, cache._c, rows[2], K.data_ptr(), V.data_ptr(), sk, sv, _ptr(start),
-               _ptr(count), cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_exp), _ptr(cache.v_exp),
-               ws.data_ptr(), st), "pisa_cache_write")
+    _launch("pisa_cache_write", _lib.pisa_cache_write, stream,
+            ((cache.k, "cache"), (K, "K"), (V, "V"), (start, "start"), (count, "count"), (ws, "ws")),
+            (cache._c, rows[2], K.data_ptr(), V.data_ptr(), _i64x3(*sk), _i64x3(*sv), _ptr(start), _ptr(count),
+             *cache._ptrs, ws.data_ptr()))
 
 
 def cache_read(cache: Cache, tokens: int, ws, start=None, count=None, K=None, V=None, stream=None):
@@ -713,10 +731,9 @@ def cache_read(cache: Cache, tokens: int, ws, start=None, count=None, K=None, V=
     V = make(rows, dtype=torch.bfloat16, device=cache.device) if V is None else _like(V, torch.bfloat16, rows, "V")
     _ranges(s.batch, start, count)
     _status_word(ws)
-    dev, st = _device_of(((cache.k, "cache"), (K, "K"), (V, "V"), (start, "start"), (count, "count"), (ws, "ws")), stream)
-    _check(_on(dev, _lib.pisa_cache_read, cache._c, rows[2], cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_exp),
-               _ptr(cache.v_exp), _ptr(start), _ptr(count), K.data_ptr(), V.data_ptr(), ws.data_ptr(), st),
-           "pisa_cache_read")
+    _launch("pisa_cache_read", _lib.pisa_cache_read, stream,
+            ((cache.k, "cache"), (K, "K"), (V, "V"), (start, "start"), (count, "count"), (ws, "ws")),
+            (cache._c, rows[2], *cache._ptrs, _ptr(start), _ptr(count), K.data_ptr(), V.data_ptr(), ws.data_ptr()))
     return K, V
 
 
@@ -730,9 +747,9 @@ def cache_append_pyramid(shape: Shape, cache: Cache, pyramid, seq_kv_old: int, s
     if (s.batch, s.heads_kv, s.capacity, s.head_dim) != (shape.batch, shape.heads_kv, shape.kv_rows, shape.head_dim):
         raise ValueError("the shape's batch, heads_kv, capacity and head_dim must be the cache's")
     _like(pyramid, torch.float32, (s.batch, s.heads_kv, shape.n_nodes, s.head_dim), "pyramid")
-    dev, st = _device_of(((cache.k, "cache"), (pyramid, "pyramid")), stream)
-    _check(_on(dev, _lib.pisa_cache_append_pyramid, shape.c(), cache.k.data_ptr(), cache.k_exp.data_ptr(),
-               pyramid.data_ptr(), int(seq_kv_old), st), "pisa_cache_append_pyramid")
+    _launch("pisa_cache_append_pyramid", _lib.pisa_cache_append_pyramid, stream,
+            ((cache.k, "cache"), (pyramid, "pyramid")),
+            (shape.c(), cache._ptrs[0], cache._ptrs[2], pyramid.data_ptr(), int(seq_kv_old)))
     return pyramid
 
 
@@ -752,6 +769,7 @@ class TreeShape:
     select_per_qhead: int = 0
     scale: float = 0.0
 
+    @functools.lru_cache(maxsize=256)
     def c(self) -> PisaTreeShape:
         return PisaTreeShape(self.batch, self.heads_q, self.heads_kv, self.drafts, self.capacity, self.head_dim,
                              int(self.format), self.block, self.seq_kv, self.topk, int(self.select_per_qhead),
@@ -796,20 +814,19 @@ def tree_attention(shape: TreeShape, cache: Cache, Q, K, V, mask, cache_len, ws,
         raise ValueError("idx goes with topk > 0")
     if idx is not None:
         _like(idx, torch.int32, (B, s.hsel, 1, s.topk), "idx")
-    O = torch.empty((B, Hq, T, D), dtype=torch.bfloat16, device=Q.device) if O is None \
-        else _like(O, torch.bfloat16, (B, Hq, T, D), "O")
+    O = Q.new_empty((B, Hq, T, D)) if O is None else _like(O, torch.bfloat16, (B, Hq, T, D), "O")
     if lse is True:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=Q.device)
+        lse = Q.new_empty((B, Hq, T), dtype=torch.float32)
     elif lse is False:
         lse = None
     elif lse is not None:
         _like(lse, torch.float32, (B, Hq, T), "lse")
     _status_word(ws)
-    dev, st = _device_of(((Q, "Q"), (K, "K"), (V, "V"), (mask, "mask"), (cache_len, "cache_len"), (cache.k, "cache"),
-                          (idx, "idx"), (O, "O"), (lse, "lse"), (ws, "ws")), stream)
-    _check(_on(dev, _lib.pisa_tree_attention, s.c(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), mask.data_ptr(),
-               cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_exp), _ptr(cache.v_exp), cache_len.data_ptr(),
-               _ptr(idx), O.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), st), "pisa_tree_attention")
+    _launch("pisa_tree_attention", _lib.pisa_tree_attention, stream,
+            ((Q, "Q"), (K, "K"), (V, "V"), (mask, "mask"), (cache_len, "cache_len"), (cache.k, "cache"), (idx, "idx"),
+             (O, "O"), (lse, "lse"), (ws, "ws")),
+            (s.c(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), mask.data_ptr(), *cache._ptrs, cache_len.data_ptr(),
+             _ptr(idx), O.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel()))
     return O, lse
 
 

@@ -165,46 +165,49 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CachePa
 }
 
 // Level-0 mean of one key block by one warp: D/16 lanes hold a row (16 bytes each), so a load
-// instruction covers 32 / (D/16) rows; the warp's loads of a 64-key block are all in flight
-// together. Lane l holds the exponents of keys l and l + 32 of every run of 64 and hands them round
-// by shuffles. Every caller sums in this order, so appends equal builds bit for bit.
+// instruction covers 32 / (D/16) rows; the loads of 32 keys are in flight together. Lane l holds the
+// exponent of key l of every run of 32 and hands it round by shuffles. Every caller sums in this
+// order, so appends equal builds bit for bit.
 template <int D>
 __device__ __forceinline__ void e4m3_block_mean(const uint8_t* K, const uint8_t* e, int blk, float* out) {
-    constexpr int LPR = D / 16, RPI = 32 / LPR, N = 64 / RPI;
+    constexpr int LPR = D / 16, RPI = 32 / LPR, N = 32 / RPI;
     const int lane = threadIdx.x & 31, chunk = lane % LPR, rsub = lane / LPR;
-    float acc[16];
+    uint64_t acc[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-    for (int r0 = 0; r0 < blk; r0 += 64) {
+    for (int k = 0; k < 8; ++k) acc[k] = 0ull;
+    const uint8_t* row = K + rsub * D + 16 * chunk;
+#pragma unroll 2
+    for (int r0 = 0; r0 < blk; r0 += 32) {
         uint4 v[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] = __ldg(reinterpret_cast<const uint4*>(K + static_cast<int64_t>(r0 + i * RPI + rsub) * D) + chunk);
-        const uint32_t e0 = __ldg(e + r0 + lane), e1 = __ldg(e + r0 + 32 + lane);
+        for (int i = 0; i < N; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(row + (r0 + i * RPI) * D));
+        const uint32_t ex = __ldg(e + r0 + lane);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int row = i * RPI + rsub;
-            const float f = exp_value(__shfl_sync(0xFFFFFFFFu, i * RPI < 32 ? e0 : e1, row & 31));
+            const float f = exp_value(__shfl_sync(0xFFFFFFFFu, ex, i * RPI + rsub));
+            const uint64_t f2 = f2_pack(f, f);
             const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float2 x = e4m3x2_values((w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
-                acc[2 * k] = fmaf(x.x, f, acc[2 * k]);
-                acc[2 * k + 1] = fmaf(x.y, f, acc[2 * k + 1]);
+                const float2 x = e4m3x2_values((k & 1) ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu);
+                asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[k]) : "l"(f2_pack(x.x, x.y)), "l"(f2));
             }
         }
     }
+    float a[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f2_unpack(acc[k], a[2 * k], a[2 * k + 1]);
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) acc[k] += __shfl_xor_sync(0xFFFFFFFFu, acc[k], o);
+        for (int k = 0; k < 16; ++k) a[k] += __shfl_xor_sync(0xFFFFFFFFu, a[k], o);
     }
     if (rsub == 0) {
         const float inv = 1.0f / static_cast<float>(blk);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            reinterpret_cast<float4*>(out + 16 * chunk)[k] = make_float4(acc[4 * k] * inv, acc[4 * k + 1] * inv,
-                                                                         acc[4 * k + 2] * inv, acc[4 * k + 3] * inv);
+            reinterpret_cast<float4*>(out + 16 * chunk)[k] =
+                make_float4(a[4 * k] * inv, a[4 * k + 1] * inv, a[4 * k + 2] * inv, a[4 * k + 3] * inv);
     }
 }
 
@@ -213,7 +216,7 @@ __device__ __forceinline__ void e4m3_block_mean(const uint8_t* K, const uint8_t*
 // shared memory; nodes over older blocks alone come out as they were. Grid: planes x the subtrees
 // that hold a new block.
 template <int D>
-__global__ void __launch_bounds__(256) cache_subtree_kernel(const CachePyramidParams p, int S, int m, int sub_lo,
+__global__ void __launch_bounds__(256, 4) cache_subtree_kernel(const CachePyramidParams p, int S, int m, int sub_lo,
                                                             int subtrees) {
     extern __shared__ __align__(16) float rows[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

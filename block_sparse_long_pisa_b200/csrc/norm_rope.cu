@@ -12,7 +12,7 @@
 //     dims: the raw bf16 words are exchanged (four shuffles), not the products.
 //   * A group of lanes keeps one token and walks heads, so cos and sin stay in registers, folded
 //     into the weights (y = r (x a + x_mate b) with a = w cos, b = -+ w_mate sin): one token's angles
-//     are formed once per block and not once per head. The angle is pos * inv_freq in fp64, taken
+//     are formed once, four per lane, and not once per head. The angle is pos * inv_freq in fp64, taken
 //     modulo one turn before it is rounded to fp32: a far position keeps its phase (an fp32 product
 //     is off by 2^-24 of an angle of 10^6, 0.06 rad).
 //   * A tile is as many tokens as a block has lane groups: the tile's stores of one head are one
@@ -96,29 +96,48 @@ struct LaneMap {
     }
 };
 
-template <int D>
-__device__ __forceinline__ void load_turn(const float2* tab, const LaneMap<D>& lm, int R, bool inter, Turn& t) {
+// cos and sin of a lane's dims at position pos. A lane forms four angles; with half pairs its mate
+// needs the same eight and forms the other four.
+template <int D, bool INTER>
+__device__ __forceinline__ void form_turn(const NormRopeParams& p, const LaneMap<D>& lm, int64_t tok, Turn& t) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         t.c[k] = 1.f;
         t.s[k] = 0.f;
     }
-    if (!lm.turns) return;
-    if (inter) {
+    if (p.R == 0) return;
+    const int i0 = INTER ? 4 * lm.lane8 : 8 * lm.lane8 - (lm.second ? p.R / 2 - 4 : 0);
+    float c[4], s[4];
+    if (lm.turns) {
+        const double pos = static_cast<double>(__ldg(p.pos + tok));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float2 cs = tab[4 * lm.lane8 + k];
-            t.c[2 * k] = t.c[2 * k + 1] = cs.x;
-            t.s[2 * k] = -cs.y;
-            t.s[2 * k + 1] = cs.y;
+            const double turns = pos * static_cast<double>(__ldg(p.inv_freq + i0 + k)) * 0.15915494309189533577;
+            sincospif(2.f * static_cast<float>(turns - rint(turns)), &s[k], &c[k]);
         }
     } else {
-        const int i0 = 8 * lm.lane8 - (lm.second ? R / 2 : 0);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float2 cs = tab[i0 + k];
-            t.c[k] = cs.x;
-            t.s[k] = lm.second ? cs.y : -cs.y;
+        for (int k = 0; k < 4; ++k) c[k] = s[k] = 0.f;
+    }
+    if constexpr (INTER) {
+        if (lm.turns) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                t.c[2 * k] = t.c[2 * k + 1] = c[k];
+                t.s[2 * k] = -s[k];
+                t.s[2 * k + 1] = s[k];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float oc = __shfl_sync(0xFFFFFFFFu, c[k], lm.mate), os = __shfl_sync(0xFFFFFFFFu, s[k], lm.mate);
+            if (lm.turns) {  // the first lane of the two formed the lower four
+                t.c[k] = lm.second ? oc : c[k];
+                t.c[4 + k] = lm.second ? c[k] : oc;
+                t.s[k] = lm.second ? os : -s[k];
+                t.s[4 + k] = lm.second ? s[k] : -os;
+            }
         }
     }
 }
@@ -138,24 +157,8 @@ __device__ __forceinline__ void mate_values(const uint4& v, const uint64_t (&own
     }
 }
 
-// cos and sin of the tile's tokens: tab[token in tile][i], i < R/2.
-__device__ __forceinline__ void fill_table(const NormRopeParams& p, int64_t tok0, int ntok, float2* tab) {
-    const int half = p.R / 2;
-    for (int e = threadIdx.x; e < ntok * half; e += kNrThreads) {
-        const int tt = e / half, i = e % half;
-        if (tok0 + tt >= p.ntokens) break;
-        const double turns = static_cast<double>(p.pos[tok0 + tt]) * static_cast<double>(p.inv_freq[i]) *
-                             0.15915494309189533577;
-        const float frac = static_cast<float>(turns - rint(turns));
-        float s, c;
-        sincospif(2.f * frac, &s, &c);
-        tab[tt * half + i] = make_float2(c, s);
-    }
-}
-
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRopeParams p) {
-    extern __shared__ __align__(16) float2 tab[];
     constexpr int LPR = D / 8;
     constexpr int G = kNrThreads / LPR;  // lane groups of the block
     constexpr int U = 4;                 // rows in flight per group
@@ -192,10 +195,8 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRope
     };
     const bool has_q = h0 < p.Hq;
     begin(!has_q);  // before the angles are formed
-    fill_table(p, tok0, p.tb, tab);
-    __syncthreads();
     Turn tn;
-    load_turn<D>(tab + (live ? tt : 0) * (p.R / 2), lm, p.R, INTER, tn);
+    form_turn<D, INTER>(p, lm, tok, tn);
     for (int side = has_q ? 0 : 1; side < 2; ++side) {
         if (side == 1 && has_q) {
             if (h1 <= p.Hq) break;
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRope
         for (int i = 0; i < todo; i += U) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if (i + u >= todo) break;
                 const bool ok = i + u < n;
                 if (!ok) v[u] = make_uint4(0u, 0u, 0u, 0u);
                 uint64_t x[4], m[4];
@@ -250,7 +252,6 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRope
 // key tiles, so a thread has one side's weights and sums.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_backward_kernel(const NormRopeParams p) {
-    extern __shared__ __align__(16) float2 tab[];
     __shared__ float red[kNrThreads * 8];
     constexpr int LPR = D / 8;
     constexpr int G = kNrThreads / LPR;
@@ -274,7 +275,6 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_backward_kernel(const
     }
     const int first = static_cast<int>(blockIdx.x) - (is_k ? p.qblocks : 0);
     const int step = is_k ? static_cast<int>(gridDim.x) - p.qblocks : p.qblocks;
-    int64_t table_of = -1;
     for (int64_t tile = first; tile < tiles; tile += step) {
         const int64_t tok0 = (tile / hsplits) * p.tb;
         const bool live = tok0 + tt < p.ntokens;
@@ -297,17 +297,12 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_backward_kernel(const
             xs += sstep;
             gs += gstep;
         }
-        if (tok0 != table_of) {
-            __syncthreads();  // the previous tile's table has been read
-            fill_table(p, tok0, p.tb, tab);
-            __syncthreads();
-            table_of = tok0;
-        }
         Turn tn;
-        load_turn<D>(tab + (live ? tt : 0) * (p.R / 2), lm, p.R, INTER, tn);
+        form_turn<D, INTER>(p, lm, tok, tn);
         for (int i = 0; i < todo; i += U) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if (i + u >= todo) break;
                 const bool ok = i + u < n;
                 if (!ok) xv[u] = gv[u] = make_uint4(0u, 0u, 0u, 0u);
                 uint64_t x[4], g[4], m[4];
@@ -374,7 +369,8 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, i
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), ty = threadIdx.x >> 5;
     const int lo = blockIdx.y == 0 ? 0 : qblocks, hi = blockIdx.y == 0 ? qblocks : blocks;
     float s = 0.f;
-    for (int i = lo + ty; i < hi; i += 32) s += part[static_cast<int64_t>(i) * D + col];
+#pragma unroll 8
+    for (int i = lo + ty; i < hi; i += 32) s += __ldcg(part + static_cast<int64_t>(i) * D + col);
     red[ty][threadIdx.x & 31] = s;
     __syncthreads();
     if (ty == 0) {
@@ -387,14 +383,15 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, i
 }
 
 // Tokens per tile and heads per tile: full tiles (one token per lane group, all heads) unless that
-// leaves SMs idle; then fewer tokens, then fewer heads, down to one row per lane group.
+// gives fewer than two blocks per SM; then fewer tokens, then fewer heads, down to one row per lane
+// group.
 static int64_t norm_rope_tiles(NormRopeParams* p, int D, int H) {
     const int G = kNrThreads / (D / 8);
     p->tb = G;
     p->hb = H;
     while (true) {
         const int64_t blocks = (p->ntokens + p->tb - 1) / p->tb * ((H + p->hb - 1) / p->hb);
-        if (blocks >= kNormRopeBlocks) return blocks;
+        if (blocks >= kNormRopeBlocks / 2) return blocks;
         if (p->tb > 1)
             p->tb /= 2;
         else if (p->hb > G)
@@ -409,17 +406,16 @@ bool launch_norm_rope(NormRopeParams p, int D, bool inter, cudaStream_t st) {
     const int64_t bx = (p.ntokens + p.tb - 1) / p.tb;
     if (bx > INT32_MAX) return false;
     const dim3 grid(static_cast<unsigned>(bx), (p.Hq + p.Hkv + p.hb - 1) / p.hb);
-    const size_t smem = static_cast<size_t>(p.tb) * (p.R / 2) * sizeof(float2);
     if (D == 64) {
         if (inter)
-            norm_rope_kernel<64, true><<<grid, kNrThreads, smem, st>>>(p);
+            norm_rope_kernel<64, true><<<grid, kNrThreads, 0, st>>>(p);
         else
-            norm_rope_kernel<64, false><<<grid, kNrThreads, smem, st>>>(p);
+            norm_rope_kernel<64, false><<<grid, kNrThreads, 0, st>>>(p);
     } else {
         if (inter)
-            norm_rope_kernel<128, true><<<grid, kNrThreads, smem, st>>>(p);
+            norm_rope_kernel<128, true><<<grid, kNrThreads, 0, st>>>(p);
         else
-            norm_rope_kernel<128, false><<<grid, kNrThreads, smem, st>>>(p);
+            norm_rope_kernel<128, false><<<grid, kNrThreads, 0, st>>>(p);
     }
     return cudaGetLastError() == cudaSuccess;
 }
@@ -442,17 +438,16 @@ bool launch_norm_rope_backward(NormRopeParams p, int D, bool inter, float* dwq, 
     if (kb > ktiles) kb = ktiles;
     p.qblocks = static_cast<int>(qb);
     const int grid = static_cast<int>(qb + kb);
-    const size_t smem = static_cast<size_t>(p.tb) * (p.R / 2) * sizeof(float2);
     if (D == 64) {
         if (inter)
-            norm_rope_backward_kernel<64, true><<<grid, kNrThreads, smem, st>>>(p);
+            norm_rope_backward_kernel<64, true><<<grid, kNrThreads, 0, st>>>(p);
         else
-            norm_rope_backward_kernel<64, false><<<grid, kNrThreads, smem, st>>>(p);
+            norm_rope_backward_kernel<64, false><<<grid, kNrThreads, 0, st>>>(p);
     } else {
         if (inter)
-            norm_rope_backward_kernel<128, true><<<grid, kNrThreads, smem, st>>>(p);
+            norm_rope_backward_kernel<128, true><<<grid, kNrThreads, 0, st>>>(p);
         else
-            norm_rope_backward_kernel<128, false><<<grid, kNrThreads, smem, st>>>(p);
+            norm_rope_backward_kernel<128, false><<<grid, kNrThreads, 0, st>>>(p);
     }
     if (cudaGetLastError() != cudaSuccess) return false;
     ++*launches;

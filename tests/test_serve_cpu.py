@@ -25,7 +25,7 @@ def nr(**kw):
     d = 64
     st = dict(xq=(3 * 4 * d, 4 * d, d), xk=(3 * 2 * d, 2 * d, d), dxq=(3 * 4 * d, 4 * d, d), dxk=(3 * 2 * d, 2 * d, d))
     st.update(strides)
-    return pisa.NormRopeShape(**a).c(*[(ctypes.c_int64 * 3)(*st[k]) for k in ("xq", "xk", "dxq", "dxk")])
+    return pisa.NormRopeShape(**a).c(*[st[k] for k in ("xq", "xk", "dxq", "dxk")])
 
 
 @pytest.mark.parametrize("bad, code", [
