@@ -48,81 +48,13 @@
 #include <cuda_fp16.h>
 
 #include "pisa_device.cuh"
+#include "pisa_tree.cuh"
 
 namespace pisa {
 
-constexpr uint32_t kTreeDetail = kKernTree << 8;
-constexpr int kTreeUMin = -100;  // smallest unit exponent of O (e4m3)
 constexpr int kTreeMaxSlots = 4;  // of the K ring and of the V ring
 constexpr int kTreeMeta = 8;      // entries (tiles and piece ends) whose description is kept
 enum : int { kTileEnd = 0, kTileCache = 1, kTileDraft = 2 };
-
-// ---------------------------------------------------------------- the runs
-
-// Units of one row tile of sequence b: the cache's, then one for the drafted tokens.
-__device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
-    return min(max(p.len[b], 0), p.cap);
-}
-__device__ __forceinline__ int tree_units(const TreeParams& p, int len) {
-    return p.topk > 0 ? 1 + p.topk * p.upb + (max(len - p.seq, 0) + 63) / 64 : 1 + (len + 63) / 64;
-}
-
-// The whole job and one position in it, formed by one warp.
-struct TreeJob {
-    int64_t total;   // units of all row tiles
-    int64_t runs;    // runs that hold any (equal to the grid unless there are fewer units)
-    __device__ __forceinline__ int64_t begin(int64_t c) const { return total * c / runs; }
-    // run that holds unit x
-    __device__ __forceinline__ int64_t run_of(int64_t x) const {
-        int64_t c = x * runs / total;
-        while (c + 1 < runs && begin(c + 1) <= x) ++c;
-        while (begin(c) > x) --c;
-        return c;
-    }
-};
-
-__device__ __forceinline__ TreeJob tree_job(const TreeParams& p) {
-    const int lane = threadIdx.x & 31;
-    int64_t sum = 0;
-    for (int b = lane; b < p.B; b += 32) sum += tree_units(p, tree_len(p, b));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    TreeJob j;
-    j.total = sum * p.rows_per_seq;
-    j.runs = min(static_cast<int64_t>(p.runs), (j.total + p.min_units - 1) / p.min_units);
-    return j;
-}
-
-// Row tile and unit at position x (whole warp).
-__device__ __forceinline__ void tree_find(const TreeParams& p, int64_t x, int64_t& tile, int& unit) {
-    const int lane = threadIdx.x & 31;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        const int u = b < p.B ? tree_units(p, tree_len(p, b)) : 0;
-        const int64_t mine = static_cast<int64_t>(u) * p.rows_per_seq;
-        int64_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        upto += before;
-        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, b < p.B && x < upto);
-        if (hit != 0) {
-            const int l = __ffs(hit) - 1;
-            const int64_t start = __shfl_sync(0xFFFFFFFFu, upto - mine, l);
-            const int ul = __shfl_sync(0xFFFFFFFFu, u, l);
-            const int64_t rel = x - start;
-            tile = static_cast<int64_t>(b0 + l) * p.rows_per_seq + rel / ul;
-            unit = static_cast<int>(rel % ul);
-            return;
-        }
-        before = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    }
-    tile = static_cast<int64_t>(p.B) * p.rows_per_seq;
-    unit = 0;
-}
 
 // ---------------------------------------------------------------- operands
 
@@ -148,17 +80,9 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a, uint64_t 
         : "memory");
 }
 
-__device__ __forceinline__ float pow2i(int e) {  // e in [-126, 127]
-    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
 __device__ __forceinline__ float warp_max(float x) {
     float r;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
@@ -1161,16 +1085,33 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
 
 // ---------------------------------------------------------------- host side
 
-// Rows of one row tile for a selection row of `rows` rows: the smallest of 16, 32, 64 and 96 that holds
-// them, or, past 96 rows, of 64 and 96 the one that pads less (96 on a tie).
+// Rows of one row tile for a selection row of `rows` rows: 8 or 16 (attn_tree_few.cu), else the smallest of
+// 32, 64 and 96 that holds them, or, past 96 rows, of 64 and 96 the one that pads less (96 on a tie).
 int tree_row_tile(int rows) {
-    for (int r : {16, 32, 64, 96})
+    for (int r : {8, 16, 32, 64, 96})
         if (rows <= r) return r;
     return (rows + 63) / 64 * 64 < (rows + 95) / 96 * 96 ? 64 : 96;
 }
 
 // CTAs on one SM: two where the shared memory of both fits.
-int tree_ctas_per_sm(int rm, bool e4m3) { return e4m3 && rm <= 32 ? 2 : 1; }
+int tree_ctas_per_sm(int rm, bool e4m3) { return rm <= 16 || (e4m3 && rm <= 32) ? 2 : 1; }
+
+bool launch_tree_merge(const TreeParams& p, int D, int rm, cudaStream_t st, int32_t* launches) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.rows_per_seq, rm / 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = D == 64 ? cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<64>, p, rm)
+                                  : cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<128>, p, rm);
+    if (e != cudaSuccess) return false;
+    ++*launches;
+    return true;
+}
 
 template <int D, bool E4M3, int R>
 static bool launch_tree(TreeParams p, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dk,
@@ -1188,25 +1129,13 @@ static bool launch_tree(TreeParams p, const CUtensorMap& k, const CUtensorMap& v
     attn_tree_kernel<D, E4M3, R><<<p.runs, C::THREADS, smem, st>>>(k, v, dk, dv, p);
     if (cudaGetLastError() != cudaSuccess) return false;
     ++*launches;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.rows_per_seq, R / 4);
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<D>, p, R) != cudaSuccess) return false;
-    ++*launches;
-    return true;
+    return launch_tree_merge(p, D, R, st, launches);
 }
 
 template <int D, bool E4M3>
 static bool launch_tree_rows(const TreeParams& p, int rm, const CUtensorMap& k, const CUtensorMap& v,
                              const CUtensorMap& dk, const CUtensorMap& dv, cudaStream_t st, int32_t* launches) {
     switch (rm) {
-        case 16: return launch_tree<D, E4M3, 16>(p, k, v, dk, dv, st, launches);
         case 32: return launch_tree<D, E4M3, 32>(p, k, v, dk, dv, st, launches);
         case 64: return launch_tree<D, E4M3, 64>(p, k, v, dk, dv, st, launches);
         default: return launch_tree<D, E4M3, 96>(p, k, v, dk, dv, st, launches);
@@ -1217,6 +1146,7 @@ bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, con
                       cudaStream_t st, int32_t* launches) {
     const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv * p.cap, drows = static_cast<int64_t>(p.B) * p.Hkv * p.T;
     CUtensorMap k, v, dk, dv;
+    if (rm <= 16) return launch_attn_tree_few(p, D, e4m3, rm, K, Kc, Vc, st, launches);
     if (!make_tmap_2d(&dk, K, drows, D, p.tp) || !make_tmap_2d(&dv, p.DV, drows, D, p.tp)) return false;
     if (e4m3) {
         if (!make_tmap_2d_u8(&k, Kc, rows, D, 64) || !make_tmap_2d_u8(&v, Vc, rows, D, 64)) return false;

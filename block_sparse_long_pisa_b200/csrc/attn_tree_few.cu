@@ -1,0 +1,756 @@
+// Tree attention for few rows: at most 16 drafted-token-and-head rows per selection row (one token of a
+// group of four or eight heads is 4 or 8). The function, the cut into runs and the treatment of the
+// drafted tokens are those of attn_tree.cu; here nothing but the bytes of the cache should count.
+//
+// Bound: the bytes of the cache, each read once. One warp takes 16 keys of every unit of 64 on its own,
+// with mma.sync m16n8k16: no barrier between warps, four copies of the softmax state per CTA that
+// meet when a piece ends. (On tcgen05 the same step is a chain of hand-overs per tile, S, softmax, P, O,
+// which few rows cannot fill: 160 to 185 us against 144 us for a first form of this kernel with the
+// rows on the M side, for one token over 64 caches of 128K rows, 64 selected 8-bit blocks.)
+//
+// Keys and dims on the M side. S^T = K Q^T (16 keys x 16 dims x 8 rows a product) and O^T = V^T P^T
+// (16 dims x 16 keys x 8 rows): rows are the N side, 8 to a tile, so a group of four heads wastes half a
+// tile and not three quarters, and a softmax thread has two rows and two keys. P^T goes from the
+// accumulators of S^T to an operand of O^T by two 8 x 8 register transposes.
+//
+// e4m3 rows become fp16 in registers, two values an instruction:
+//   * Q is scaled by a power of two per row to a maximum in [2^14, 2^15) and rounded to fp16, which
+//     keeps bf16's 8 bits for values down to 2^-29 of the row's largest.
+//   * K's row exponent and Q's come back as an exact factor of the score, in fp32.
+//   * V's row exponent goes into P: P' = p 2^(e - 127 - u), u the largest V exponent so far less 7, O in
+//     units of 2^u. P <= 2^8, so P' <= 2^15 fits fp16; it keeps 11 bits down to 2^-21 of the largest
+//     row times the largest p, and a floor of 2^-31 below.
+//   * ldmatrix hands out byte pairs: in Q K^T the dims of a 16-dim chunk take the order that the bytes
+//     come in (any order does), in V^T P^T the even dims of a chunk are rows 0-7 of the product and the
+//     odd ones rows 8-15.
+// A bf16 cache takes P as bf16 (range of V); so do the drafted tokens.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "pisa_device.cuh"
+#include "pisa_tree.cuh"
+
+namespace pisa {
+
+constexpr float kFewLazy = 8.0f;    // log2 units a score may exceed the kept maximum by
+constexpr int kFewStages = 8;       // most stages of the ring
+constexpr int kFewThreads = 160;    // four consumer warps and the producer
+
+__device__ __forceinline__ void few_ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void few_ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t few_transpose(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+template <bool F16>
+__device__ __forceinline__ void few_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// two e4m3 values (of the low, the high half of a register) -> two fp16
+__device__ __forceinline__ uint32_t few_f16(uint32_t two) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(two));
+    return h;
+}
+__device__ __forceinline__ uint32_t few_f16_hi(uint32_t two) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(h) : "r"(two));
+    return h;
+}
+// byte offset of 16-byte chunk `c` of row `row` in a tile of 128-byte (64-byte) swizzled rows
+__device__ __forceinline__ uint32_t few_at128(int row, int c) {
+    return static_cast<uint32_t>(row * 128 + ((c ^ (row & 7)) << 4));
+}
+template <int D>
+__device__ __forceinline__ uint32_t few_at_e4m3(int row, int c) {
+    return D == 128 ? few_at128(row, c) : static_cast<uint32_t>(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+}
+
+template <int D, bool E4M3, int NT>
+struct FewCfg {
+    static constexpr int ROW = E4M3 ? D : 2 * D;
+    static constexpr int TILE = 64 * ROW;                // K (or V) of one unit
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int EXPS = E4M3 ? 128 : 0;          // exponent bytes of K and of V
+    static constexpr int DRAFT = 16 * 2 * D;             // drafted K (or V), 16 rows
+    static constexpr int RM = 8 * NT;
+    static constexpr int CH = 32 / NT;                   // dims that meet at a time when a piece ends
+    static constexpr int FIXED = 1024 + 2 * DRAFT + 4 * RM * (CH + 2) * 4;
+};
+
+// One warp's state: for its rows 2 (lane % 4), + 1 of every row tile of 8 the kept maximum (log2 units)
+// and the sum over its keys; O^T: tile j is dims 16 j + lane / 4 (+ 8) (e4m3: 16 j + 2 (lane / 4), + 1);
+// the unit exponent of O.
+template <int D, int NT>
+struct FewState {
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+    int u;
+    bool unit_set;
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void few_scale(FewState<D, NT>& s, const float (&a)[NT][2]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            s.o[t][j][0] *= a[t][0];
+            s.o[t][j][1] *= a[t][1];
+            s.o[t][j][2] *= a[t][0];
+            s.o[t][j][3] *= a[t][1];
+        }
+    }
+}
+
+// Scores of 16 keys (log2 units, -inf where masked; [0], [1]: this thread's first key, [2], [3]: its second)
+// -> probabilities against the kept maxima, which move when a score exceeds one by kFewLazy.
+template <int D, int NT>
+__device__ __forceinline__ void few_softmax(FewState<D, NT>& s, float (&x)[NT][4]) {
+    bool over = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        over = over || fmaxf(x[t][0], x[t][2]) > s.m[t][0] + kFewLazy || fmaxf(x[t][1], x[t][3]) > s.m[t][1] + kFewLazy;
+    if (__any_sync(0xFFFFFFFFu, over)) {
+        float a[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float top = fmaxf(x[t][e], x[t][2 + e]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                const float now = fmaxf(s.m[t][e], top);
+                a[t][e] = now == s.m[t][e] ? 1.f : fast_exp2(s.m[t][e] - now);
+                s.m[t][e] = now;
+                s.l[t][e] *= a[t][e];
+            }
+        }
+        few_scale<D, NT>(s, a);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        // a row with no key yet keeps m = -inf: its scores are all -inf and give 0
+        const float r0 = s.m[t][0] == -INFINITY ? 0.f : s.m[t][0], r1 = s.m[t][1] == -INFINITY ? 0.f : s.m[t][1];
+        x[t][0] = fast_exp2(x[t][0] - r0);
+        x[t][1] = fast_exp2(x[t][1] - r1);
+        x[t][2] = fast_exp2(x[t][2] - r0);
+        x[t][3] = fast_exp2(x[t][3] - r1);
+        s.l[t][0] += x[t][0] + x[t][2];
+        s.l[t][1] += x[t][1] + x[t][3];
+    }
+}
+
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    attn_tree_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
+                         const TreeParams p) {
+    using C = FewCfg<D, E4M3, NT>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* dk_s = ring + p.nk * C::STAGE;              // drafted K, then V: [D / 64][16][128 B]
+    float* comb = reinterpret_cast<float*>(dk_s + 2 * C::DRAFT);       // [warp][row][CH]
+    float* cml = comb + 4 * C::RM * C::CH;                             // [warp][row][m, l]
+    uint8_t* exps = reinterpret_cast<uint8_t*>(cml + 4 * C::RM * 2);   // [stage][K 64, V 64]
+    __shared__ __align__(8) uint64_t full[kFewStages], empty[kFewStages], dfull, dempty;
+    __shared__ int meta[kFewStages];   // keys of the stage's tile that count; 0: the piece ends
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const TreeJob job = tree_job(p);
+    if (static_cast<int64_t>(blockIdx.x) >= job.runs) return;
+    int64_t pos = job.begin(blockIdx.x);
+    const int64_t end = job.begin(blockIdx.x + 1);
+    int64_t tile;
+    int unit;
+    tree_find(p, pos, tile, unit);
+    if (tid == 0) {
+        for (int i = 0; i < p.nk; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 4);
+        }
+        mbar_init(&dfull, 1);
+        mbar_init(&dempty, 4);
+        fence_barrier_init();
+    }
+    __syncthreads();
+
+    int s = 0;            // ring stage, and the parity of its current use
+    uint32_t par = 0, dpar = 0;
+    bool ok = true;       // cleared by a wait that ran out: nothing more is waited for
+    auto advance = [&]() {
+        if (++s == p.nk) {
+            s = 0;
+            par ^= 1u;
+        }
+    };
+
+    if (warp == 4) {
+        // ------------------------------------------------ producer
+        int used = 0, drafts = 0;
+        if (lane == 0) {
+            prefetch_tmap(&tmK);
+            prefetch_tmap(&tmV);
+            prefetch_tmap(&tmDK);
+            prefetch_tmap(&tmDV);
+        }
+        while (pos < end && ok) {
+            const int b = static_cast<int>(tile / p.rows_per_seq);
+            const int hs = static_cast<int>(tile % p.rows_per_seq) / p.mt;
+            const int kvh = p.per_qhead ? hs / p.g : hs;
+            const int64_t plane = static_cast<int64_t>(b) * p.Hkv + kvh;
+            const int len = tree_len(p, b);
+            const int units = tree_units(p, len);
+            const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
+            if (tile % p.rows_per_seq == 0 && unit == 0 && lane == 0 && p.len[b] != len)
+                record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB0u);
+            const int32_t* row = p.topk > 0 ? p.idx + (static_cast<int64_t>(b) * p.Hsel + hs) * p.topk : nullptr;
+            const int nsel = p.topk * p.upb;
+            const int uc = min(u1, units - 1);  // the last unit is the drafted tokens
+            for (int u = unit; u < uc && ok; u += 32) {
+                // up to 32 units at a time: position of each unit's first key, -1 = nothing there
+                int at = -1;
+                if (u + lane < uc) {
+                    const int c = u + lane;
+                    if (p.topk == 0) {
+                        at = 64 * c;
+                    } else if (c >= nsel) {
+                        at = p.seq + 64 * (c - nsel);
+                    } else {
+                        const int j = __ldg(row + c / p.upb);
+                        if (j >= p.n0)
+                            record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB1u);
+                        else if (j >= 0)
+                            at = (j * p.upb + c % p.upb) * 64;
+                    }
+                }
+                for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < len); left != 0 && ok; left &= left - 1) {
+                    const int a = __shfl_sync(0xFFFFFFFFu, at, __ffs(left) - 1);
+                    if (lane == 0) {
+                        ok = used < p.nk || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x11u);
+                        if (ok) {
+                            meta[s] = min(64, len - a);
+                            uint8_t* kt = ring + s * C::STAGE;
+                            const int64_t krow = plane * p.cap + a;
+                            const int y = static_cast<int>(krow);
+                            mbar_arrive_expect_tx(&full[s], C::STAGE + C::EXPS);
+                            if constexpr (E4M3) {
+                                tma_load_2d(kt, &tmK, 0, y, &full[s]);
+                                tma_load_2d(kt + C::TILE, &tmV, 0, y, &full[s]);
+                                bulk_load(exps + s * 128, p.k_exp + krow, 64, &full[s]);
+                                bulk_load(exps + s * 128 + 64, p.v_exp + krow, 64, &full[s]);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < D / 64; ++c) {
+                                    tma_load_2d(kt + c * 8192, &tmK, 64 * c, y, &full[s]);
+                                    tma_load_2d(kt + C::TILE + c * 8192, &tmV, 64 * c, y, &full[s]);
+                                }
+                            }
+                        }
+                    }
+                    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                    if (ok) {
+                        ++used;
+                        advance();
+                    }
+                }
+            }
+            if (u1 == units && ok) {  // the drafted tokens, in a buffer of their own
+                if (lane == 0) {
+                    ok = drafts == 0 || mbar_wait(&dempty, dpar ^ 1u, p.status, kTreeDetail | 0x12u);
+                    if (ok) {
+                        mbar_arrive_expect_tx(&dfull, 2 * C::DRAFT);
+                        const int y = static_cast<int>(plane * p.T);
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            tma_load_2d(dk_s + c * 2048, &tmDK, 64 * c, y, &dfull);
+                            tma_load_2d(dk_s + C::DRAFT + c * 2048, &tmDV, 64 * c, y, &dfull);
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                if (ok) {
+                    ++drafts;
+                    dpar ^= 1u;
+                }
+            }
+            if (ok) {  // end of the piece: a slot without a tile
+                if (lane == 0) {
+                    ok = used < p.nk || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x13u);
+                    if (ok) {
+                        meta[s] = 0;
+                        mbar_arrive(&full[s]);
+                    }
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                if (ok) {
+                    ++used;
+                    advance();
+                }
+            }
+            pos += u1 - unit;
+            unit = 0;
+            ++tile;
+        }
+        // every copy lands before the block ends, also when a consumer gave up (earlier uses of a stage
+        // were complete before it was filled again)
+        if (lane == 0) {
+            for (int i = 0; i < p.nk && i < used; ++i) {
+                s = s == 0 ? p.nk - 1 : s - 1;
+                if (s == p.nk - 1) par ^= 1u;
+                if (!mbar_wait(&full[s], par, p.status, kTreeDetail | 0x14u)) break;
+            }
+            if (drafts > 0) mbar_wait(&dfull, dpar ^ 1u, p.status, kTreeDetail | 0x15u);
+        }
+        __syncthreads();
+        return;
+    }
+
+    // ---------------------------------------------------- consumers
+    const int r = lane >> 2, q4 = lane & 3, mi = lane >> 3, mr = lane & 7;
+    const int key0 = 16 * warp;         // this warp's keys of a unit
+    const int rows = p.gh * p.T;
+    while (pos < end) {
+        const int b = static_cast<int>(tile / p.rows_per_seq);
+        const int rem = static_cast<int>(tile % p.rows_per_seq);
+        const int hs = rem / p.mt;      // one row tile per selection row (mt = 1)
+        const int units = tree_units(p, tree_len(p, b));
+        const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
+        const int64_t out0 = (static_cast<int64_t>(b) * p.Hq + hs * p.gh) * p.T;  // first output row
+
+        FewState<D, NT> st;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) st.o[t][j][0] = st.o[t][j][1] = st.o[t][j][2] = st.o[t][j][3] = 0.f;
+            st.m[t][0] = st.m[t][1] = -INFINITY;
+            st.l[t][0] = st.l[t][1] = 0.f;
+        }
+        st.u = 0;
+        st.unit_set = false;
+
+        // Q as the B operand: row 8 t + r; bf16: dims 16 k + 2 q4 (+ 8); e4m3: dims 16 k + 4 q4 .. + 3 as
+        // fp16, scaled; and the score factors of this thread's rows 8 t + 2 q4, + 1
+        uint32_t qf[NT][D / 16][2];
+        float f[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const __nv_bfloat16* q = p.Q + (out0 + 8 * t + r) * D;
+            const bool have = 8 * t + r < rows;
+            if constexpr (E4M3) {
+                uint2 x[D / 16];
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    x[k] = have ? __ldg(reinterpret_cast<const uint2*>(q + 16 * k) + q4) : make_uint2(0u, 0u);
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[k].x << 16)), fabsf(__uint_as_float(x[k].x & 0xFFFF0000u))));
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[k].y << 16)), fabsf(__uint_as_float(x[k].y & 0xFFFF0000u))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                // exponent field of the factor that brings the maximum to [2^14, 2^15)
+                const int e = min(253, 268 - static_cast<int>(__float_as_uint(top) >> 23));
+                const float g = __uint_as_float(static_cast<uint32_t>(e) << 23);
+                const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    qf[t][k][0] = pack_f16x2(__uint_as_float(x[k].x << 16) * g, __uint_as_float(x[k].x & 0xFFFF0000u) * g);
+                    qf[t][k][1] = pack_f16x2(__uint_as_float(x[k].y << 16) * g, __uint_as_float(x[k].y & 0xFFFF0000u) * g);
+                }
+                f[t][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * q4);       // row 2 q4 lives in lanes 8 q4 ..
+                f[t][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * q4 + 4);
+            } else {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t* w = reinterpret_cast<const uint32_t*>(q + 16 * k) + q4;
+                    qf[t][k][0] = have ? __ldg(w) : 0u;
+                    qf[t][k][1] = have ? __ldg(w + 4) : 0u;
+                }
+                f[t][0] = f[t][1] = p.scale_log2;
+            }
+        }
+
+        while (ok) {
+            ok = mbar_wait(&full[s], par, p.status, kTreeDetail | 0x16u);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const int lim = meta[s];
+            if (lim == 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
+                advance();
+                break;
+            }
+            uint8_t* kt = ring + s * C::STAGE;
+            uint8_t* es = exps + s * 128;
+            const uint32_t kb = smem_u32(kt), vb = kb + C::TILE;
+            if (key0 < lim) {
+                if (key0 + 16 > lim) {
+                    // rows past the sequence hold whatever the cache held: V's must not reach the product
+                    // as NaN (0 * NaN), exponents must not set the unit
+                    for (int e = lane; e < 16 * (C::ROW / 16); e += 32) {
+                        const int key = key0 + e / (C::ROW / 16), c = e % (C::ROW / 16);
+                        if (key >= lim) {
+                            const uint32_t o = E4M3 ? few_at_e4m3<D>(key, c) : (c / 8) * 8192 + few_at128(key, c % 8);
+                            *reinterpret_cast<uint4*>(kt + C::TILE + o) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    if (E4M3 && lane < 16 && key0 + lane >= lim) es[key0 + lane] = es[64 + key0 + lane] = 0;
+                    __syncwarp();
+                }
+                float x[NT][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t a[4];  // (keys 0-7, chunk 2c), (keys 8-15, 2c), (keys 0-7, 2c + 1), (keys 8-15, 2c + 1)
+                        few_ldsm4(kb + few_at_e4m3<D>(key0 + mr + 8 * (mi & 1), 2 * c + (mi >> 1)), a);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t a0 = few_f16(a[2 * h]), a2 = few_f16_hi(a[2 * h]);
+                            const uint32_t a1 = few_f16(a[2 * h + 1]), a3 = few_f16_hi(a[2 * h + 1]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                few_mma<true>(x[t], a0, a1, a2, a3, qf[t][2 * c + h][0], qf[t][2 * c + h][1]);
+                        }
+                    }
+                    const float k0 = __uint_as_float(static_cast<uint32_t>(es[key0 + r]) << 23);
+                    const float k1 = __uint_as_float(static_cast<uint32_t>(es[key0 + r + 8]) << 23);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        x[t][0] *= k0 * f[t][0];
+                        x[t][1] *= k0 * f[t][1];
+                        x[t][2] *= k1 * f[t][0];
+                        x[t][3] *= k1 * f[t][1];
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t a[4];
+                        few_ldsm4(kb + (k / 4) * 8192 + few_at128(key0 + mr + 8 * (mi & 1), 2 * (k % 4) + (mi >> 1)), a);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            few_mma<false>(x[t], a[0], a[1], a[2], a[3], qf[t][k][0], qf[t][k][1]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[t][e] *= p.scale_log2;
+                    }
+                }
+                if (key0 + 16 > lim) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        if (key0 + r >= lim) x[t][0] = x[t][1] = -INFINITY;
+                        if (key0 + r + 8 >= lim) x[t][2] = x[t][3] = -INFINITY;
+                    }
+                }
+                if constexpr (E4M3) {
+                    // the unit exponent: the largest V exponent of this warp's keys so far, less 7
+                    const uint4 w = *reinterpret_cast<const uint4*>(es + 64 + key0);
+                    uint32_t top = __vmaxu4(__vmaxu4(w.x, w.y), __vmaxu4(w.z, w.w));
+                    top = __vmaxu4(top, top >> 16);
+                    top = max(top & 0xFFu, (top >> 8) & 0xFFu);
+                    const int u = max(kTreeUMin, min(static_cast<int>(top), 254) - 127 - 7);
+                    if (!st.unit_set || u > st.u) {
+                        const float g = pow2i(max(-126, st.u - u));
+                        float a[NT][2];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) a[t][0] = a[t][1] = g;
+                        few_scale<D, NT>(st, a);
+                        st.u = u;
+                        st.unit_set = true;
+                    }
+                }
+                few_softmax<D, NT>(st, x);
+                uint32_t pb[NT][2];  // P^T: keys 2 q4, + 1 (+ 8) of row 8 t + r
+                if constexpr (E4M3) {
+                    const int e0 = es[64 + key0 + r], e1 = es[64 + key0 + r + 8];
+                    // a row of exponent 255 stands for NaN for every token (its bytes are zero, 0 * inf)
+                    const float g0 = __uint_as_float(static_cast<uint32_t>(e0 == 255 ? 255 : max(e0 - st.u, 0)) << 23);
+                    const float g1 = __uint_as_float(static_cast<uint32_t>(e1 == 255 ? 255 : max(e1 - st.u, 0)) << 23);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        pb[t][0] = few_transpose(pack_f16x2(x[t][0] * g0, x[t][1] * g0));
+                        pb[t][1] = few_transpose(pack_f16x2(x[t][2] * g1, x[t][3] * g1));
+                    }
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t a[4];  // (keys 0-7, chunk 2c), (keys 8-15, 2c), (keys 0-7, 2c + 1), (keys 8-15, 2c + 1)
+                        few_ldsm4_t(vb + few_at_e4m3<D>(key0 + mr + 8 * (mi & 1), 2 * c + (mi >> 1)), a);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) a[i] = __byte_perm(a[i], 0u, 0x3120);  // (even, even, odd, odd)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t a0 = few_f16(a[2 * h]), a1 = few_f16_hi(a[2 * h]);
+                            const uint32_t a2 = few_f16(a[2 * h + 1]), a3 = few_f16_hi(a[2 * h + 1]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) few_mma<true>(st.o[t][2 * c + h], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        pb[t][0] = few_transpose(pack_bf16x2(x[t][0], x[t][1]));
+                        pb[t][1] = few_transpose(pack_bf16x2(x[t][2], x[t][3]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t a[4];
+                        few_ldsm4_t(vb + (j / 4) * 8192 + few_at128(key0 + mr + 8 * (mi >> 1), 2 * (j % 4) + (mi & 1)), a);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) few_mma<false>(st.o[t][j], a[0], a[1], a[2], a[3], pb[t][0], pb[t][1]);
+                    }
+                }
+                if (key0 + 16 > lim) fence_proxy_async_smem();  // the zeros, before the next copy into the stage
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+            advance();
+        }
+
+        if (u1 == units) {
+            // ---- the drafted tokens (16 at most): the first warp takes them
+            if (ok) ok = mbar_wait(&dfull, dpar, p.status, kTreeDetail | 0x17u);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok) {
+                dpar ^= 1u;
+                if (warp == 0) {
+                    const uint64_t live = (1ull << p.T) - 1ull;
+                    uint32_t mk[NT][2];  // the ancestor bits of this thread's rows
+                    float x[NT][4];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int row = 8 * t + 2 * q4 + e;
+                            mk[t][e] = row < rows ? static_cast<uint32_t>(__ldg(p.mask + static_cast<int64_t>(b) * p.T + row % p.T) & live) : 0u;
+                        }
+                        x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+                    }
+                    const uint32_t kb = smem_u32(dk_s);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t a[4];
+                        few_ldsm4(kb + (k / 4) * 2048 + few_at128(mr + 8 * (mi & 1), 2 * (k % 4) + (mi >> 1)), a);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            uint32_t b0, b1;
+                            if constexpr (E4M3) {  // bf16 rows as they are
+                                const uint32_t* w = reinterpret_cast<const uint32_t*>(p.Q + (out0 + 8 * t + r) * D + 16 * k) + q4;
+                                const bool have = 8 * t + r < rows;
+                                b0 = have ? __ldg(w) : 0u;
+                                b1 = have ? __ldg(w + 4) : 0u;
+                            } else {
+                                b0 = qf[t][k][0];
+                                b1 = qf[t][k][1];
+                            }
+                            few_mma<false>(x[t], a[0], a[1], a[2], a[3], b0, b1);
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            x[t][e] = (mk[t][e] >> r) & 1u ? x[t][e] * p.scale_log2 : -INFINITY;
+                            x[t][2 + e] = (mk[t][e] >> (r + 8)) & 1u ? x[t][2 + e] * p.scale_log2 : -INFINITY;
+                        }
+                    }
+                    few_softmax<D, NT>(st, x);
+                    const float g = E4M3 ? pow2i(min(127, max(-126, -st.u))) : 1.f;
+                    uint32_t pb[NT][2];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        pb[t][0] = few_transpose(pack_bf16x2(x[t][0] * g, x[t][1] * g));
+                        pb[t][1] = few_transpose(pack_bf16x2(x[t][2] * g, x[t][3] * g));
+                    }
+                    // V value by value, in the order of O's tiles: rows past the tokens are left out, and so is a
+                    // value that is not finite, which would reach every token through 0 * x
+                    auto value = [&](int key, int dim) -> uint32_t {
+                        if (key >= p.T) return 0u;
+                        return *reinterpret_cast<const uint16_t*>(dk_s + C::DRAFT + (dim / 64) * 2048 +
+                                                                  few_at128(key, (dim % 64) / 8) + 2 * (dim % 8));
+                    };
+                    auto finite = [](uint32_t h) { return (h & 0x7F80u) != 0x7F80u; };
+                    bool odd = false;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        const int d0 = 16 * j + (E4M3 ? 2 * r : r), d1 = E4M3 ? d0 + 1 : d0 + 8;
+                        uint32_t a[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int dim = i & 1 ? d1 : d0, key = 2 * q4 + 8 * (i >> 1);
+                            uint32_t lo = value(key, dim), hi = value(key + 1, dim);
+                            odd = odd || !finite(lo) || !finite(hi);
+                            lo = finite(lo) ? lo : 0u;
+                            hi = finite(hi) ? hi : 0u;
+                            a[i] = lo | (hi << 16);
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) few_mma<false>(st.o[t][j], a[0], a[1], a[2], a[3], pb[t][0], pb[t][1]);
+                    }
+                    if (__any_sync(0xFFFFFFFFu, odd)) {  // given to the tokens that attend it
+                        for (int key = 0; key < p.T; ++key) {
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j) {
+                                const int d0 = 16 * j + (E4M3 ? 2 * r : r), d1 = E4M3 ? d0 + 1 : d0 + 8;
+                                const uint32_t v0 = value(key, d0), v1 = value(key, d1);
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        if (!((mk[t][e] >> key) & 1u)) continue;
+                                        if (!finite(v0)) st.o[t][j][e] += __uint_as_float(v0 << 16);
+                                        if (!finite(v1)) st.o[t][j][2 + e] += __uint_as_float(v1 << 16);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&dempty);
+            }
+        }
+
+        // ---- the piece's end: the four warps meet in shared memory, CH dims at a time
+        float uf = 1.f;
+        if constexpr (E4M3) uf = pow2i(min(127, max(-126, st.u)));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = st.l[t][e];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+                if (r == 0) {
+                    const int row = warp * C::RM + 8 * t + 2 * q4 + e;
+                    cml[2 * row] = st.m[t][e];
+                    cml[2 * row + 1] = l;
+                }
+            }
+        }
+        const bool whole = unit == 0 && u1 == units;
+        // partial slots: 2c for a piece that goes on with a row tile, 2c + 1 for one that begins it
+        float* part = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (unit == 0 ? 1 : 0)) * C::RM * (D + 2);
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += C::CH) {
+#pragma unroll
+            for (int jj = 0; jj < C::CH / 16; ++jj) {
+                const int j = c0 / 16 + jj;
+                const int d0 = 16 * jj + (E4M3 ? 2 * r : r), d1 = E4M3 ? d0 + 1 : d0 + 8;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float* at = comb + (warp * C::RM + 8 * t + 2 * q4 + e) * C::CH;
+                        at[d0] = st.o[t][j][e] * uf;
+                        at[d1] = st.o[t][j][2 + e] * uf;
+                    }
+                }
+            }
+            named_bar_sync(1, 128);
+            for (int e = tid; e < C::RM * C::CH; e += 128) {
+                const int row = e / C::CH, d = c0 + e % C::CH;
+                float M = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) M = fmaxf(M, cml[2 * (k * C::RM + row)]);
+                float v = 0.f, l = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float mk = cml[2 * (k * C::RM + row)], lk = cml[2 * (k * C::RM + row) + 1];
+                    // a warp without a key for the row has l = 0 (and o = 0) unless it met a NaN
+                    const float w = mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : fast_exp2(mk - M);
+                    v += w * comb[(k * C::RM + row) * C::CH + e % C::CH];
+                    l += w * lk;
+                }
+                if (whole) {
+                    if (row < rows) {
+                        p.O[(out0 + row) * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
+                        if (d == 0 && p.lse != nullptr)
+                            p.lse[out0 + row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+                    }
+                } else {
+                    part[row * D + d] = v;
+                    if (d == 0) {
+                        part[C::RM * D + 2 * row] = l == 0.f ? -INFINITY : M;
+                        part[C::RM * D + 2 * row + 1] = l;
+                    }
+                }
+            }
+            named_bar_sync(1, 128);
+        }
+        pos += u1 - unit;
+        unit = 0;
+        ++tile;
+    }
+    __syncthreads();
+}
+
+template <int D, bool E4M3, int NT>
+static bool launch_few(TreeParams p, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dk,
+                       const CUtensorMap& dv, cudaStream_t st, int32_t* launches) {
+    using C = FewCfg<D, E4M3, NT>;
+    constexpr int budget = 112 * 1024;  // two CTAs share an SM's shared memory
+    constexpr int fit = (budget - C::FIXED) / (C::STAGE + C::EXPS);
+    static_assert(fit >= 2, "two stages must fit");
+    p.nk = fit < kFewStages ? fit : kFewStages;
+    p.nv = 0;
+    const int smem = C::FIXED + p.nk * (C::STAGE + C::EXPS);
+    static std::atomic<uint64_t> configured{0};
+    if (!configure_smem_once(reinterpret_cast<const void*>(attn_tree_few_kernel<D, E4M3, NT>), smem, configured))
+        return false;
+    attn_tree_few_kernel<D, E4M3, NT><<<p.runs, kFewThreads, smem, st>>>(k, v, dk, dv, p);
+    if (cudaGetLastError() != cudaSuccess) return false;
+    ++*launches;
+    return launch_tree_merge(p, D, C::RM, st, launches);
+}
+
+bool launch_attn_tree_few(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
+                          cudaStream_t st, int32_t* launches) {
+    const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv * p.cap, drows = static_cast<int64_t>(p.B) * p.Hkv * p.T;
+    CUtensorMap k, v, dk, dv;
+    if (!make_tmap_2d(&dk, K, drows, D, 16) || !make_tmap_2d(&dv, p.DV, drows, D, 16)) return false;
+    if (e4m3 ? !make_tmap_2d_u8(&k, Kc, rows, D, 64) || !make_tmap_2d_u8(&v, Vc, rows, D, 64)
+             : !make_tmap_2d(&k, Kc, rows, D, 64) || !make_tmap_2d(&v, Vc, rows, D, 64))
+        return false;
+#define PISA_FEW_CASE(DD, EE, NN) \
+    if (D == DD && e4m3 == EE && rm == 8 * NN) return launch_few<DD, EE, NN>(p, k, v, dk, dv, st, launches);
+    PISA_FEW_CASE(64, false, 1)
+    PISA_FEW_CASE(64, false, 2)
+    PISA_FEW_CASE(64, true, 1)
+    PISA_FEW_CASE(64, true, 2)
+    PISA_FEW_CASE(128, false, 1)
+    PISA_FEW_CASE(128, false, 2)
+    PISA_FEW_CASE(128, true, 1)
+    PISA_FEW_CASE(128, true, 2)
+#undef PISA_FEW_CASE
+    return false;
+}
+
+}  // namespace pisa

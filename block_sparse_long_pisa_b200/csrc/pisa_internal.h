@@ -281,7 +281,8 @@ struct TreeParams {
     int32_t mt, rows_per_seq;       // row tiles per selection row, and per sequence (Hsel * mt)
     int32_t runs, min_units;        // runs (CTAs) at most, and units one run has at least on average
     int32_t tp;                     // drafted tokens rounded up to 16
-    int32_t nk, nv;                 // slots of the K and of the V ring (set by the launcher)
+    int32_t nk, nv;                 // slots of the K and of the V ring, or (few rows) stages of the one
+                                    // ring in nk (set by the launcher)
     float scale_log2;
 };
 
@@ -314,6 +315,9 @@ bool launch_cache_pyramid(const CachePyramidParams& p, cudaStream_t st, int32_t*
 // Rows of one row tile for a selection row that `rows` = heads x drafted tokens share.
 int tree_row_tile(int rows);
 int tree_ctas_per_sm(int rm, bool e4m3);
+bool launch_tree_merge(const TreeParams& p, int D, int rm, cudaStream_t st, int32_t* launches);
+bool launch_attn_tree_few(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
+                          cudaStream_t st, int32_t* launches);
 bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
                       cudaStream_t st, int32_t* launches);
 bool launch_attn_backward(const BwdParams& p, int32_t batch, cudaStream_t st, int32_t* launches);
