@@ -175,7 +175,7 @@ struct TreeCfg {
     static constexpr int NWG = R >= 64 ? R / 32 : 1;     // softmax warpgroups: each takes RW columns
     static constexpr int RW = R / NWG;
     static constexpr int CW = 16;                        // columns of O taken at a time
-    static constexpr int NP = 2;                         // P buffers
+    static constexpr int NP = !E4M3 && R > 64 ? 1 : 2;   // P buffers: one where a second would cost a slot
     static constexpr float LAZY = E4M3 ? 4.f : 8.f;      // log2 units a score may exceed the kept maximum by
     // dynamic shared memory without the rings: Q, P, masks, row parameters (8 floats a row), exponents
     static constexpr int FIXED = 1024 + QB + NP * PB + R * 8 + R * 32 + kTreeMeta * EXPS;
@@ -642,6 +642,12 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
             uint64_t l2[C::RW / 2];  // this key's share of the rows' sums
 #pragma unroll
             for (int i = 0; i < C::RW / 2; ++i) l2[i] = 0ull;
+            // bf16: the kept maxima in registers (a shared-memory load waits for the products' operand reads)
+            uint64_t nm2[E4M3 ? 1 : C::RW / 2];
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int i = 0; i < C::RW / 2; ++i) nm2[i] = 0ull;
+            }
             bool fresh = true, cached = false;  // no tile yet; a tile of the cache so far
             int u = 0, uexp = 0;   // unit exponent of O, and the V exponent it was set by (e4m3)
 
@@ -705,15 +711,15 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                 const uint64_t kf2 = f2_pack(kf, kf);
 #pragma unroll
                 for (int i = 0; i < C::RW / 4; ++i) {
-                    const float4 nm = *reinterpret_cast<const float4*>(nms + 4 * i);
                     if constexpr (E4M3) {
+                        const float4 nm = *reinterpret_cast<const float4*>(nms + 4 * i);
                         float4 f = *reinterpret_cast<const float4*>(rf + 4 * i);
                         if (draft) f = make_float4(1.f, 1.f, 1.f, 1.f);  // bf16 rows as they are
                         x[2 * i] = f2_fma(f2_mul(x[2 * i], kf2), f2_pack(f.x, f.y), f2_pack(nm.x, nm.y));
                         x[2 * i + 1] = f2_fma(f2_mul(x[2 * i + 1], kf2), f2_pack(f.z, f.w), f2_pack(nm.z, nm.w));
                     } else {
-                        x[2 * i] = f2_fma(x[2 * i], kf2, f2_pack(nm.x, nm.y));
-                        x[2 * i + 1] = f2_fma(x[2 * i + 1], kf2, f2_pack(nm.z, nm.w));
+                        x[2 * i] = f2_fma(x[2 * i], kf2, nm2[2 * i]);
+                        x[2 * i + 1] = f2_fma(x[2 * i + 1], kf2, nm2[2 * i + 1]);
                     }
                 }
                 if (partial) {
@@ -792,6 +798,11 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                         const float4 d = *reinterpret_cast<const float4*>(ws + 4 * i);
                         x[2 * i] = f2_add(x[2 * i], f2_pack(d.x, d.y));
                         x[2 * i + 1] = f2_add(x[2 * i + 1], f2_pack(d.z, d.w));
+                        if constexpr (!E4M3) {
+                            const float4 nm = *reinterpret_cast<const float4*>(nms + 4 * i);
+                            nm2[2 * i] = f2_pack(nm.x, nm.y);
+                            nm2[2 * i + 1] = f2_pack(nm.z, nm.w);
+                        }
                     }
                     if (!fresh) {
                         const int j = pt - 1;
@@ -822,8 +833,8 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                     }
                     fresh = false;
                 }
-                // P's buffer is free: this tile's S is complete, and with it every product issued before it, the
-                // P.V of two tiles before among them
+                // With two buffers P's is free: this tile's S is complete, and with it every product issued
+                // before it, the P.V of two tiles before among them.
                 uint8_t* pb = p_s + (pt % C::NP) * C::PB;
 #pragma unroll
                 for (int i = 0; i < C::RW / 2; ++i) {
@@ -832,6 +843,8 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                     x[i] = f2_pack(fast_exp2(lo), fast_exp2(hi));
                     l2[i] = f2_add(l2[i], x[i]);
                 }
+                if (C::NP == 1 && pt > 0 && ok)  // the one buffer: the last P.V has read it
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pvdone[0], (pt - 1) & 1, p.status, kTreeDetail | 0x0Eu));
                 if constexpr (E4M3) {
                     // a row of exponent 255 stands for NaN (its bytes are zero); a row that does not count has
                     // P = 0 and a factor of 2^-126
@@ -1093,8 +1106,8 @@ int tree_row_tile(int rows) {
     return (rows + 63) / 64 * 64 < (rows + 95) / 96 * 96 ? 64 : 96;
 }
 
-// CTAs on one SM: two where the shared memory of both fits.
-int tree_ctas_per_sm(int rm, bool e4m3) { return rm <= 16 || (e4m3 && rm <= 32) ? 2 : 1; }
+// CTAs on one SM: as many as its shared memory takes.
+int tree_ctas_per_sm(int rm, bool e4m3) { return e4m3 && rm == 8 ? 3 : rm <= 16 || (e4m3 && rm <= 32) ? 2 : 1; }
 
 bool launch_tree_merge(const TreeParams& p, int D, int rm, cudaStream_t st, int32_t* launches) {
     cudaLaunchConfig_t cfg{};

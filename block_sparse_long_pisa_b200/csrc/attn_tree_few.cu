@@ -100,73 +100,80 @@ struct FewCfg {
     static constexpr int RM = 8 * NT;
     static constexpr int CH = 32 / NT;                   // dims that meet at a time when a piece ends
     static constexpr int FIXED = 1024 + 2 * DRAFT + 4 * RM * (CH + 2) * 4;
+    // three CTAs on an SM where two stages a CTA or more remain (the decode step above: 101 us, 112 with two
+    // CTAs of five stages), else two
+    static constexpr int CTAS = E4M3 && NT == 1 ? 3 : 2;
 };
 
-// One warp's state: for its rows 2 (lane % 4), + 1 of every row tile of 8 the kept maximum (log2 units)
-// and the sum over its keys; O^T: tile j is dims 16 j + lane / 4 (+ 8) (e4m3: 16 j + 2 (lane / 4), + 1);
-// the unit exponent of O.
+// One warp's state: for its rows 2 (lane % 4), + 1 of every row tile of 8 the reference that its
+// probabilities are taken against (a maximum so far, log2 units; 0 while there is none) and the sum over
+// its keys; O^T: tile j is dims 16 j + lane / 4 (+ 8) (e4m3: 16 j + 2 (lane / 4), + 1); the unit exponent of
+// O and the V exponent that it was set by.
 template <int D, int NT>
 struct FewState {
     float o[NT][D / 16][4];
-    float m[NT][2], l[NT][2];
-    int u;
-    bool unit_set;
+    float ref[NT][2], l[NT][2];
+    int u, uexp;
+    bool fresh;   // no key yet
 };
 
+// Scores of 16 keys (log2 units, -inf where masked; [0], [1]: this thread's first key, [2], [3]: its
+// second), ev: the larger V exponent of the two -> probabilities. References move, and O and the sums
+// with them, when a score exceeds one by kFewLazy; the unit when an exponent exceeds the one it was set by.
 template <int D, int NT>
-__device__ __forceinline__ void few_scale(FewState<D, NT>& s, const float (&a)[NT][2]) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            s.o[t][j][0] *= a[t][0];
-            s.o[t][j][1] *= a[t][1];
-            s.o[t][j][2] *= a[t][0];
-            s.o[t][j][3] *= a[t][1];
-        }
-    }
-}
-
-// Scores of 16 keys (log2 units, -inf where masked; [0], [1]: this thread's first key, [2], [3]: its second)
-// -> probabilities against the kept maxima, which move when a score exceeds one by kFewLazy.
-template <int D, int NT>
-__device__ __forceinline__ void few_softmax(FewState<D, NT>& s, float (&x)[NT][4]) {
-    bool over = false;
+__device__ __forceinline__ void few_softmax(FewState<D, NT>& s, float (&x)[NT][4], int ev) {
+    bool over = s.fresh || ev > s.uexp;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-        over = over || fmaxf(x[t][0], x[t][2]) > s.m[t][0] + kFewLazy || fmaxf(x[t][1], x[t][3]) > s.m[t][1] + kFewLazy;
+        over = over || fmaxf(x[t][0], x[t][2]) > s.ref[t][0] + kFewLazy || fmaxf(x[t][1], x[t][3]) > s.ref[t][1] + kFewLazy;
     if (__any_sync(0xFFFFFFFFu, over)) {
-        float a[NT][2];
+        float g = 1.f;
+        const int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(ev)));
+        if (e > s.uexp) {
+            s.uexp = e;
+            const int u = max(kTreeUMin, min(e, 254) - 127 - 7);
+            g = s.fresh ? 1.f : pow2i(max(-126, s.u - u));
+            s.u = u;
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+            float a[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float top = fmaxf(x[t][e], x[t][2 + e]);
+            for (int e2 = 0; e2 < 2; ++e2) {
+                float top = fmaxf(x[t][e2], x[t][2 + e2]);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const float now = fmaxf(s.m[t][e], top);
-                a[t][e] = now == s.m[t][e] ? 1.f : fast_exp2(s.m[t][e] - now);
-                s.m[t][e] = now;
-                s.l[t][e] *= a[t][e];
+                const float old = s.ref[t][e2];
+                // a row with nothing so far keeps 0 (its scores are all -inf and give 0)
+                const float now = s.fresh ? (top == -INFINITY ? 0.f : top) : fmaxf(old, top);
+                a[e2] = s.fresh || now == old ? 1.f : fast_exp2(old - now);
+                s.ref[t][e2] = now;
+                s.l[t][e2] *= a[e2];
+                a[e2] *= g;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                s.o[t][j][0] *= a[0];
+                s.o[t][j][1] *= a[1];
+                s.o[t][j][2] *= a[0];
+                s.o[t][j][3] *= a[1];
             }
         }
-        few_scale<D, NT>(s, a);
+        s.fresh = false;
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        // a row with no key yet keeps m = -inf: its scores are all -inf and give 0
-        const float r0 = s.m[t][0] == -INFINITY ? 0.f : s.m[t][0], r1 = s.m[t][1] == -INFINITY ? 0.f : s.m[t][1];
-        x[t][0] = fast_exp2(x[t][0] - r0);
-        x[t][1] = fast_exp2(x[t][1] - r1);
-        x[t][2] = fast_exp2(x[t][2] - r0);
-        x[t][3] = fast_exp2(x[t][3] - r1);
+        x[t][0] = fast_exp2(x[t][0] - s.ref[t][0]);
+        x[t][1] = fast_exp2(x[t][1] - s.ref[t][1]);
+        x[t][2] = fast_exp2(x[t][2] - s.ref[t][0]);
+        x[t][3] = fast_exp2(x[t][3] - s.ref[t][1]);
         s.l[t][0] += x[t][0] + x[t][2];
         s.l[t][1] += x[t][1] + x[t][3];
     }
 }
 
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kFewThreads, 2)
+__global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
     attn_tree_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
                          const TreeParams p) {
@@ -347,11 +354,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) st.o[t][j][0] = st.o[t][j][1] = st.o[t][j][2] = st.o[t][j][3] = 0.f;
-            st.m[t][0] = st.m[t][1] = -INFINITY;
+            st.ref[t][0] = st.ref[t][1] = 0.f;
             st.l[t][0] = st.l[t][1] = 0.f;
         }
         st.u = 0;
-        st.unit_set = false;
+        st.uexp = 0;
+        st.fresh = true;
 
         // Q as the B operand: row 8 t + r; bf16: dims 16 k + 2 q4 (+ 8); e4m3: dims 16 k + 4 q4 .. + 3 as
         // fp16, scaled; and the score factors of this thread's rows 8 t + 2 q4, + 1
@@ -470,27 +478,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         if (key0 + r + 8 >= lim) x[t][2] = x[t][3] = -INFINITY;
                     }
                 }
-                if constexpr (E4M3) {
-                    // the unit exponent: the largest V exponent of this warp's keys so far, less 7
-                    const uint4 w = *reinterpret_cast<const uint4*>(es + 64 + key0);
-                    uint32_t top = __vmaxu4(__vmaxu4(w.x, w.y), __vmaxu4(w.z, w.w));
-                    top = __vmaxu4(top, top >> 16);
-                    top = max(top & 0xFFu, (top >> 8) & 0xFFu);
-                    const int u = max(kTreeUMin, min(static_cast<int>(top), 254) - 127 - 7);
-                    if (!st.unit_set || u > st.u) {
-                        const float g = pow2i(max(-126, st.u - u));
-                        float a[NT][2];
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) a[t][0] = a[t][1] = g;
-                        few_scale<D, NT>(st, a);
-                        st.u = u;
-                        st.unit_set = true;
-                    }
-                }
-                few_softmax<D, NT>(st, x);
+                const int e0 = E4M3 ? es[64 + key0 + r] : 0, e1 = E4M3 ? es[64 + key0 + r + 8] : 0;
+                few_softmax<D, NT>(st, x, max(e0, e1));
                 uint32_t pb[NT][2];  // P^T: keys 2 q4, + 1 (+ 8) of row 8 t + r
                 if constexpr (E4M3) {
-                    const int e0 = es[64 + key0 + r], e1 = es[64 + key0 + r + 8];
                     // a row of exponent 255 stands for NaN for every token (its bytes are zero, 0 * inf)
                     const float g0 = __uint_as_float(static_cast<uint32_t>(e0 == 255 ? 255 : max(e0 - st.u, 0)) << 23);
                     const float g1 = __uint_as_float(static_cast<uint32_t>(e1 == 255 ? 255 : max(e1 - st.u, 0)) << 23);
@@ -581,7 +572,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                             x[t][2 + e] = (mk[t][e] >> (r + 8)) & 1u ? x[t][2 + e] * p.scale_log2 : -INFINITY;
                         }
                     }
-                    few_softmax<D, NT>(st, x);
+                    few_softmax<D, NT>(st, x, 0);
                     const float g = E4M3 ? pow2i(min(127, max(-126, -st.u))) : 1.f;
                     uint32_t pb[NT][2];
 #pragma unroll
@@ -650,7 +641,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
                 if (r == 0) {
                     const int row = warp * C::RM + 8 * t + 2 * q4 + e;
-                    cml[2 * row] = st.m[t][e];
+                    cml[2 * row] = l == 0.f ? -INFINITY : st.ref[t][e];
                     cml[2 * row + 1] = l;
                 }
             }
@@ -684,8 +675,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float mk = cml[2 * (k * C::RM + row)], lk = cml[2 * (k * C::RM + row) + 1];
-                    // a warp without a key for the row has l = 0 (and o = 0) unless it met a NaN
-                    const float w = mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : fast_exp2(mk - M);
+                    const float w = mk == -INFINITY ? 0.f : fast_exp2(mk - M);  // a warp without a key for the row
                     v += w * comb[(k * C::RM + row) * C::CH + e % C::CH];
                     l += w * lk;
                 }
@@ -716,7 +706,7 @@ template <int D, bool E4M3, int NT>
 static bool launch_few(TreeParams p, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dk,
                        const CUtensorMap& dv, cudaStream_t st, int32_t* launches) {
     using C = FewCfg<D, E4M3, NT>;
-    constexpr int budget = 112 * 1024;  // two CTAs share an SM's shared memory
+    constexpr int budget = (C::CTAS == 3 ? 74 : 112) * 1024;  // of the SM's shared memory
     constexpr int fit = (budget - C::FIXED) / (C::STAGE + C::EXPS);
     static_assert(fit >= 2, "two stages must fit");
     p.nk = fit < kFewStages ? fit : kFewStages;
