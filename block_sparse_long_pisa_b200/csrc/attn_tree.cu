@@ -52,88 +52,13 @@
 
 namespace pisa {
 
-constexpr int kTreeMaxSlots = 4;  // of the K ring and of the V ring
-constexpr int kTreeMeta = 8;      // entries (tiles and piece ends) whose description is kept
-enum : int { kTileEnd = 0, kTileCache = 1, kTileDraft = 2 };
 
 // ---------------------------------------------------------------- operands
-
-// Shared-memory matrix descriptor; layout: 0 = none, 2 = 128-byte, 4 = 64-byte swizzle.
-__device__ __forceinline__ uint64_t tree_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(layout) << 61);
-}
-__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
-
-// Instruction descriptor for kind::f8f6f4: A e4m3, B e4m3 (0) or e5m2 (1), fp32 accumulator, M = 128.
-__host__ __device__ constexpr uint32_t idesc_f8(int n, int b_type, int a_mn, int b_mn) {
-    return (1u << 4) | (static_cast<uint32_t>(b_type) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
-           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
-}
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 
 __device__ __forceinline__ float warp_max(float x) {
     float r;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
-}
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t cvt_e5m2x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float2 e4m3x2_f32(uint32_t two) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-    return __half22float2(*reinterpret_cast<__half2*>(&h));
-}
-// Barrier over a softmax warpgroup's threads; true if `x` holds in any of them.
-__device__ __forceinline__ bool softmax_any(uint32_t bar, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(x)), "r"(bar)
-        : "memory");
-    return r != 0;
-}
-// Whether the barrier's phase of this parity has completed (no wait).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return r != 0;
 }
 __device__ __forceinline__ void softmax_sync(uint32_t bar) { named_bar_sync(bar, 128); }
 
@@ -240,155 +165,11 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
     const uint32_t tm_o = tm + 2 * C::SW;
 
     bool ok = true;       // cleared by a wait that ran out: nothing more is waited for
-    // A place in a ring: slot, parity of its current use, and uses so far.
-    struct At {
-        int s = 0, n = 0;
-        uint32_t par = 0;
-        __device__ __forceinline__ void next(int slots) {
-            ++n;
-            if (++s == slots) {
-                s = 0;
-                par ^= 1u;
-            }
-        }
-    };
-    At k, v;              // K ring (tiles and piece ends), V ring (tiles)
+    RingAt k, v;          // K ring (tiles and piece ends), V ring (tiles)
 
     if (warp == 4 * C::NWG) {
-        // ------------------------------------------------ producer
-        if (lane == 0) {
-            prefetch_tmap(&tmK);
-            prefetch_tmap(&tmV);
-            prefetch_tmap(&tmDK);
-            prefetch_tmap(&tmDV);
-        }
-        // one entry: a tile's K and then its V, or the end of a piece; of a tile of the cache the first
-        // keys of its halves (second -1: absent)
-        auto issue = [&](int kind, int64_t plane, int len, int a0, int a1) {
-            if (lane == 0) {
-                ok = k.n < p.nk || mbar_wait(&kempty[k.s], k.par ^ 1u, p.status, kTreeDetail | 0x01u);
-                if (ok) {
-                    uint8_t* kt = ring + k.s * C::TILE;
-                    uint64_t* kb = &kfull[k.s];
-                    const int e = k.n % kTreeMeta;
-                    const int halves = a1 >= 0 ? 2 : 1;
-                    const int dbytes = p.tp * 2 * D, dy = static_cast<int>(plane * p.T);
-                    if (kind == kTileEnd) {
-                        meta[e] = make_int4(kind, 0, 0, 0);
-                        mbar_arrive(kb);
-                    } else if (kind == kTileDraft) {
-                        meta[e] = make_int4(kind, 0, 0, 0);
-                        mbar_arrive_expect_tx(kb, dbytes);
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c) tma_load_2d(kt + c * 8192, &tmDK, 64 * c, dy, kb);
-                    } else {
-                        meta[e] = make_int4(kind, min(64, len - a0), a1 >= 0 ? min(64, len - a1) : 0, 0);
-                        mbar_arrive_expect_tx(kb, halves * (C::TILE + C::EXPS) / 2);
-                        for (int h = 0; h < halves; ++h) {
-                            const int64_t row = plane * p.cap + (h == 0 ? a0 : a1);
-                            if constexpr (E4M3) {
-                                tma_load_2d(kt + h * 64 * D, &tmK, 0, static_cast<int>(row), kb);
-                                bulk_load(exps + e * 256 + h * 64, p.k_exp + row, 64, kb);
-                                bulk_load(exps + e * 256 + 128 + h * 64, p.v_exp + row, 64, kb);
-                            } else {
-#pragma unroll
-                                for (int c = 0; c < D / 64; ++c)
-                                    tma_load_2d(kt + c * 16384 + h * 8192, &tmK, 64 * c, static_cast<int>(row), kb);
-                            }
-                        }
-                    }
-                    k.next(p.nk);
-                    if (kind != kTileEnd) {
-                        ok = v.n < p.nv || mbar_wait(&vempty[v.s], v.par ^ 1u, p.status, kTreeDetail | 0x02u);
-                        if (ok) {
-                            uint8_t* vt = vring + v.s * C::TILE;
-                            uint64_t* vb = &vfull[v.s];
-                            if (kind == kTileDraft) {
-                                mbar_arrive_expect_tx(vb, dbytes);
-#pragma unroll
-                                for (int c = 0; c < D / 64; ++c) tma_load_2d(vt + c * 8192, &tmDV, 64 * c, dy, vb);
-                            } else {
-                                mbar_arrive_expect_tx(vb, halves * C::TILE / 2);
-                                for (int h = 0; h < halves; ++h) {
-                                    const int y = static_cast<int>(plane * p.cap + (h == 0 ? a0 : a1));
-                                    if constexpr (E4M3) {
-                                        tma_load_2d(vt + h * 64 * D, &tmV, 0, y, vb);
-                                    } else {
-#pragma unroll
-                                        for (int c = 0; c < D / 64; ++c)
-                                            tma_load_2d(vt + c * 16384 + h * 8192, &tmV, 64 * c, y, vb);
-                                    }
-                                }
-                            }
-                            v.next(p.nv);
-                        }
-                    }
-                }
-            }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        };
-        while (pos < end && ok) {
-            const int b = static_cast<int>(tile / p.rows_per_seq);
-            const int hs = static_cast<int>(tile % p.rows_per_seq) / p.mt;
-            const int kvh = p.per_qhead ? hs / p.g : hs;
-            const int64_t plane = static_cast<int64_t>(b) * p.Hkv + kvh;
-            const int len = tree_len(p, b);
-            const int units = tree_units(p, len);
-            const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
-            if (tile % p.rows_per_seq == 0 && unit == 0 && lane == 0 && p.len[b] != len)
-                record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB0u);
-            const int32_t* row = p.topk > 0 ? p.idx + (static_cast<int64_t>(b) * p.Hsel + hs) * p.topk : nullptr;
-            const int nsel = p.topk * p.upb;
-            const int uc = min(u1, units - 1);  // the last unit is the drafted tokens
-            int first = -1;                     // a unit that waits for its partner
-            for (int u = unit; u < uc && ok; u += 32) {
-                // up to 32 units at a time: position of each unit's first key, -1 = nothing there
-                int at = -1;
-                if (u + lane < uc) {
-                    const int c = u + lane;
-                    if (p.topk == 0) {
-                        at = 64 * c;
-                    } else if (c >= nsel) {
-                        at = p.seq + 64 * (c - nsel);
-                    } else {
-                        const int j = __ldg(row + c / p.upb);
-                        if (j >= p.n0)
-                            record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB1u);
-                        else if (j >= 0)
-                            at = (j * p.upb + c % p.upb) * 64;
-                    }
-                }
-                for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < len); left != 0 && ok; left &= left - 1) {
-                    const int a = __shfl_sync(0xFFFFFFFFu, at, __ffs(left) - 1);
-                    if (first < 0) {
-                        first = a;
-                    } else {
-                        issue(kTileCache, plane, len, first, a);
-                        first = -1;
-                    }
-                }
-            }
-            if (first >= 0 && ok) issue(kTileCache, plane, len, first, -1);
-            if (u1 == units && ok) issue(kTileDraft, plane, len, 0, 0);
-            if (ok) issue(kTileEnd, plane, len, 0, 0);
-            pos += u1 - unit;
-            unit = 0;
-            ++tile;
-        }
-        // every copy lands before the block ends, also when another role gave up (earlier uses of a slot
-        // were complete before it was filled again)
-        if (lane == 0) {
-            for (int i = 0; i < p.nk && i < k.n; ++i) {
-                k.s = k.s == 0 ? p.nk - 1 : k.s - 1;
-                if (k.s == p.nk - 1) k.par ^= 1u;
-                if (!mbar_wait(&kfull[k.s], k.par, p.status, kTreeDetail | 0x03u)) break;
-            }
-            for (int i = 0; i < p.nv && i < v.n; ++i) {
-                v.s = v.s == 0 ? p.nv - 1 : v.s - 1;
-                if (v.s == p.nv - 1) v.par ^= 1u;
-                if (!mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x04u)) break;
-            }
-        }
+        tree_producer<D, E4M3>(p, tmK, tmV, tmDK, tmDV, ring, vring, exps, kfull, kempty, vfull, vempty, meta, pos, end,
+                               tile, unit);
     } else if (warp == 4 * C::NWG + 1) {
         // ------------------------------------------------ MMA
         if (lane == 0) {
@@ -893,6 +674,8 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                         *reinterpret_cast<uint4*>(pb + (cb / 8 + g) * 2048 + key * 16) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                if (wg == 0 && partial && ok)  // what follows writes V's tile: it has landed
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x0Fu));
                 if (wg == 0 && partial && !valid && !draft) {
                     // what the cache holds past the sequence must not meet P's zeros as a NaN
                     for (int c = 0; c < C::ROW / 16; ++c) {
@@ -1042,11 +825,11 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
     const int64_t tile = blockIdx.x;
     const int b = static_cast<int>(tile / p.rows_per_seq);
     const int rem = static_cast<int>(tile % p.rows_per_seq);
-    const int hs = rem / p.mt, row_base = (rem % p.mt) * RM;
+    const int hs = rem / p.mt, row_base = (rem % p.mt) * p.rpt;
     const int rows = p.gh * p.T;
     const int row = static_cast<int>(blockIdx.y) * 4 + static_cast<int>(threadIdx.x >> 5);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (row_base + row >= rows) return;
+    if (row >= p.rpt || row_base + row >= rows) return;
     const TreeJob job = tree_job(p);
     // units before this row tile (whole warp)
     const int lane = threadIdx.x & 31;
@@ -1098,12 +881,12 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
 
 // ---------------------------------------------------------------- host side
 
-// Rows of one row tile for a selection row of `rows` rows: 8 or 16 (attn_tree_few.cu), else the smallest of
-// 32, 64 and 96 that holds them, or, past 96 rows, of 64 and 96 the one that pads less (96 on a tie).
+// Rows of one row tile for a selection row of `rows` rows: 8 or 16 (attn_tree_few.cu), 32 (here), 128 or
+// 256 (attn_tree_many.cu); past 256 rows several tiles share them evenly.
 int tree_row_tile(int rows) {
-    for (int r : {8, 16, 32, 64, 96})
+    for (int r : {8, 16, 32, 128})
         if (rows <= r) return r;
-    return (rows + 63) / 64 * 64 < (rows + 95) / 96 * 96 ? 64 : 96;
+    return 256;
 }
 
 // CTAs on one SM: as many as its shared memory takes.
@@ -1160,6 +943,7 @@ bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, con
     const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv * p.cap, drows = static_cast<int64_t>(p.B) * p.Hkv * p.T;
     CUtensorMap k, v, dk, dv;
     if (rm <= 16) return launch_attn_tree_few(p, D, e4m3, rm, K, Kc, Vc, st, launches);
+    if (rm >= 128) return launch_attn_tree_many(p, D, e4m3, rm, K, Kc, Vc, st, launches);
     if (!make_tmap_2d(&dk, K, drows, D, p.tp) || !make_tmap_2d(&dv, p.DV, drows, D, p.tp)) return false;
     if (e4m3) {
         if (!make_tmap_2d_u8(&k, Kc, rows, D, 64) || !make_tmap_2d_u8(&v, Vc, rows, D, 64)) return false;

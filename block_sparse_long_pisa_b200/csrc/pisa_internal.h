@@ -279,6 +279,7 @@ struct TreeParams {
     int32_t B, Hq, Hkv, Hsel, g, gh, T, cap, seq, topk, n0, per_qhead;
     int32_t upb;                    // 64-key units per block
     int32_t mt, rows_per_seq;       // row tiles per selection row, and per sequence (Hsel * mt)
+    int32_t rpt;                    // rows of one row tile that are used
     int32_t runs, min_units;        // runs (CTAs) at most, and units one run has at least on average
     int32_t tp;                     // drafted tokens rounded up to 16
     int32_t nk, nv;                 // slots of the K and of the V ring, or (few rows) stages of the one
@@ -316,6 +317,8 @@ bool launch_cache_pyramid(const CachePyramidParams& p, cudaStream_t st, int32_t*
 int tree_row_tile(int rows);
 int tree_ctas_per_sm(int rm, bool e4m3);
 bool launch_tree_merge(const TreeParams& p, int D, int rm, cudaStream_t st, int32_t* launches);
+bool launch_attn_tree_many(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
+                           cudaStream_t st, int32_t* launches);
 bool launch_attn_tree_few(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
                           cudaStream_t st, int32_t* launches);
 bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,

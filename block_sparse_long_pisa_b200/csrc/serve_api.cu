@@ -344,6 +344,7 @@ pisa_status pisa_tree_attention(const pisa_tree_shape* shape, const void* Q, con
     p.upb = shape->block / 64;
     p.mt = t.mt;
     p.rows_per_seq = t.hsel * t.mt;
+    p.rpt = (t.rows + t.mt - 1) / t.mt;
     p.runs = t.runs;
     p.min_units = kTreeMinUnits;
     p.tp = (shape->drafts + 15) / 16 * 16;

@@ -435,6 +435,14 @@ TREE_CASES = [
     (1, 4, 1, 64, 192, 128, 0, 64, 0, 0, 0, [190], "any"),
     (1, 4, 1, 64, 192, 128, 1, 64, 0, 0, 0, [190], "any"),
     (1, 5, 1, 64, 192, 64, 1, 64, 128, 2, 0, [131], "tree"),
+    (2, 8, 2, 24, 448, 128, 0, 64, 384, 3, 0, [448, 70], "tree"),
+    (2, 8, 2, 24, 448, 128, 1, 64, 384, 3, 0, [448, 70], "tree"),
+    (1, 9, 3, 11, 320, 64, 1, 64, 0, 0, 0, [319], "tree"),
+    (1, 6, 1, 64, 256, 128, 1, 128, 128, 1, 0, [200], "any"),
+    (1, 6, 1, 64, 256, 64, 0, 64, 0, 0, 0, [129], "tree"),
+    (3, 8, 1, 20, 8192, 128, 1, 64, 0, 0, 0, [8000, 0, 64], "chain"),
+    (3, 4, 1, 16, 8192, 128, 0, 64, 0, 0, 0, [1, 8191, 4000], "tree"),
+    (2, 3, 1, 9, 256, 64, 0, 64, 192, 1, 1, [192, 255], "tree"),
     (1, 1, 1, 2, 40960, 128, 1, 64, 0, 0, 0, [40001], "chain"),
     (1, 2, 1, 2, 20480, 64, 0, 128, 0, 0, 0, [20479], "chain"),
     (33, 2, 2, 2, 128, 64, 1, 64, 0, 0, 0, None, "tree"),
@@ -506,7 +514,7 @@ def test_tree_attention(pisa, case):
     assert none is None and torch.equal(O, O2)
 
 
-@pytest.mark.parametrize("case", [TREE_CASES[i] for i in (4, 10, 13, 17)])
+@pytest.mark.parametrize("case", [TREE_CASES[i] for i in (4, 10, 13, 17, 18, 19, 24)])
 @pytest.mark.parametrize("spread, qscale", [(12, 1.0), (0, 30.0), (6, 1e-3)])
 def test_tree_attention_of_unlike_rows(pisa, case, spread, qscale):
     """Value rows from 2^-12 to 2^12 of one another (the unit of O moves), peaked and flat scores."""
@@ -517,7 +525,7 @@ def test_tree_attention_of_unlike_rows(pisa, case, spread, qscale):
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
-@pytest.mark.parametrize("T, Hq", [(5, 2), (9, 4), (40, 2)])
+@pytest.mark.parametrize("T, Hq", [(5, 1), (5, 2), (8, 4), (9, 4), (40, 2), (40, 4)])
 def test_drafts_that_are_not_attended_do_not_touch_a_token(pisa, fmt, T, Hq):
     """Drafted token 2 holds NaN keys and values, token 3 infinite values: the tokens that attend
     neither are as if both held zeros; those that do see a NaN."""
