@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                     tc_fence_after();
                 }
                 if (mt.x == kTileEnd) {
-                    if (softmax_any(bar, !ok) && softmax_any(bar, !ok)) ok = false;
+                    if (vote_any(bar, 128, !ok) && vote_any(bar, 128, !ok)) ok = false;
                     ++it;
                     k.next(p.nk);
                     break;
@@ -527,8 +527,8 @@ __global__ void __launch_bounds__(TreeCfg<D, E4M3, R>::THREADS, TreeCfg<D, E4M3,
                     top = fmax3(top, lo, hi);
                 }
                 const bool over = top > C::LAZY || (E4M3 && ev > uexp);
-                if (softmax_any(bar, !ok || fresh || over)) {
-                    if (softmax_any(bar, !ok)) {
+                if (vote_any(bar, 128, !ok || fresh || over)) {
+                    if (vote_any(bar, 128, !ok)) {
                         ok = false;
                         break;
                     }

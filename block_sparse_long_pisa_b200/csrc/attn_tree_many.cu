@@ -6,11 +6,11 @@
 // TMEM, so a score costs no shared memory at all (with the keys on the M side, attn_tree.cu, K and V are
 // fetched as the 128-lane operand for every 96 rows, the values transposed at half the rate, and P goes
 // through shared memory: 363 us for trees of 48 tokens of four heads over 8 ragged bf16 caches). A
-// softmax thread owns a row: its maximum, its sum and its mask are its own, warps meet only when a
-// piece begins and, for a e4m3 cache, to form the tile's exponent factors together.
+// row belongs to two softmax threads, one for each half of a tile's keys (one thread for all of them made the
+// softmax the longer side of every tile: 314 us); the two warps meet in one vote a tile.
 //
 // A tile is 128 keys (two units of the cache, or the drafted tokens). Two passes over S in TMEM: the row's
-// maximum (the kept one moves when a score exceeds it by 2^kLazy, and O with it, by the warp alone), then
+// maximum (the kept one moves when a score exceeds it by 2^LAZY, and O with it, by the two warps), then
 // the probabilities, written as operand A of P V over the columns of S that have been read. Order of the
 // MMA lane with two row tiles: S(0, g), P V(1, g - 1), S(1, g), P V(0, g): the softmax of one runs under the
 // products of the other; with one row tile S has two buffers and the order is S(g), P V(g - 1).
@@ -33,9 +33,9 @@ struct ManyCfg {
     static constexpr int EXPS = E4M3 ? 256 : 0;
     static constexpr int QB = 128 * 2 * D;               // one row tile of Q: bf16, or its two 8-bit terms
     static constexpr int FACT = E4M3 ? 1024 : 0;         // factors of 128 keys: K's, then V's
-    static constexpr int FIXED = 1024 + NM * (QB + FACT) + kTreeMeta * EXPS;
+    static constexpr int FIXED = 1024 + NM * (QB + FACT + 1024) + kTreeMeta * EXPS;  // 1024: [half][row] exchange
     static constexpr int RM = 128 * NM;
-    static constexpr int THREADS = 128 * NM + 64;
+    static constexpr int THREADS = 256 * NM + 64;
     static constexpr int O_COL = 256;                    // S: two of 128 columns (row tiles, or buffers)
     static constexpr float LAZY = E4M3 ? 4.f : 8.f;      // log2 units a score may exceed the kept maximum by
 };
@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
     uint8_t* vring = ring + p.nk * C::TILE;
     uint8_t* q_s = vring + p.nv * C::TILE;               // [row tile][QB]
     float* fact = reinterpret_cast<float*>(q_s + NM * C::QB);          // [row tile][K 128, V 128]
-    uint8_t* exps = reinterpret_cast<uint8_t*>(fact) + NM * C::FACT;   // [entry][K 128, V 128]
+    float* xch = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(fact) + NM * C::FACT);  // [row tile][half][128]
+    uint8_t* exps = reinterpret_cast<uint8_t*>(xch) + NM * 1024;       // [entry][K 128, V 128]
     __shared__ __align__(8) uint64_t kfull[kTreeMaxSlots], kempty[kTreeMaxSlots], vfull[kTreeMaxSlots],
         vempty[kTreeMaxSlots], sfull[2], pfull[2], pvdone[2], qfull, done;
     __shared__ int4 meta[kTreeMeta];  // kind, keys that count in the two halves
@@ -91,15 +92,15 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 4);
+            mbar_init(&pfull[i], 8);
             mbar_init(&pvdone[i], 1);
             dflag[0][i] = dflag[1][i] = 0;
         }
-        mbar_init(&qfull, 4 * NM);
+        mbar_init(&qfull, 8 * NM);
         mbar_init(&done, 1);
         fence_barrier_init();
     }
-    if (warp == 4 * NM + 1) tmem_alloc(&tmem_slot, 512);
+    if (warp == 8 * NM + 1) tmem_alloc(&tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -110,10 +111,10 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
     auto bar_of = [](int h, int n) { return NM == 2 ? h : n & 1; };
     auto par_of = [](int n) { return static_cast<uint32_t>((NM == 2 ? n : n >> 1) & 1); };
 
-    if (warp == 4 * NM) {
+    if (warp == 8 * NM) {
         tree_producer<D, E4M3>(p, tmK, tmV, tmDK, tmDV, ring, vring, exps, kfull, kempty, vfull, vempty, meta, pos, end,
                                tile, unit);
-    } else if (warp == 4 * NM + 1) {
+    } else if (warp == 8 * NM + 1) {
         // ------------------------------------------------ MMA
         if (lane == 0) {
             const uint32_t q0 = smem_u32(q_s);
@@ -261,8 +262,12 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------ softmax: thread = row of row tile h = TMEM lane
-        const int h = warp / 4, row = tid & 127;
+        // ------------------------------------------------ softmax: a row of row tile h (TMEM lane), half of
+        // a tile's keys
+        const int h = (warp / 4) % NM, half = warp / (4 * NM), row = tid & 127;
+        const uint32_t pair = 1 + 4 * h + warp % 4, group = 9 + h;  // barriers of the row's two warps, of the row tile
+        float* mine_x = xch + h * 256 + half * 128 + row;
+        const float* other_x = xch + h * 256 + (1 - half) * 128 + row;
         const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
         const int rows = p.gh * p.T;
         float* kfac = fact + h * 256;
@@ -279,13 +284,13 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
             const int base = (rem % p.mt) * p.rpt, mine = min(p.rpt, rows - base);
             const int per = (mine + NM - 1) / NM;
             const int first = base + h * per, nrows = max(0, min(per, mine - h * per));
-            const bool live = (warp % 4) * 32 < nrows;     // the warp has a row
+            const bool live = (warp % 4) * 32 < nrows;     // the two warps have a row
             const uint4* qg = reinterpret_cast<const uint4*>(p.Q + (out0 + first) * D);
             uint8_t* qt = q_s + h * C::QB;
 
             // Q as bf16: [D / 64][128 rows][128 B], 128-byte swizzle
             auto q_bf16 = [&]() {
-                for (int e = row; e < 128 * (D / 8); e += 128) {
+                for (int e = half * 128 + row; e < 128 * (D / 8); e += 256) {
                     const int r = e / (D / 8), c = e % (D / 8);
                     const uint4 x = r < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4*>(qt + (c / 8) * 16384 + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = x;
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
             float rf = 1.f;  // score factor of this thread's row
             // Q as e4m3 + e5m2 terms [128 rows][D B] each; D/8 lanes hold a row
             auto q_terms = [&]() {
-                for (int e = row; e < 128 * (D / 8); e += 128) {
+                for (int e = half * 128 + row; e < 128 * (D / 8); e += 256) {
                     const int r = e / (D / 8), c = e % (D / 8);
                     const uint4 x = r < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -328,9 +333,9 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                     *reinterpret_cast<uint2*>(qt + 128 * D + off) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
                     if (c == 0) kfac[r] = __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
                 }
-                named_bar_sync(1 + h, 128);
+                named_bar_sync(group, 256);
                 rf = kfac[row];
-                named_bar_sync(1 + h, 128);  // the table is the keys' from here on
+                named_bar_sync(group, 256);  // the table is the keys' from here on
             };
             auto q_ready = [&]() {
                 fence_proxy_async_smem();
@@ -347,19 +352,28 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                        (p.T == 64 ? ~0ull : (1ull << p.T) - 1ull);
             q_ready();
 
-            // Whether a wait ran out. The warps of an e4m3 row tile meet at barriers, so they leave together.
-            auto stop = [&]() {
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (E4M3 && softmax_any(1 + h, !ok)) ok = false;
-                return !ok;
-            };
             float m = 0.f;      // the reference: a maximum so far, log2 units; 0 while there is none
             uint64_t l2 = 0ull; // the row's sum, in two halves
             bool fresh = true;
             int u = 0, uexp = 0;
             while (true) {
+                // Warps that meet at barriers leave together when a wait ran out in one of them: e4m3, the row
+                // tile's at a vote of their own; bf16, the row's two at the vote of the maxima, which is
+                // taken a second time whenever the first is true, by a warp that does not know the slot too.
                 if (ok) ok = mbar_wait(&sfull[bar_of(h, it)], par_of(it), p.status, kTreeDetail | 0x28u);
-                if (stop()) break;
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if constexpr (E4M3) {
+                    if (vote_any(group, 256, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                } else if (!ok) {
+                    if (live) {
+                        vote_any(pair, 64, true);
+                        vote_any(pair, 64, true);
+                    }
+                    break;
+                }
                 tc_fence_after();
                 const int me = k.n % kTreeMeta;
                 const int4 mt = meta[me];
@@ -369,10 +383,14 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                     q_ready();
                     ++it;
                     ok = mbar_wait(&sfull[bar_of(h, it)], par_of(it), p.status, kTreeDetail | 0x29u);
-                    if (stop()) break;
+                    if (vote_any(group, 256, !ok)) {
+                        ok = false;
+                        break;
+                    }
                     tc_fence_after();
                 }
                 if (mt.x == kTileEnd) {
+                    if (!E4M3 && live && vote_any(pair, 64, false) && vote_any(pair, 64, false)) ok = false;
                     ++it;
                     k.next(p.nk);
                     break;
@@ -380,18 +398,18 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                 const bool draft = mt.x == kTileDraft;
                 const bool whole_tile = !draft && mt.y == 64 && mt.z == 64;
                 uint8_t* vt = vring + v.s * C::TILE;
-                if (!whole_tile) {  // what follows writes V's tile: it has landed
+                if (half == 0 && !whole_tile) {  // what follows writes V's tile: it has landed
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x2Bu));
                 }
-                // V rows that do not count must not meet P's zeros as a NaN: each row tile's threads clear them
-                // before their own P (the same zeros twice)
-                if (!draft && !whole_tile && (row & 63) >= (row < 64 ? mt.y : mt.z)) {
+                // V rows that do not count must not meet P's zeros as a NaN: each row tile clears them before its
+                // own P (two row tiles: the same zeros twice)
+                if (half == 0 && !draft && !whole_tile && (row & 63) >= (row < 64 ? mt.y : mt.z)) {
                     for (int c = 0; c < C::ROW / 16; ++c) {
                         uint8_t* z = vt + (E4M3 ? row * D + 16 * c : (c / 8) * 16384 + row * 128 + 16 * (c % 8));
                         *reinterpret_cast<uint4*>(z) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
-                if (draft && row < p.tp) {
+                if (half == 0 && draft && row < p.tp) {
                     // a drafted value that is not finite would reach every token through 0 * x: it is taken out
                     // here (by whichever row tile comes first) and given to the tokens that attend it at the end
                     uint32_t bad = 0;
@@ -420,7 +438,6 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                         kf *= rf;
                         // the tile's factors, one key a thread; the unit is set by the largest V exponent
                         const bool counts = (row & 63) < (row < 64 ? mt.y : mt.z);
-                        const uint32_t ek = counts ? exps[me * 256 + row] : 0u;
                         const uint32_t four = *reinterpret_cast<const uint32_t*>(exps + me * 256 + 128 + 4 * lane);
                         int top = 0;
 #pragma unroll
@@ -435,16 +452,19 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                             if (!fresh) uf = pow2i(max(-126, u - un));
                             u = un;
                         }
-                        const int ev = counts ? exps[me * 256 + 128 + row] : 0;
-                        kfac[row] = __uint_as_float(ek << 23);
-                        // a row of exponent 255 stands for NaN (its bytes are zero)
-                        vfac[row] = __uint_as_float(ev == 255 ? 0x7FFFFFFFu : static_cast<uint32_t>(max(ev - u, 1)) << 23);
-                        named_bar_sync(1 + h, 128);
+                        if (half == 0) {
+                            const uint32_t ek = counts ? exps[me * 256 + row] : 0u;
+                            kfac[row] = __uint_as_float(ek << 23);
+                        } else {  // a row of exponent 255 stands for NaN (its bytes are zero)
+                            const int ev = counts ? exps[me * 256 + 128 + row] : 0;
+                            vfac[row] = __uint_as_float(ev == 255 ? 0x7FFFFFFFu : static_cast<uint32_t>(max(ev - u, 1)) << 23);
+                        }
+                        named_bar_sync(group, 256);
                     }
                 }
                 const uint32_t ts = tm + lanes + bar_of(h, it) * 128;
                 const uint32_t to = tm + lanes + C::O_COL + h * 128;
-                const int ncol = draft ? p.tp : 128;
+                const int cb = 64 * half, ce = draft ? (half == 0 ? p.tp : 0) : cb + 64;  // this warp's columns
                 const uint64_t kf2 = f2_pack(kf, kf);
                 // 32 columns of S as scores (log2 units, -inf where masked)
                 auto scores = [&](int c0, uint64_t (&x)[16]) {
@@ -478,7 +498,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                 if (live) {
                     float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < ncol; c0 += 32) {
+                    for (int c0 = cb; c0 < ce; c0 += 32) {
                         uint64_t x[16];
                         scores(c0, x);
 #pragma unroll
@@ -490,9 +510,16 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                             t1 = fmax3(t1, d, e);
                         }
                     }
-                    const float top = fmaxf(t0, t1);
+                    float top = fmaxf(t0, t1);
                     const bool over = fresh || top > m + C::LAZY || uf != 1.f;
-                    if (__any_sync(0xFFFFFFFFu, over)) {
+                    if (vote_any(pair, 64, over)) {
+                        if (!E4M3 && vote_any(pair, 64, false)) {
+                            ok = false;
+                            break;
+                        }
+                        *mine_x = top;
+                        named_bar_sync(pair, 64);
+                        top = fmaxf(top, *other_x);
                         // a row with nothing so far keeps 0 (its scores are all -inf and give 0)
                         const float now = fresh ? (top == -INFINITY ? 0.f : top) : fmaxf(m, top);
                         const float a = fresh || now == m ? 1.f : fast_exp2(m - now);
@@ -506,7 +533,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                             }
                             const float f = a * uf;
 #pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 32) {
+                            for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {  // half of O's columns each
                                 uint32_t w[32];
                                 tmem_ld32(to + c0, w);
                                 tmem_wait_ld();
@@ -522,7 +549,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                     const float pf = E4M3 && draft ? pow2i(min(127, max(-126, -u))) : 1.f;
                     const uint64_t pf2 = f2_pack(pf, pf);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < ncol; c0 += 32) {
+                    for (int c0 = cb; c0 < ce; c0 += 32) {
                         uint64_t x[16];
                         scores(c0, x);
                         uint64_t s0 = 0ull, s1 = 0ull;
@@ -581,7 +608,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                 fresh = false;
                 tc_fence_before();
                 fence_proxy_async_smem();
-                if (E4M3 && !draft) named_bar_sync(1 + h, 128);  // the table has been read
+                if (E4M3 && !draft) named_bar_sync(group, 256);  // the table has been read
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pfull[bar_of(h, pt)]);
                 ++it;
@@ -601,16 +628,18 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
             if (live) {
                 float la, lb;
                 f2_unpack(l2, la, lb);
-                const float l = la + lb;
+                *mine_x = la + lb;
+                named_bar_sync(pair, 64);
+                const float l = half == 0 ? *mine_x + *other_x : *other_x + *mine_x;  // the same order in both
                 const float uo = E4M3 ? pow2i(min(127, max(-126, u))) : 1.f;
                 const float f = whole ? (l == 0.f ? 0.f : uo / l) : uo;
                 const bool mine_row = row < nrows;
                 const int kvh = p.per_qhead ? hs / p.g : hs;
                 const __nv_bfloat16* dv = p.DV + (static_cast<int64_t>(b) * p.Hkv + kvh) * p.T * D;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
                     uint32_t w[32];
-                    if (pt > 0 && !fresh) {
+                    if (!fresh) {
                         tmem_ld32(tm + lanes + C::O_COL + h * 128 + c0, w);
                         tmem_wait_ld();
                     } else {
@@ -645,7 +674,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                         }
                     }
                 }
-                if (mine_row) {
+                if (mine_row && half == 0) {
                     if (whole) {
                         if (p.lse != nullptr)
                             p.lse[out0 + base + at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
@@ -658,7 +687,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
             tc_fence_before();
             // the flags of the next piece: nobody reads the ones of the piece before any more (its successor's Q
             // was announced by every row tile)
-            if (h == 0 && row < 2) dflag[(piece + 1) & 1][row] = 0;
+            if (h == 0 && half == 0 && row < 2) dflag[(piece + 1) & 1][row] = 0;
             ++piece;
             pos += u1 - unit;
             unit = 0;
@@ -666,7 +695,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
         }
     }
     __syncthreads();
-    if (warp == 4 * NM + 1) {
+    if (warp == 8 * NM + 1) {
         tc_fence_after();
         tmem_dealloc(tm, 512);
     }

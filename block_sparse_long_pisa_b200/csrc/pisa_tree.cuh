@@ -137,16 +137,16 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t two) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
-// Barrier over a softmax warpgroup's threads; true if `x` holds in any of them.
-__device__ __forceinline__ bool softmax_any(uint32_t bar, bool x) {
+// Barrier `bar` over `count` threads (whole warps); true if `x` holds in any of them.
+__device__ __forceinline__ bool vote_any(uint32_t bar, uint32_t count, bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(x)), "r"(bar)
+        : "r"(static_cast<uint32_t>(x)), "r"(bar), "r"(count)
         : "memory");
     return r != 0;
 }
