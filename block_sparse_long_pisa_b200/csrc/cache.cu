@@ -273,21 +273,12 @@ __global__ void __launch_bounds__(128) cache_block_mean_kernel(const CachePyrami
     e4m3_block_mean<D>(p.K + row * D, p.e + row, p.blk, p.pyr + (plane * p.plane_rows + j) * D);
 }
 
-// The nodes of levels l0 .. L - 1 over the blocks [b_lo, b_hi) of one plane per CTA, level after level;
-// with LEVEL0 (few new blocks) the CTA's warps form the level-0 means first, and the whole append is
-// one launch.
-template <int D, bool LEVEL0>
+// The nodes of levels l0 .. L - 1 over the blocks [b_lo, b_hi) of one plane per CTA, level after level.
+template <int D>
 __global__ void __launch_bounds__(256) cache_pyramid_kernel(const CachePyramidParams p, int l0) {
     const int64_t plane = blockIdx.x;
     float* out = p.pyr + plane * p.plane_rows * D;
-    if constexpr (LEVEL0) {
-        for (int j = p.b_lo + (threadIdx.x >> 5); j < p.b_hi; j += blockDim.x >> 5) {
-            const int64_t row = plane * p.N + static_cast<int64_t>(j) * p.blk;
-            e4m3_block_mean<D>(p.K + row * D, p.e + row, p.blk, out + static_cast<int64_t>(j) * D);
-        }
-    } else {
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // the level-0 grid is complete
-    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the grid before is complete
     int64_t width = 1;
     for (int l = 1; l < l0; ++l) width *= p.factor;
     for (int l = l0; l < p.L; ++l) {
@@ -302,6 +293,49 @@ __global__ void __launch_bounds__(256) cache_pyramid_kernel(const CachePyramidPa
                 node_mean4(below + 4 * q, 0, D, c, p.factor, p.lsize[l - 1], width, p.n0);
         }
         width = wl;
+    }
+}
+
+// A whole append of few blocks in one launch, one plane per CTA. What is older than the append and still
+// counts, the siblings to the left of the first new node of every level, is fetched into shared memory
+// while the level-0 means are formed, so the levels above follow from shared memory alone. `lo[l]`: first
+// row of level l held (the first new node's leftmost sibling), `at[l]`: where its rows begin.
+struct AppendRows {
+    int32_t lo[PISA_MAX_LEVELS], hi[PISA_MAX_LEVELS], fresh[PISA_MAX_LEVELS], at[PISA_MAX_LEVELS];
+};
+template <int D>
+__global__ void __launch_bounds__(256) cache_append_kernel(const CachePyramidParams p, const AppendRows a) {
+    extern __shared__ __align__(16) float rows[];
+    const int64_t plane = blockIdx.x;
+    float* out = p.pyr + plane * p.plane_rows * D;
+    const int warp = threadIdx.x >> 5;
+    for (int l = 0; l < p.L; ++l) {
+        for (int e = threadIdx.x; e < (a.fresh[l] - a.lo[l]) * (D / 4); e += blockDim.x)
+            reinterpret_cast<float4*>(rows + a.at[l] * D)[e] =
+                reinterpret_cast<const float4*>(out + (static_cast<int64_t>(p.loff[l]) + a.lo[l]) * D)[e];
+    }
+    for (int j = p.b_lo + warp; j < p.b_hi; j += blockDim.x >> 5) {
+        const int64_t at = plane * p.N + static_cast<int64_t>(j) * p.blk;
+        e4m3_block_mean<D>(p.K + at * D, p.e + at, p.blk, rows + (a.at[0] + j - a.lo[0]) * D);
+    }
+    int64_t width = 1;
+    for (int l = 0; l < p.L; ++l) {
+        __syncthreads();
+        const int n = a.hi[l] - a.fresh[l];
+        float* level = rows + a.at[l] * D;
+        float* dst = out + (static_cast<int64_t>(p.loff[l]) + a.fresh[l]) * D;
+        for (int e = threadIdx.x; e < n * (D / 4); e += blockDim.x) {
+            const int c = a.fresh[l] + e / (D / 4), q = e % (D / 4);
+            float4 v;
+            if (l == 0) {
+                v = *reinterpret_cast<const float4*>(level + (c - a.lo[0]) * D + 4 * q);
+            } else {
+                v = node_mean4(rows + a.at[l - 1] * D + 4 * q, a.lo[l - 1], D, c, p.factor, p.lsize[l - 1], width, p.n0);
+                *reinterpret_cast<float4*>(level + (c - a.lo[l]) * D + 4 * q) = v;
+            }
+            reinterpret_cast<float4*>(dst)[e] = v;
+        }
+        if (l > 0) width *= p.factor;
     }
 }
 
@@ -334,17 +368,34 @@ bool launch_cache_read(const CacheParams& p, int D, bool e4m3, cudaStream_t st) 
     return D == 64 ? launch_cache_rows<64>(p, e4m3, false, st) : launch_cache_rows<128>(p, e4m3, false, st);
 }
 
-// New blocks per plane up to which an append is one launch (a plane's 8 warps take one block each);
-// past it the level-0 means get a grid of their own, whose warps fill the SMs.
+// New blocks per plane up to which an append is one launch (a plane's 8 warps take one block each), if the
+// rows it holds fit this much shared memory; past it the level-0 means get a grid of their own, whose
+// warps fill the SMs. (One new block in 64 x 8 planes of 256 blocks: 11.4 us when every level read the one
+// below from global memory.)
 constexpr int kCachePyramidOneLaunch = 8;
+constexpr size_t kCacheAppendSmem = 48 * 1024;
 
 template <int D>
 static bool launch_cache_pyramid_d(const CachePyramidParams& p, cudaStream_t st, int32_t* launches) {
     if (p.b_hi - p.b_lo <= kCachePyramidOneLaunch) {
-        cache_pyramid_kernel<D, true><<<p.planes, 256, 0, st>>>(p, 1);
-        if (cudaGetLastError() != cudaSuccess) return false;
-        ++*launches;
-        return true;
+        AppendRows a{};
+        int64_t total = 0, width = 1;
+        for (int l = 0; l < p.L; ++l) {
+            a.fresh[l] = static_cast<int32_t>(p.b_lo / width);
+            a.hi[l] = static_cast<int32_t>((p.b_hi - 1) / width + 1);
+            a.lo[l] = l + 1 < p.L ? a.fresh[l] / p.factor * p.factor : a.fresh[l];
+            a.at[l] = static_cast<int32_t>(total);
+            total += a.hi[l] - a.lo[l];
+            width *= p.factor;
+        }
+        if (total * D * sizeof(float) <= kCacheAppendSmem) {
+            // a warp per new block, two at least: many planes of one block each then fit the SMs at once
+            const int threads = p.b_hi - p.b_lo <= 2 ? 64 : 256;
+            cache_append_kernel<D><<<p.planes, threads, total * D * sizeof(float), st>>>(p, a);
+            if (cudaGetLastError() != cudaSuccess) return false;
+            ++*launches;
+            return true;
+        }
     }
     int l0 = 1;  // first level that the second launch forms
     if (p.L >= 2 && p.factor <= 64) {
@@ -378,7 +429,7 @@ static bool launch_cache_pyramid_d(const CachePyramidParams& p, cudaStream_t st,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, cache_pyramid_kernel<D, false>, p, l0) != cudaSuccess) return false;
+    if (cudaLaunchKernelEx(&cfg, cache_pyramid_kernel<D>, p, l0) != cudaSuccess) return false;
     ++*launches;
     return true;
 }
