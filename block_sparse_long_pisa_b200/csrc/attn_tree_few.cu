@@ -1,5 +1,5 @@
 // Tree attention for few rows: at most 16 drafted-token-and-head rows per selection row (one token of a
-// group of four or eight heads is 4 or 8). The function, the cut into runs and the treatment of the
+// group of four or eight heads is 4 or 8), or two tiles of such (e4m3, up to 32 rows). The function, the cut into runs and the treatment of the
 // drafted tokens are those of attn_tree.cu; here nothing but the bytes of the cache should count.
 //
 // Bound: the bytes of the cache, each read once. One warp takes 16 keys of every unit of 64 on its own,
@@ -340,14 +340,14 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
     // ---------------------------------------------------- consumers
     const int r = lane >> 2, q4 = lane & 3, mi = lane >> 3, mr = lane & 7;
     const int key0 = 16 * warp;         // this warp's keys of a unit
-    const int rows = p.gh * p.T;
     while (pos < end) {
         const int b = static_cast<int>(tile / p.rows_per_seq);
         const int rem = static_cast<int>(tile % p.rows_per_seq);
-        const int hs = rem / p.mt;      // one row tile per selection row (mt = 1)
+        const int hs = rem / p.mt, base = (rem % p.mt) * p.rpt;  // the row tile's rows base .. of the selection row's
+        const int rows = min(p.rpt, p.gh * p.T - base);
         const int units = tree_units(p, tree_len(p, b));
         const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
-        const int64_t out0 = (static_cast<int64_t>(b) * p.Hq + hs * p.gh) * p.T;  // first output row
+        const int64_t out0 = (static_cast<int64_t>(b) * p.Hq + hs * p.gh) * p.T + base;  // first output row
 
         FewState<D, NT> st;
 #pragma unroll
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int row = 8 * t + 2 * q4 + e;
-                            mk[t][e] = row < rows ? static_cast<uint32_t>(__ldg(p.mask + static_cast<int64_t>(b) * p.T + row % p.T) & live) : 0u;
+                            mk[t][e] = row < rows ? static_cast<uint32_t>(__ldg(p.mask + static_cast<int64_t>(b) * p.T + (base + row) % p.T) & live) : 0u;
                         }
                         x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
                     }

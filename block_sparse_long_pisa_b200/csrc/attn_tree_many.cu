@@ -1,22 +1,28 @@
-// Tree attention for many rows: more than 32 drafted-token-and-head rows per selection row. The function,
-// the cut into runs and the treatment of the drafted tokens are those of attn_tree.cu; here the tensor
-// cores and the exponentials count as much as the bytes.
+// Tree attention for many rows: more than 16 drafted-token-and-head rows per selection row. The function and
+// the cut into runs are in attn_tree.cu; here the tensor cores and the exponentials count as much as the
+// bytes.
 //
-// Rows on the M side, 128 to a tile, one or two tiles in a CTA: S = Q K^T and O = P V with P read from
-// TMEM, so a score costs no shared memory at all (with the keys on the M side, attn_tree.cu, K and V are
-// fetched as the 128-lane operand for every 96 rows, the values transposed at half the rate, and P goes
-// through shared memory: 363 us for trees of 48 tokens of four heads over 8 ragged bf16 caches). A
-// row belongs to two softmax threads, one for each half of a tile's keys (one thread for all of them made the
-// softmax the longer side of every tile: 314 us); the two warps meet in one vote a tile.
+// Rows on the M side, 128 to a tile, one or two tiles in a CTA: S = Q K^T and O = P V with tcgen05, P read
+// from TMEM, so a score costs no shared memory at all. (Keys on the M side, S^T = K Q^T and O^T = V^T P^T with
+// 32 or 96 rows on N, was built first: K and V are then fetched as the 128-lane operand for every row tile,
+// the values transposed at half the rate, and P goes through shared memory; 363 us for trees of 48 tokens of
+// four heads over 8 ragged bf16 caches, 299 us this way.) A row belongs to two softmax threads, one for each
+// half of a tile's keys; the two warps meet in one vote a tile.
 //
 // A tile is 128 keys (two units of the cache, or the drafted tokens). Two passes over S in TMEM: the row's
-// maximum (the kept one moves when a score exceeds it by 2^LAZY, and O with it, by the two warps), then
+// maximum (the kept one moves when a score exceeds it by 2^kManyLazy, and O with it, by the two warps), then
 // the probabilities, written as operand A of P V over the columns of S that have been read. Order of the
 // MMA lane with two row tiles: S(0, g), P V(1, g - 1), S(1, g), P V(0, g): the softmax of one runs under the
 // products of the other; with one row tile S has two buffers and the order is S(g), P V(g - 1).
 //
-// e4m3: Q as e4m3 + e5m2 terms, P as three e5m2 terms, exponents as in attn_tree.cu; the key's two exponent
-// factors come from a table that the warps of a row tile fill for each tile of keys.
+// An e4m3 cache is turned into bf16 tiles on the way in: an e4m3 value times a power of two is a bf16 value
+// (rounded once below bf16's smallest normal), and everything after is the same. For each ring one warp fetches
+// the bytes, 32 rows a stage, and two or four converter warps write the swizzled tiles, some 65 instructions for
+// 512 values. That is what bounds this form (64 caches of 16K rows, 64 blocks of 128 each, tokens of four heads,
+// against bf16: 16 tokens 357 us, 252 us; 64 tokens 664 us, 537 us), together with the instruction cache: with
+// the converters' loop unrolled four times and a copy of it for K and one for V, 32 tokens took 790 us and not
+// 392 us. (With e4m3 operands in the products instead, P and Q need two and three 8-bit terms and every score a
+// factor from a table: 469 us for the 16 tokens.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -26,33 +32,252 @@
 
 namespace pisa {
 
+constexpr int kManyStages = 8;     // e4m3: most stages of a ring
+constexpr int kManySlots = 2;      // e4m3: slots of a ring
+constexpr float kManyLazy = 8.f;    // log2 units a score may exceed the kept maximum by
+
 template <int D, bool E4M3, int NM>
 struct ManyCfg {
-    static constexpr int ROW = E4M3 ? D : 2 * D;
-    static constexpr int TILE = 128 * ROW;               // one slot of a ring
-    static constexpr int EXPS = E4M3 ? 256 : 0;
-    static constexpr int QB = 128 * 2 * D;               // one row tile of Q: bf16, or its two 8-bit terms
-    static constexpr int FACT = E4M3 ? 1024 : 0;         // factors of 128 keys: K's, then V's
-    static constexpr int FIXED = 1024 + NM * (QB + FACT + 1024) + kTreeMeta * EXPS;  // 1024: [half][row] exchange
+    static constexpr int TILE = 128 * 2 * D;             // one slot of a ring: K or V of a tile, bf16
+    static constexpr int QB = 128 * 2 * D;               // one row tile of Q
+    static constexpr int FIXED = 1024 + NM * (QB + 1024);  // 1024: [half][row] exchange
     static constexpr int RM = 128 * NM;
-    static constexpr int THREADS = 256 * NM + 64;
+    // e4m3: converters of a ring, rows of a stage
+    static constexpr int NC = NM == 2 ? 2 : 4, SR = 32, STAGE = SR * D + SR;
+    static constexpr int THREADS = 256 * NM + 32 + (E4M3 ? 64 + 64 * NC : 32);
     static constexpr int O_COL = 256;                    // S: two of 128 columns (row tiles, or buffers)
-    static constexpr float LAZY = E4M3 ? 4.f : 8.f;      // log2 units a score may exceed the kept maximum by
 };
 
-// D[tmem] (+)= A[tmem] * B[smem]: 8-bit A, four values to a column.
-__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+// The producer warp (bf16): keeps the K and the V ring full by TMA. Every entry (a tile, or the end of a
+// piece) takes a K slot and describes itself in meta[entry % kTreeMeta]; a tile takes a V slot too. K and V
+// of a cache tile: [D / 64][128 rows][128 B]; of the drafted tokens: [D / 64][64 rows][128 B].
+template <int D>
+__device__ __forceinline__ void many_producer(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                              const CUtensorMap& tmDK, const CUtensorMap& tmDV, uint8_t* ring,
+                                              uint8_t* vring, uint64_t* kfull, uint64_t* kempty, uint64_t* vfull,
+                                              uint64_t* vempty, int4* meta, int64_t pos, int64_t end, int64_t tile,
+                                              int unit) {
+    constexpr int TILE = 128 * 2 * D;
+    const int lane = threadIdx.x & 31;
+    RingAt k, v;
+    bool ok = true;
+    if (lane == 0) {
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+        prefetch_tmap(&tmDK);
+        prefetch_tmap(&tmDV);
+    }
+    auto issue = [&](int kind, int64_t plane, int len, int a0, int a1) {
+        if (lane == 0) {
+            ok = k.n < p.nk || mbar_wait(&kempty[k.s], k.par ^ 1u, p.status, kTreeDetail | 0x21u);
+            if (ok) {
+                uint8_t* kt = ring + k.s * TILE;
+                uint64_t* kb = &kfull[k.s];
+                const int halves = a1 >= 0 ? 2 : 1;
+                const int dbytes = p.tp * 2 * D, dy = static_cast<int>(plane * p.T);
+                meta[k.n % kTreeMeta] = make_int4(kind, min(64, len - a0), a1 >= 0 ? min(64, len - a1) : 0, 0);
+                if (kind == kTileEnd) {
+                    mbar_arrive(kb);
+                } else if (kind == kTileDraft) {
+                    mbar_arrive_expect_tx(kb, dbytes);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) tma_load_2d(kt + c * 8192, &tmDK, 64 * c, dy, kb);
+                } else {
+                    mbar_arrive_expect_tx(kb, halves * TILE / 2);
+                    for (int h = 0; h < halves; ++h) {
+                        const int y = static_cast<int>(plane * p.cap + (h == 0 ? a0 : a1));
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) tma_load_2d(kt + c * 16384 + h * 8192, &tmK, 64 * c, y, kb);
+                    }
+                }
+                k.next(p.nk);
+                if (kind != kTileEnd) {
+                    ok = v.n < p.nv || mbar_wait(&vempty[v.s], v.par ^ 1u, p.status, kTreeDetail | 0x22u);
+                    if (ok) {
+                        uint8_t* vt = vring + v.s * TILE;
+                        uint64_t* vb = &vfull[v.s];
+                        if (kind == kTileDraft) {
+                            mbar_arrive_expect_tx(vb, dbytes);
+#pragma unroll
+                            for (int c = 0; c < D / 64; ++c) tma_load_2d(vt + c * 8192, &tmDV, 64 * c, dy, vb);
+                        } else {
+                            mbar_arrive_expect_tx(vb, halves * TILE / 2);
+                            for (int h = 0; h < halves; ++h) {
+                                const int y = static_cast<int>(plane * p.cap + (h == 0 ? a0 : a1));
+#pragma unroll
+                                for (int c = 0; c < D / 64; ++c) tma_load_2d(vt + c * 16384 + h * 8192, &tmV, 64 * c, y, vb);
+                            }
+                        }
+                        v.next(p.nv);
+                    }
+                }
+            }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    };
+    tree_entries(p, pos, end, tile, unit, true, ok, issue);
+    // every copy lands before the block ends, also when another role gave up (earlier uses of a slot were
+    // complete before it was filled again)
+    if (lane == 0) {
+        for (int i = 0; i < p.nk && i < k.n; ++i) {
+            k.s = k.s == 0 ? p.nk - 1 : k.s - 1;
+            if (k.s == p.nk - 1) k.par ^= 1u;
+            if (!mbar_wait(&kfull[k.s], k.par, p.status, kTreeDetail | 0x23u)) break;
+        }
+        for (int i = 0; i < p.nv && i < v.n; ++i) {
+            v.s = v.s == 0 ? p.nv - 1 : v.s - 1;
+            if (v.s == p.nv - 1) v.par ^= 1u;
+            if (!mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x24u)) break;
+        }
+    }
 }
-// kind::f8f6f4, A e4m3 (0) or e5m2 (1), B e4m3, M = 128
-__host__ __device__ constexpr uint32_t idesc_f8_a(int n, int a_type, int b_mn) {
-    return (1u << 4) | (static_cast<uint32_t>(a_type) << 7) | (static_cast<uint32_t>(b_mn) << 16) |
-           (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+
+// e4m3: for each ring, stages between the cache and the ring, SR rows with their exponents.
+enum : int { kStepEnd = kTileEnd, kStepRows = kTileCache, kStepDraft = kTileDraft, kStepStop = 3 };
+struct ManyStages {
+    uint8_t* bytes;              // [p.ns][SR][D]
+    uint8_t* exps;               // [p.ns][SR]
+    uint64_t *full, *empty;
+    int4* step;                  // kind | part of its tile << 4; keys of the two halves; use of the ring; plane
+};
+
+// The warp that fills the stages of the K ring or (is_v) of the V ring by bulk copy.
+template <int D, int SR, int NC>
+__device__ __forceinline__ void many_fetch(const TreeParams& p, const CUtensorMap* tmC, bool is_v, const ManyStages& g, int64_t pos, int64_t end,
+                                           int64_t tile, int unit) {
+    const int lane = threadIdx.x & 31;
+    const uint8_t* exps = is_v ? p.v_exp : p.k_exp;
+    RingAt r;
+    int use = 0;  // of the ring, by the entry at hand
+    bool ok = true;
+    auto step = [&](int what, int keys, int plane, int64_t row, bool copy) {  // lane 0
+        ok = ok && (r.n < p.ns || mbar_wait(&g.empty[r.s], r.par ^ 1u, p.status, kTreeDetail | (is_v ? 0x31u : 0x30u)));
+        if (!ok) return;
+        g.step[r.s] = make_int4(what, keys, use, plane);
+        if (copy) {
+            mbar_arrive_expect_tx(&g.full[r.s], SR * D + SR);
+            tma_load_2d(g.bytes + r.s * SR * D, tmC, 0, static_cast<int>(row), &g.full[r.s]);
+            bulk_load(g.exps + r.s * SR, exps + row, SR, &g.full[r.s]);
+        } else {
+            mbar_arrive(&g.full[r.s]);
+        }
+        r.next(p.ns);
+    };
+    auto issue = [&](int kind, int64_t plane, int len, int a0, int a1) {
+        if (is_v && kind == kTileEnd) return;
+        if (lane == 0) {
+            const int n0 = min(64, len - a0), n1 = a1 >= 0 ? min(64, len - a1) : 0;
+#pragma unroll 1
+            for (int i = 0; i < 128 / SR; ++i) {
+                const int r0 = i * SR;  // first row of the tile
+                step(kind | i << 4, n0 | n1 << 16, static_cast<int>(plane), plane * p.cap + (r0 < 64 ? a0 + r0 : a1 + r0 - 64),
+                     kind == kTileCache && (r0 < 64 ? r0 < n0 : r0 - 64 < n1));
+            }
+            ++use;
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    };
+    tree_entries(p, pos, end, tile, unit, !is_v, ok, issue);
+    if (lane == 0) {
+#pragma unroll 1
+        for (int i = 0; i < NC; ++i) step(kStepStop, 0, 0, 0, false);
+        // every copy lands before the block ends, also when another role gave up
+        for (int i = 0; i < p.ns && i < r.n; ++i) {
+            r.s = r.s == 0 ? p.ns - 1 : r.s - 1;
+            if (r.s == p.ns - 1) r.par ^= 1u;
+            if (!mbar_wait(&g.full[r.s], r.par, p.status, kTreeDetail | (is_v ? 0x33u : 0x32u))) break;
+        }
+    }
+}
+
+// Converter warp cw of the NC that turn the stages into the bf16 tiles of the K ring or (is_v) of the V ring:
+// every NC-th step is its own (what a step costs beside its rows, 500 cycles, is then paid by one warp). Rows
+// that do not count become zeros. The drafted tokens are bf16 and come by TMA. Every entry has 128 / SR steps,
+// a multiple of NC, so that each warp takes part in every use of a slot and no parity of a barrier is passed
+// over; the ring's full barriers count one arrival a step.
+template <int D, int SR, int NC>
+__device__ __forceinline__ void many_converter(const TreeParams& p, const CUtensorMap* tmD, bool is_v, int cw,
+                                               const ManyStages& g, uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                               int4* meta) {
+    constexpr int TILE = 128 * 2 * D;
+    constexpr int LPR = D / 16, RPI = 32 / LPR;          // lanes of a row, rows a warp takes at a time
+    static_assert(128 / SR % NC == 0, "each warp sees every use");
+    const int lane = threadIdx.x & 31, chunk = lane % LPR, rsub = lane / LPR;
+    int drafts = -1;                                     // this warp's last use of the ring for drafted tokens
+    bool ok = true;
+    if (lane == 0) prefetch_tmap(tmD);
+    RingAt r;
+    for (int i = 0; i < cw; ++i) r.next(p.ns);
+    while (true) {
+        ok = mbar_wait(&g.full[r.s], r.par, p.status, kTreeDetail | (is_v ? 0x35u : 0x34u));
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        const int4 what = g.step[r.s];
+        const int kind = what.x & 15, part = what.x >> 4, use = what.z;
+        if (kind == kStepStop) {
+            // `use` is the number of uses: the slot's last one (its parity says whether all before are complete)
+            if (drafts >= 0) drafts = use - 1 - (use - 1 - drafts) % kManySlots;
+            break;
+        }
+        const int slot = use % kManySlots;
+        ok = use < kManySlots ||
+             mbar_wait(&empty[slot], (use / kManySlots & 1) ^ 1u, p.status, kTreeDetail | (is_v ? 0x22u : 0x21u));
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (lane == 0 && part == 0 && !is_v)
+            meta[use % kTreeMeta] = make_int4(kind, what.y & 0xFFFF, what.y >> 16, 0);
+        uint8_t* t = ring + slot * TILE;
+        if (kind == kStepRows) {
+            const int r0 = part * SR, n = r0 < 64 ? what.y & 0xFFFF : (what.y >> 16) + 64;  // rows below n count
+            const uint8_t* src = g.bytes + r.s * SR * D;
+            const uint8_t* ex = g.exps + r.s * SR;
+#pragma unroll 1
+            for (int row = rsub; row < SR; row += RPI) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                uint32_t e = 0;
+                if (r0 + row < n) {
+                    x = *reinterpret_cast<const uint4*>(src + row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4));
+                    e = ex[row];
+                }
+                // seeeemmm as a bf16 with the exponent field eeee is the value times 2^-120, its subnormals too;
+                // times 2^(e - 7), which is no bf16 above e = 134: the rest comes after. 255: a NaN
+                const uint32_t f = e == 255u ? 0x7FC0u : (min(e, 134u) + 120u) << 7, f1 = f | (f << 16);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t y = __byte_perm(w[c / 2], 0u, (c & 1) ? 0x3424 : 0x1404);
+                    o[c] = bf16x2_mul((y & 0x80008000u) | ((y >> 4) & 0x07F007F0u), f1);
+                }
+                if (e > 134u && e < 255u) {  // a row of very large values
+                    const uint32_t f0 = (e - 134u + 127u) << 7, f2 = f0 | (f0 << 16);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) o[c] = bf16x2_mul(o[c], f2);
+                }
+                uint8_t* dst = t + (chunk / 4) * 16384 + (r0 + row) * 128;
+                const int c = 2 * (chunk % 4);
+                *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&g.empty[r.s]);
+            if (kind == kStepDraft && part == 0) {
+                drafts = use;
+                mbar_arrive_expect_tx(&full[slot], p.tp * 2 * D);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) tma_load_2d(t + c * 8192, tmD, 64 * c, what.w * p.T, &full[slot]);
+            } else {
+                mbar_arrive(&full[slot]);
+            }
+        }
+        for (int i = 0; i < NC; ++i) r.next(p.ns);
+    }
+    // the drafted tokens' copies land before the block ends, also when another role gave up
+    if (lane == 0 && drafts >= 0)
+        mbar_wait(&full[drafts % kManySlots], drafts / kManySlots & 1, p.status, kTreeDetail | (is_v ? 0x24u : 0x23u));
 }
 
 template <int D, bool E4M3, int NM>
@@ -64,12 +289,12 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* vring = ring + p.nk * C::TILE;
-    uint8_t* q_s = vring + p.nv * C::TILE;               // [row tile][QB]
-    float* fact = reinterpret_cast<float*>(q_s + NM * C::QB);          // [row tile][K 128, V 128]
-    float* xch = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(fact) + NM * C::FACT);  // [row tile][half][128]
-    uint8_t* exps = reinterpret_cast<uint8_t*>(xch) + NM * 1024;       // [entry][K 128, V 128]
+    uint8_t* q_s = vring + p.nv * C::TILE;               // [row tile][D / 64][128 rows][128 B]
+    float* xch = reinterpret_cast<float*>(q_s + NM * C::QB);  // [row tile][half][128]
+    uint8_t* stages = reinterpret_cast<uint8_t*>(xch) + NM * 1024;  // e4m3: of K, of V
     __shared__ __align__(8) uint64_t kfull[kTreeMaxSlots], kempty[kTreeMaxSlots], vfull[kTreeMaxSlots],
-        vempty[kTreeMaxSlots], sfull[2], pfull[2], pvdone[2], qfull, done;
+        vempty[kTreeMaxSlots], rfull[2][kManyStages], rempty[2][kManyStages], sfull[2], pfull[2], pvdone[2], qfull, done;
+    __shared__ int4 step[2][kManyStages];
     __shared__ int4 meta[kTreeMeta];  // kind, keys that count in the two halves
     __shared__ uint32_t tmem_slot, dflag[2][2];
 
@@ -83,13 +308,18 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
     tree_find(p, pos, tile, unit);
     if (tid == 0) {
         for (int i = 0; i < p.nk; ++i) {
-            mbar_init(&kfull[i], 1);
+            mbar_init(&kfull[i], E4M3 ? 128 / C::SR : 1);
             mbar_init(&kempty[i], 1);
         }
         for (int i = 0; i < p.nv; ++i) {
-            mbar_init(&vfull[i], 1);
+            mbar_init(&vfull[i], E4M3 ? 128 / C::SR : 1);
             mbar_init(&vempty[i], 1);
         }
+        for (int i = 0; i < p.ns; ++i)
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&rfull[x][i], 1);
+                mbar_init(&rempty[x][i], 1);
+            }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i], 8);
@@ -100,7 +330,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
         mbar_init(&done, 1);
         fence_barrier_init();
     }
-    if (warp == 8 * NM + 1) tmem_alloc(&tmem_slot, 512);
+    if (warp == 8 * NM) tmem_alloc(&tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -111,10 +341,26 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
     auto bar_of = [](int h, int n) { return NM == 2 ? h : n & 1; };
     auto par_of = [](int n) { return static_cast<uint32_t>((NM == 2 ? n : n >> 1) & 1); };
 
-    if (warp == 8 * NM) {
-        tree_producer<D, E4M3>(p, tmK, tmV, tmDK, tmDV, ring, vring, exps, kfull, kempty, vfull, vempty, meta, pos, end,
-                               tile, unit);
-    } else if (warp == 8 * NM + 1) {
+    if (warp > 8 * NM) {
+        // ------------------------------------------------ tiles
+        if constexpr (E4M3)
+        {
+            // one copy of the code for K and V: the roles' code together is more than the instruction cache holds
+            const int w = warp - 8 * NM - 1;
+            const bool is_v = w < 2 ? w == 1 : w - 2 >= C::NC;
+            const int x = is_v ? 1 : 0;
+            const int n = p.ns * C::SR;  // rows of a ring's stages; the bytes of both rings (each stage at a multiple
+                                         // of 1024, the swizzle's period), then the exponents
+            const ManyStages g = {stages + x * n * D, stages + 2 * n * D + x * n, rfull[x], rempty[x], step[x]};
+            if (w < 2)
+                many_fetch<D, C::SR, C::NC>(p, is_v ? &tmV : &tmK, is_v, g, pos, end, tile, unit);
+            else
+                many_converter<D, C::SR, C::NC>(p, is_v ? &tmDV : &tmDK, is_v, w - 2 - x * C::NC, g, is_v ? vring : ring,
+                                                is_v ? vfull : kfull, is_v ? vempty : kempty, meta);
+        } else {
+            many_producer<D>(p, tmK, tmV, tmDK, tmDV, ring, vring, kfull, kempty, vfull, vempty, meta, pos, end, tile, unit);
+        }
+    } else if (warp == 8 * NM) {
         // ------------------------------------------------ MMA
         if (lane == 0) {
             const uint32_t q0 = smem_u32(q_s);
@@ -122,132 +368,90 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
             int pn = 0, pit = 0;      // tiles whose P V was issued for every row tile; the S slot of the next one
             bool pend = false;        // P V of the tile before is still to be issued (two row tiles: for tile 1)
             bool pdraft = false;      // and that tile is the drafted tokens
-            bool fresh[2] = {true, true};  // the next P V begins O
+            uint32_t fresh = 3u;      // bit h: the next P V of row tile h begins O
             uint32_t qpar = 0;
             bool issued = false;
-            // S of row tile h from the K slot at hand
+            // S of row tile h from the K slot at hand. (Loops stay loops here: the roles' code together is more
+            // than the instruction cache holds, and what waits in this lane is seldom its own issue.)
             auto qk = [&](int h, bool draft) {
                 const uint32_t kt = smem_u32(ring + k.s * C::TILE), qt = q0 + h * C::QB;
                 const uint32_t d = tm + bar_of(h, it) * 128;
-                if (draft || !E4M3) {
-                    const uint32_t sub = draft ? 8192 : 16384;
-                    const uint64_t a = tree_desc(qt, 16, 1024, 2), b = tree_desc(kt, 16, 1024, 2);
-                    const uint32_t id = idesc_bf16_f32(128, draft ? p.tp : 128, 0, 0);
+                const uint32_t sub = draft ? 8192 : 16384;
+                const uint64_t a = smem_desc_sw128(qt, 16, 1024), b = smem_desc_sw128(kt, 16, 1024);
+                const uint32_t id = idesc_bf16_f32(128, draft ? p.tp : 128, 0, 0);
 #pragma unroll
-                    for (int n = 0; n < D / 16; ++n)
-                        mma_bf16_ss(d, desc_at(a, (n / 4) * 16384 + (n % 4) * 32), desc_at(b, (n / 4) * sub + (n % 4) * 32), id,
-                                    n > 0 ? 1u : 0u);
-                } else {
-                    const uint64_t a = D == 128 ? tree_desc(qt, 16, 1024, 2) : tree_desc(qt, 16, 512, 4);
-                    const uint64_t b = D == 128 ? tree_desc(kt, 16, 1024, 2) : tree_desc(kt, 16, 512, 4);
-#pragma unroll
-                    for (int n = 0; n < D / 32; ++n) {
-                        mma_f8_ss(d, desc_at(a, n * 32), desc_at(b, n * 32), idesc_f8_a(128, 0, 0), n > 0 ? 1u : 0u);
-                        mma_f8_ss(d, desc_at(a, 128 * D + n * 32), desc_at(b, n * 32), idesc_f8_a(128, 1, 0), 1u);
-                    }
-                }
+                for (int n = 0; n < D / 16; ++n)
+                    mma_bf16_ss(d, desc_at(a, (n / 4) * 16384 + (n % 4) * 32), desc_at(b, (n / 4) * sub + (n % 4) * 32), id,
+                                n > 0 ? 1u : 0u);
                 mma_commit(&sfull[bar_of(h, it)]);
             };
             // P V of row tile h for tile number n (S slot sit) from the V slot at hand
             auto pv = [&](int h, int n, int sit, bool draft) {
-                ok = mbar_wait(&pfull[bar_of(h, n)], par_of(n), p.status, kTreeDetail | 0x21u) &&
-                     mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x22u);
+                ok = mbar_wait(&pfull[bar_of(h, n)], par_of(n), p.status, kTreeDetail | 0x25u) &&
+                     mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x26u);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t vt = smem_u32(vring + v.s * C::TILE);
                 const uint32_t a = tm + bar_of(h, sit) * 128, d = tm + C::O_COL + h * 128;
-                if (draft || !E4M3) {
-                    const uint64_t b = tree_desc(vt, draft ? 8192 : 16384, 1024, 2);
-                    const int steps = draft ? p.tp / 16 : 8;
-                    for (int i = 0; i < steps; ++i)
-                        mma_bf16_ts(d, a + 32 * (i / 2) + 8 * (i % 2), desc_at(b, i * 2048), idesc_bf16_f32(128, D, 0, 1),
-                                    !fresh[h] || i > 0 ? 1u : 0u);
-                } else {
-                    const uint64_t b = D == 128 ? tree_desc(vt, 0, 1024, 2) : tree_desc(vt, 0, 512, 4);
+                const uint64_t b = smem_desc_sw128(vt, draft ? 8192 : 16384, 1024);
+                const int steps = draft ? p.tp / 16 : 8;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                        for (int t = 0; t < 3; ++t)
-                            mma_f8_ts(d, a + 32 * i + 8 * t, desc_at(b, i * 32 * D), idesc_f8_a(D, 1, 1),
-                                      !fresh[h] || i > 0 || t > 0 ? 1u : 0u);
-                    }
-                }
-                fresh[h] = false;
+                for (int i = 0; i < 8; ++i)
+                    if (i < steps) mma_bf16_ts(d, a + 32 * (i / 2) + 8 * (i % 2), desc_at(b, i * 2048), idesc_bf16_f32(128, D, 0, 1),
+                                i > 0 ? 1u : !(fresh >> h & 1u));
+                fresh &= ~(1u << h);
                 mma_commit(&pvdone[bar_of(h, n)]);
-            };
-            // the P V that is still to be issued (two row tiles: of tile 1), and with it the V slot's release
-            auto flush = [&]() {
-                if (!pend || !ok) return;
-                pv(NM - 1, pn, pit, pdraft);
-                if (!ok) return;
-                mma_commit(&vempty[v.s]);
-                v.next(p.nv);
-                ++pn;
-                pend = false;
-            };
-            auto announce = [&]() {  // an S slot without scores, after every product so far
-                issued = true;
-                mma_commit(&sfull[bar_of(0, it)]);
-                if (NM == 2) mma_commit(&sfull[1]);
-                ++it;
             };
             while (pos < end && ok) {
                 const int b = static_cast<int>(tile / p.rows_per_seq);
                 const int units = tree_units(p, tree_len(p, b));
                 const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
-                ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x23u);
+                ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x29u);
                 qpar ^= 1u;
-                fresh[0] = fresh[1] = true;
-                while (ok) {
-                    ok = mbar_wait(&kfull[k.s], k.par, p.status, kTreeDetail | 0x24u);
+                fresh = 3u;
+                bool over = false;
+                while (ok && !over) {
+                    ok = mbar_wait(&kfull[k.s], k.par, p.status, kTreeDetail | 0x2Cu);
                     if (!ok) break;
                     const int kind = meta[k.n % kTreeMeta].x;
                     const bool draft = kind == kTileDraft;
-                    if (kind == kTileEnd) {
-                        flush();
-                        if (ok) {
-                            announce();  // the softmax may read O
-                            mbar_arrive(&kempty[k.s]);
-                            k.next(p.nk);
-                        }
-                        break;
-                    }
-                    if (E4M3 && draft) {  // Q comes again, as bf16
-                        flush();
-                        if (!ok) break;
-                        announce();
-                        ok = mbar_wait(&qfull, qpar, p.status, kTreeDetail | 0x25u);
-                        qpar ^= 1u;
-                        if (!ok) break;
-                    }
-                    // S goes where an earlier tile's P is read from: two row tiles, the tile before's; one row
-                    // tile, that of two before
-                    const int back = NM == 2 ? 1 : 2;
-                    auto free_s = [&](int h) {
-                        if (tn >= back)
-                            ok = mbar_wait(&pvdone[bar_of(h, tn - back)], par_of(tn - back), p.status, kTreeDetail | 0x26u);
-                        tc_fence_after();
-                        return ok;
-                    };
+                    over = kind == kTileEnd;
                     issued = true;
-                    if (!free_s(0)) break;
-                    qk(0, draft);
-                    if constexpr (NM == 2) {
-                        flush();          // P V(1) of the tile before
-                        if (!ok || !free_s(1)) break;
-                        qk(1, draft);
-                        mma_commit(&kempty[k.s]);
-                        pv(0, tn, it, draft);
-                        if (!ok) break;
-                    } else {
-                        mma_commit(&kempty[k.s]);
-                        flush();
-                        if (!ok) break;
+                    // one step for each row tile: its S, then the P V that is due (two row tiles: of the other one)
+#pragma unroll 1
+                    for (int h = 0; h < (over ? 1 : NM) && ok; ++h) {
+                        if (!over) {
+                            // S goes where an earlier tile's P is read from: two row tiles, the tile before's; one
+                            // row tile, that of two before
+                            const int back = NM == 2 ? 1 : 2;
+                            if (tn >= back)
+                                ok = mbar_wait(&pvdone[bar_of(h, tn - back)], par_of(tn - back), p.status, kTreeDetail | 0x2Du);
+                            if (!ok) break;
+                            tc_fence_after();
+                            qk(h, draft);
+                            if (h == NM - 1) mma_commit(&kempty[k.s]);
+                        }
+                        const bool due = h == 0;  // of the tile before, the last product of its V slot
+                        if (due && !pend) continue;
+                        pv(due ? NM - 1 : 0, due ? pn : tn, due ? pit : it, due ? pdraft : draft);
+                        if (ok && due) {
+                            mma_commit(&vempty[v.s]);
+                            v.next(p.nv);
+                            ++pn;
+                            pend = false;
+                        }
                     }
-                    pend = true;
-                    pdraft = draft;
-                    pit = it;
-                    ++tn;
+                    if (!ok) break;
+                    if (over) {  // an S slot without scores, after every product so far: the softmax may read O
+                        mma_commit(&sfull[bar_of(0, it)]);
+                        if (NM == 2) mma_commit(&sfull[1]);
+                        mbar_arrive(&kempty[k.s]);
+                    } else {
+                        pend = true;
+                        pdraft = draft;
+                        pit = it;
+                        ++tn;
+                    }
                     ++it;
                     k.next(p.nk);
                 }
@@ -265,13 +469,11 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
         // ------------------------------------------------ softmax: a row of row tile h (TMEM lane), half of
         // a tile's keys
         const int h = (warp / 4) % NM, half = warp / (4 * NM), row = tid & 127;
-        const uint32_t pair = 1 + 4 * h + warp % 4, group = 9 + h;  // barriers of the row's two warps, of the row tile
+        const uint32_t pair = 1 + 4 * h + warp % 4;  // barrier of the row's two warps
         float* mine_x = xch + h * 256 + half * 128 + row;
         const float* other_x = xch + h * 256 + (1 - half) * 128 + row;
         const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
         const int rows = p.gh * p.T;
-        float* kfac = fact + h * 256;
-        float* vfac = kfac + 128;
         int it = 0, pt = 0, piece = 0;
         while (pos < end && ok) {
             const int b = static_cast<int>(tile / p.rows_per_seq);
@@ -288,86 +490,30 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
             const uint4* qg = reinterpret_cast<const uint4*>(p.Q + (out0 + first) * D);
             uint8_t* qt = q_s + h * C::QB;
 
-            // Q as bf16: [D / 64][128 rows][128 B], 128-byte swizzle
-            auto q_bf16 = [&]() {
-                for (int e = half * 128 + row; e < 128 * (D / 8); e += 256) {
-                    const int r = e / (D / 8), c = e % (D / 8);
-                    const uint4 x = r < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(qt + (c / 8) * 16384 + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = x;
-                }
-            };
-            float rf = 1.f;  // score factor of this thread's row
-            // Q as e4m3 + e5m2 terms [128 rows][D B] each; D/8 lanes hold a row
-            auto q_terms = [&]() {
-                for (int e = half * 128 + row; e < 128 * (D / 8); e += 256) {
-                    const int r = e / (D / 8), c = e % (D / 8);
-                    const uint4 x = r < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    float vv[8], top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        vv[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
-                        top = fmaxf(top, fabsf(vv[i]));
-                    }
-#pragma unroll
-                    for (int o = 1; o < D / 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                    // 2^(f - 127) brings the maximum to [224, 448): 448 = 1.75 * 2^8
-                    const uint32_t tb = __float_as_uint(top);
-                    const int f = min(253, 127 + 8 + 127 - static_cast<int>(tb >> 23) - ((tb & 0x7FFFFFu) > 0x600000u ? 1 : 0));
-                    const float sc = __uint_as_float(static_cast<uint32_t>(f) << 23);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float a = vv[2 * i] * sc, bb = vv[2 * i + 1] * sc;
-                        hi[i] = cvt_e4m3x2(a, bb);
-                        const float2 hh = e4m3x2_f32(hi[i]);
-                        lo[i] = cvt_e5m2x2(a - hh.x, bb - hh.y);
-                        // an infinity saturates the first term: the second makes the score a NaN
-                        if (isinf(a)) lo[i] = (lo[i] & 0xFF00u) | 0x7Fu;
-                        if (isinf(bb)) lo[i] = (lo[i] & 0x00FFu) | 0x7F00u;
-                    }
-                    const int ch = c / 2;
-                    const uint32_t off = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) + 8 * (c & 1)
-                                                  : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) + 8 * (c & 1);
-                    *reinterpret_cast<uint2*>(qt + off) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-                    *reinterpret_cast<uint2*>(qt + 128 * D + off) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-                    if (c == 0) kfac[r] = __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
-                }
-                named_bar_sync(group, 256);
-                rf = kfac[row];
-                named_bar_sync(group, 256);  // the table is the keys' from here on
-            };
-            auto q_ready = [&]() {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&qfull);
-            };
-            if constexpr (E4M3)
-                q_terms();
-            else
-                q_bf16();
+            // Q: [D / 64][128 rows][128 B], 128-byte swizzle
+            for (int e = half * 128 + row; e < 128 * (D / 8); e += 256) {
+                const int r = e / (D / 8), c = e % (D / 8);
+                const uint4 x = r < nrows ? __ldg(qg + e) : make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(qt + (c / 8) * 16384 + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = x;
+            }
             uint64_t bits = 0;  // the row's ancestors
             if (u1 == units && row < nrows)
                 bits = __ldg(p.mask + static_cast<int64_t>(b) * p.T + (first + row) % p.T) &
                        (p.T == 64 ? ~0ull : (1ull << p.T) - 1ull);
-            q_ready();
+            // the MMA lane saw the piece before to its end (the slot that ends a piece comes through it)
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&qfull);
 
             float m = 0.f;      // the reference: a maximum so far, log2 units; 0 while there is none
             uint64_t l2 = 0ull; // the row's sum, in two halves
             bool fresh = true;
-            int u = 0, uexp = 0;
             while (true) {
-                // Warps that meet at barriers leave together when a wait ran out in one of them: e4m3, the row
-                // tile's at a vote of their own; bf16, the row's two at the vote of the maxima, which is
-                // taken a second time whenever the first is true, by a warp that does not know the slot too.
+                // The row's two warps leave together when a wait ran out in one of them: the vote of the maxima
+                // is taken a second time whenever the first is true, by a warp that does not know the slot too.
                 if (ok) ok = mbar_wait(&sfull[bar_of(h, it)], par_of(it), p.status, kTreeDetail | 0x28u);
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                if constexpr (E4M3) {
-                    if (vote_any(group, 256, !ok)) {
-                        ok = false;
-                        break;
-                    }
-                } else if (!ok) {
+                if (!ok) {
                     if (live) {
                         vote_any(pair, 64, true);
                         vote_any(pair, 64, true);
@@ -375,22 +521,9 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const int me = k.n % kTreeMeta;
-                const int4 mt = meta[me];
-                if (E4M3 && mt.x == kTileDraft) {
-                    // this slot only says that the drafted tokens come: Q's buffer is free for the bf16 rows
-                    q_bf16();
-                    q_ready();
-                    ++it;
-                    ok = mbar_wait(&sfull[bar_of(h, it)], par_of(it), p.status, kTreeDetail | 0x29u);
-                    if (vote_any(group, 256, !ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                }
+                const int4 mt = meta[k.n % kTreeMeta];
                 if (mt.x == kTileEnd) {
-                    if (!E4M3 && live && vote_any(pair, 64, false) && vote_any(pair, 64, false)) ok = false;
+                    if (live && vote_any(pair, 64, false) && vote_any(pair, 64, false)) ok = false;
                     ++it;
                     k.next(p.nk);
                     break;
@@ -398,14 +531,14 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                 const bool draft = mt.x == kTileDraft;
                 const bool whole_tile = !draft && mt.y == 64 && mt.z == 64;
                 uint8_t* vt = vring + v.s * C::TILE;
-                if (half == 0 && !whole_tile) {  // what follows writes V's tile: it has landed
+                if (half == 0 && (draft || (!E4M3 && !whole_tile))) {  // what follows writes V's tile: it has landed
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x2Bu));
                 }
                 // V rows that do not count must not meet P's zeros as a NaN: each row tile clears them before its
                 // own P (two row tiles: the same zeros twice)
-                if (half == 0 && !draft && !whole_tile && (row & 63) >= (row < 64 ? mt.y : mt.z)) {
-                    for (int c = 0; c < C::ROW / 16; ++c) {
-                        uint8_t* z = vt + (E4M3 ? row * D + 16 * c : (c / 8) * 16384 + row * 128 + 16 * (c % 8));
+                if (!E4M3 && half == 0 && !draft && !whole_tile && (row & 63) >= (row < 64 ? mt.y : mt.z)) {
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint8_t* z = vt + (c / 8) * 16384 + row * 128 + 16 * (c % 8);
                         *reinterpret_cast<uint4*>(z) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
@@ -431,41 +564,10 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                     }
                     if (bad) atomicOr(&dflag[piece & 1][row >> 5], 1u << (row & 31));
                 }
-                float kf = p.scale_log2;   // times the key's factor
-                float uf = 1.f;            // what a new unit does to O
-                if constexpr (E4M3) {
-                    if (!draft) {
-                        kf *= rf;
-                        // the tile's factors, one key a thread; the unit is set by the largest V exponent
-                        const bool counts = (row & 63) < (row < 64 ? mt.y : mt.z);
-                        const uint32_t four = *reinterpret_cast<const uint32_t*>(exps + me * 256 + 128 + 4 * lane);
-                        int top = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int key = 4 * lane + i;
-                            if ((key & 63) < (key < 64 ? mt.y : mt.z)) top = max(top, static_cast<int>((four >> (8 * i)) & 0xFFu));
-                        }
-                        top = min(254, static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(top))));
-                        if (fresh || top > uexp) {
-                            uexp = top;
-                            const int un = max(kTreeUMin, top - 127 + static_cast<int>(C::LAZY) - 15);
-                            if (!fresh) uf = pow2i(max(-126, u - un));
-                            u = un;
-                        }
-                        if (half == 0) {
-                            const uint32_t ek = counts ? exps[me * 256 + row] : 0u;
-                            kfac[row] = __uint_as_float(ek << 23);
-                        } else {  // a row of exponent 255 stands for NaN (its bytes are zero)
-                            const int ev = counts ? exps[me * 256 + 128 + row] : 0;
-                            vfac[row] = __uint_as_float(ev == 255 ? 0x7FFFFFFFu : static_cast<uint32_t>(max(ev - u, 1)) << 23);
-                        }
-                        named_bar_sync(group, 256);
-                    }
-                }
                 const uint32_t ts = tm + lanes + bar_of(h, it) * 128;
                 const uint32_t to = tm + lanes + C::O_COL + h * 128;
                 const int cb = 64 * half, ce = draft ? (half == 0 ? p.tp : 0) : cb + 64;  // this warp's columns
-                const uint64_t kf2 = f2_pack(kf, kf);
+                const uint64_t kf2 = f2_pack(p.scale_log2, p.scale_log2);
                 // 32 columns of S as scores (log2 units, -inf where masked)
                 auto scores = [&](int c0, uint64_t (&x)[16]) {
                     uint32_t w[32];
@@ -474,14 +576,6 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         x[i] = f2_mul(f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), kf2);
-                    }
-                    if (E4M3 && !draft) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 f = *reinterpret_cast<const float4*>(kfac + c0 + 4 * i);
-                            x[2 * i] = f2_mul(x[2 * i], f2_pack(f.x, f.y));
-                            x[2 * i + 1] = f2_mul(x[2 * i + 1], f2_pack(f.z, f.w));
-                        }
                     }
                     if (!whole_tile) {
                         const int lim = draft ? 0 : (c0 < 64 ? mt.y : mt.z) - (c0 & 63);
@@ -511,9 +605,8 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                         }
                     }
                     float top = fmaxf(t0, t1);
-                    const bool over = fresh || top > m + C::LAZY || uf != 1.f;
-                    if (vote_any(pair, 64, over)) {
-                        if (!E4M3 && vote_any(pair, 64, false)) {
+                    if (vote_any(pair, 64, fresh || top > m + kManyLazy)) {
+                        if (vote_any(pair, 64, false)) {
                             ok = false;
                             break;
                         }
@@ -531,14 +624,13 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                                                                        kTreeDetail | 0x2Au));
                                 tc_fence_after();
                             }
-                            const float f = a * uf;
 #pragma unroll 1
                             for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {  // half of O's columns each
                                 uint32_t w[32];
                                 tmem_ld32(to + c0, w);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+                                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * a);
                                 tmem_st32(to + c0, w);
                             }
                             tmem_wait_st();
@@ -546,8 +638,6 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                         }
                     }
                     const uint64_t nm2 = f2_pack(-m, -m);
-                    const float pf = E4M3 && draft ? pow2i(min(127, max(-126, -u))) : 1.f;
-                    const uint64_t pf2 = f2_pack(pf, pf);
 #pragma unroll 1
                     for (int c0 = cb; c0 < ce; c0 += 32) {
                         uint64_t x[16];
@@ -564,51 +654,20 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                                 s0 = f2_add(s0, x[i]);
                         }
                         l2 = f2_add(l2, f2_add(s0, s1));
-                        if (E4M3 && !draft) {
+                        uint32_t w[16];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 f = *reinterpret_cast<const float4*>(vfac + c0 + 4 * i);
-                                x[2 * i] = f2_mul(x[2 * i], f2_pack(f.x, f.y));
-                                x[2 * i + 1] = f2_mul(x[2 * i + 1], f2_pack(f.z, f.w));
-                            }
-                            uint32_t t[3][8];
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                uint32_t hh[2], a1[2], a2[2], a3[2];
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    float a, c;
-                                    f2_unpack(x[2 * q + e], a, c);
-                                    hh[e] = pack_f16x2(a, c);
-                                    a1[e] = hh[e] & 0xFF00FF00u;
-                                    hh[e] = sub_f16x2(hh[e], a1[e]);
-                                    a2[e] = hh[e] & 0xFF00FF00u;
-                                    a3[e] = sub_f16x2(hh[e], a2[e]) + 0x00800080u;  // rounded, not cut
-                                }
-                                t[0][q] = __byte_perm(a1[0], a1[1], 0x7531);
-                                t[1][q] = __byte_perm(a2[0], a2[1], 0x7531);
-                                t[2][q] = __byte_perm(a3[0], a3[1], 0x7531);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 3; ++i) tmem_st8(ts + c0 + 8 * i, t[i]);
-                        } else {
-                            uint32_t w[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float a, c;
-                                if constexpr (E4M3) x[i] = f2_mul(x[i], pf2);
-                                f2_unpack(x[i], a, c);
-                                w[i] = pack_bf16x2(a, c);
-                            }
-                            tmem_st16(ts + c0, w);
+                        for (int i = 0; i < 16; ++i) {
+                            float a, c;
+                            f2_unpack(x[i], a, c);
+                            w[i] = pack_bf16x2(a, c);
                         }
+                        tmem_st16(ts + c0, w);
                     }
                     tmem_wait_st();
                 }
                 fresh = false;
                 tc_fence_before();
                 fence_proxy_async_smem();
-                if (E4M3 && !draft) named_bar_sync(group, 256);  // the table has been read
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&pfull[bar_of(h, pt)]);
                 ++it;
@@ -631,8 +690,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                 *mine_x = la + lb;
                 named_bar_sync(pair, 64);
                 const float l = half == 0 ? *mine_x + *other_x : *other_x + *mine_x;  // the same order in both
-                const float uo = E4M3 ? pow2i(min(127, max(-126, u))) : 1.f;
-                const float f = whole ? (l == 0.f ? 0.f : uo / l) : uo;
+                const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                 const bool mine_row = row < nrows;
                 const int kvh = p.per_qhead ? hs / p.g : hs;
                 const __nv_bfloat16* dv = p.DV + (static_cast<int64_t>(b) * p.Hkv + kvh) * p.T * D;
@@ -695,7 +753,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
         }
     }
     __syncthreads();
-    if (warp == 8 * NM + 1) {
+    if (warp == 8 * NM) {
         tc_fence_after();
         tmem_dealloc(tm, 512);
     }
@@ -707,11 +765,15 @@ static bool launch_many(TreeParams p, const CUtensorMap& k, const CUtensorMap& v
     using C = ManyCfg<D, E4M3, NM>;
     constexpr int budget = 225 * 1024;
     constexpr int fit = (budget - C::FIXED) / C::TILE;
-    constexpr int slots = fit < 2 * kTreeMaxSlots ? fit : 2 * kTreeMaxSlots;
+    constexpr int most = E4M3 ? 2 * kManySlots : 2 * kTreeMaxSlots, slots = fit < most ? fit : most;
     static_assert(slots >= 4, "two slots of K and of V must fit");
+    constexpr int spare = (budget - C::FIXED - slots * C::TILE) / (2 * C::STAGE);
+    constexpr int ns = !E4M3 ? 0 : spare < kManyStages ? spare : kManyStages;
+    static_assert(!E4M3 || ns >= 2, "two stages of each must fit");
     p.nk = slots / 2;
     p.nv = slots - p.nk;
-    const int smem = C::FIXED + slots * C::TILE;
+    p.ns = ns;
+    constexpr int smem = C::FIXED + slots * C::TILE + 2 * ns * C::STAGE;
     static std::atomic<uint64_t> configured{0};
     if (!configure_smem_once(reinterpret_cast<const void*>(attn_tree_many_kernel<D, E4M3, NM>), smem, configured))
         return false;
@@ -726,7 +788,7 @@ bool launch_attn_tree_many(TreeParams p, int D, bool e4m3, int rm, const void* K
     const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv * p.cap, drows = static_cast<int64_t>(p.B) * p.Hkv * p.T;
     CUtensorMap k, v, dk, dv;
     if (!make_tmap_2d(&dk, K, drows, D, p.tp) || !make_tmap_2d(&dv, p.DV, drows, D, p.tp)) return false;
-    if (e4m3 ? !make_tmap_2d_u8(&k, Kc, rows, D, 64) || !make_tmap_2d_u8(&v, Vc, rows, D, 64)
+    if (e4m3 ? !make_tmap_2d_u8(&k, Kc, rows, D, 32) || !make_tmap_2d_u8(&v, Vc, rows, D, 32)
              : !make_tmap_2d(&k, Kc, rows, D, 64) || !make_tmap_2d(&v, Vc, rows, D, 64))
         return false;
 #define PISA_MANY_CASE(DD, EE, NN) \

@@ -282,8 +282,9 @@ struct TreeParams {
     int32_t rpt;                    // rows of one row tile that are used
     int32_t runs, min_units;        // runs (CTAs) at most, and units one run has at least on average
     int32_t tp;                     // drafted tokens rounded up to 16
-    int32_t nk, nv;                 // slots of the K and of the V ring, or (few rows) stages of the one
-                                    // ring in nk (set by the launcher)
+    int32_t ns;                     // e4m3, many rows: stages (set by the launcher)
+    int32_t nk, nv;                 // slots of the K and of the V ring; few rows: stages of the one ring in
+                                    // nk (set by the launcher)
     float scale_log2;
 };
 
@@ -314,14 +315,14 @@ bool launch_cache_write(const CacheParams& p, int D, bool e4m3, cudaStream_t st)
 bool launch_cache_read(const CacheParams& p, int D, bool e4m3, cudaStream_t st);
 bool launch_cache_pyramid(const CachePyramidParams& p, cudaStream_t st, int32_t* launches);
 // Rows of one row tile for a selection row that `rows` = heads x drafted tokens share.
-int tree_row_tile(int rows);
+int tree_row_tile(int rows, int T, bool e4m3);
 int tree_ctas_per_sm(int rm, bool e4m3);
 bool launch_tree_merge(const TreeParams& p, int D, int rm, cudaStream_t st, int32_t* launches);
 bool launch_attn_tree_many(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
                            cudaStream_t st, int32_t* launches);
 bool launch_attn_tree_few(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
                           cudaStream_t st, int32_t* launches);
-bool launch_attn_tree(TreeParams p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
+bool launch_attn_tree(const TreeParams& p, int D, bool e4m3, int rm, const void* K, const void* Kc, const void* Vc,
                       cudaStream_t st, int32_t* launches);
 bool launch_attn_backward(const BwdParams& p, int32_t batch, cudaStream_t st, int32_t* launches);
 // Backward column pass (dK, dV) on the tensor cores (head dim 64 or 128, 64- or 128-key blocks:

@@ -1,7 +1,6 @@
 // What the two kernels of the tree attention share: the cut of the work into runs, and small helpers.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -90,46 +89,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // ---------------------------------------------------------------- operands
 
-// Shared-memory matrix descriptor; layout: 0 = none, 2 = 128-byte, 4 = 64-byte swizzle.
-__device__ __forceinline__ uint64_t tree_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(layout) << 61);
-}
+// A matrix descriptor's start moved by `bytes`.
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
-// Instruction descriptor for kind::f8f6f4: A e4m3, B e4m3 (0) or e5m2 (1), fp32 accumulator, M = 128.
-__host__ __device__ constexpr uint32_t idesc_f8(int n, int b_type, int a_mn, int b_mn) {
-    return (1u << 4) | (static_cast<uint32_t>(b_type) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
-           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
-}
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t cvt_e5m2x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ float2 e4m3x2_f32(uint32_t two) {
@@ -150,19 +120,8 @@ __device__ __forceinline__ bool vote_any(uint32_t bar, uint32_t count, bool x) {
         : "memory");
     return r != 0;
 }
-// Whether the barrier's phase of this parity has completed (no wait).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return r != 0;
-}
-// ---------------------------------------------------------------- the copies
+
+// ---------------------------------------------------------------- the tiles
 
 constexpr int kTreeMaxSlots = 4;  // of the K ring and of the V ring
 constexpr int kTreeMeta = 8;      // entries (tiles and piece ends) whose description is kept
@@ -181,91 +140,13 @@ struct RingAt {
     }
 };
 
-// The producer warp of the kernels whose tiles are 128 keys (two units): keeps a ring of K tiles and one
-// of V tiles full. Every entry (a tile, or the end of a piece) takes a K slot and describes itself in
-// meta[entry % kTreeMeta]; a tile takes a V slot too. K and V of a cache tile: [128 rows], bf16 as D / 64
-// column tiles of 128 bytes; of the drafted tokens: D / 64 column tiles of 64 rows.
-template <int D, bool E4M3>
-__device__ __forceinline__ void tree_producer(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                              const CUtensorMap& tmDK, const CUtensorMap& tmDV, uint8_t* ring,
-                                              uint8_t* vring, uint8_t* exps, uint64_t* kfull, uint64_t* kempty,
-                                              uint64_t* vfull, uint64_t* vempty, int4* meta, int64_t pos, int64_t end,
-                                              int64_t tile, int unit) {
-    constexpr int TILE = 128 * (E4M3 ? D : 2 * D), EXPS = E4M3 ? 256 : 0;
+// The entries of a CTA's pieces in order: issue(kind, plane, len, a0, a1) for every tile of 128 keys (two
+// units, first keys a0 and a1, a1 = -1 for none), for the drafted tokens, and for the end of each piece.
+// Run by a whole warp; `reports`: this warp records bad lengths and indices. Stops when ok is cleared.
+template <class Issue>
+__device__ __forceinline__ void tree_entries(const TreeParams& p, int64_t pos, int64_t end, int64_t tile, int unit,
+                                             bool reports, bool& ok, Issue issue) {
     const int lane = threadIdx.x & 31;
-    RingAt k, v;
-    bool ok = true;
-    if (lane == 0) {
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-        prefetch_tmap(&tmDK);
-        prefetch_tmap(&tmDV);
-    }
-    // one entry: a tile's K and then its V, or the end of a piece; of a tile of the cache the first
-    // keys of its halves (second -1: absent)
-    auto issue = [&](int kind, int64_t plane, int len, int a0, int a1) {
-        if (lane == 0) {
-            ok = k.n < p.nk || mbar_wait(&kempty[k.s], k.par ^ 1u, p.status, kTreeDetail | 0x01u);
-            if (ok) {
-                uint8_t* kt = ring + k.s * TILE;
-                uint64_t* kb = &kfull[k.s];
-                const int e = k.n % kTreeMeta;
-                const int halves = a1 >= 0 ? 2 : 1;
-                const int dbytes = p.tp * 2 * D, dy = static_cast<int>(plane * p.T);
-                if (kind == kTileEnd) {
-                    meta[e] = make_int4(kind, 0, 0, 0);
-                    mbar_arrive(kb);
-                } else if (kind == kTileDraft) {
-                    meta[e] = make_int4(kind, 0, 0, 0);
-                    mbar_arrive_expect_tx(kb, dbytes);
-    #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) tma_load_2d(kt + c * 8192, &tmDK, 64 * c, dy, kb);
-                } else {
-                    meta[e] = make_int4(kind, min(64, len - a0), a1 >= 0 ? min(64, len - a1) : 0, 0);
-                    mbar_arrive_expect_tx(kb, halves * (TILE + EXPS) / 2);
-                    for (int h = 0; h < halves; ++h) {
-                        const int64_t row = plane * p.cap + (h == 0 ? a0 : a1);
-                        if constexpr (E4M3) {
-                            tma_load_2d(kt + h * 64 * D, &tmK, 0, static_cast<int>(row), kb);
-                            bulk_load(exps + e * 256 + h * 64, p.k_exp + row, 64, kb);
-                            bulk_load(exps + e * 256 + 128 + h * 64, p.v_exp + row, 64, kb);
-                        } else {
-    #pragma unroll
-                            for (int c = 0; c < D / 64; ++c)
-                                tma_load_2d(kt + c * 16384 + h * 8192, &tmK, 64 * c, static_cast<int>(row), kb);
-                        }
-                    }
-                }
-                k.next(p.nk);
-                if (kind != kTileEnd) {
-                    ok = v.n < p.nv || mbar_wait(&vempty[v.s], v.par ^ 1u, p.status, kTreeDetail | 0x02u);
-                    if (ok) {
-                        uint8_t* vt = vring + v.s * TILE;
-                        uint64_t* vb = &vfull[v.s];
-                        if (kind == kTileDraft) {
-                            mbar_arrive_expect_tx(vb, dbytes);
-    #pragma unroll
-                            for (int c = 0; c < D / 64; ++c) tma_load_2d(vt + c * 8192, &tmDV, 64 * c, dy, vb);
-                        } else {
-                            mbar_arrive_expect_tx(vb, halves * TILE / 2);
-                            for (int h = 0; h < halves; ++h) {
-                                const int y = static_cast<int>(plane * p.cap + (h == 0 ? a0 : a1));
-                                if constexpr (E4M3) {
-                                    tma_load_2d(vt + h * 64 * D, &tmV, 0, y, vb);
-                                } else {
-    #pragma unroll
-                                    for (int c = 0; c < D / 64; ++c)
-                                        tma_load_2d(vt + c * 16384 + h * 8192, &tmV, 64 * c, y, vb);
-                                }
-                            }
-                        }
-                        v.next(p.nv);
-                    }
-                }
-            }
-        }
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-    };
     while (pos < end && ok) {
         const int b = static_cast<int>(tile / p.rows_per_seq);
         const int hs = static_cast<int>(tile % p.rows_per_seq) / p.mt;
@@ -274,15 +155,14 @@ __device__ __forceinline__ void tree_producer(const TreeParams& p, const CUtenso
         const int len = tree_len(p, b);
         const int units = tree_units(p, len);
         const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
-        if (tile % p.rows_per_seq == 0 && unit == 0 && lane == 0 && p.len[b] != len)
+        if (reports && tile % p.rows_per_seq == 0 && unit == 0 && lane == 0 && p.len[b] != len)
             record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB0u);
         const int32_t* row = p.topk > 0 ? p.idx + (static_cast<int64_t>(b) * p.Hsel + hs) * p.topk : nullptr;
         const int nsel = p.topk * p.upb;
         const int uc = min(u1, units - 1);  // the last unit is the drafted tokens
         int first = -1;                     // a unit that waits for its partner
         for (int u = unit; u < uc && ok; u += 32) {
-            // up to 32 units at a time: position of each unit's first key, -1 = nothing there
-            int at = -1;
+            int at = -1;  // position of this lane's unit; -1 = nothing there
             if (u + lane < uc) {
                 const int c = u + lane;
                 if (p.topk == 0) {
@@ -291,10 +171,11 @@ __device__ __forceinline__ void tree_producer(const TreeParams& p, const CUtenso
                     at = p.seq + 64 * (c - nsel);
                 } else {
                     const int j = __ldg(row + c / p.upb);
-                    if (j >= p.n0)
-                        record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB1u);
-                    else if (j >= 0)
+                    if (j >= p.n0) {
+                        if (reports) record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB1u);
+                    } else if (j >= 0) {
                         at = (j * p.upb + c % p.upb) * 64;
+                    }
                 }
             }
             for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < len); left != 0 && ok; left &= left - 1) {
@@ -313,20 +194,6 @@ __device__ __forceinline__ void tree_producer(const TreeParams& p, const CUtenso
         pos += u1 - unit;
         unit = 0;
         ++tile;
-    }
-    // every copy lands before the block ends, also when another role gave up (earlier uses of a slot
-    // were complete before it was filled again)
-    if (lane == 0) {
-        for (int i = 0; i < p.nk && i < k.n; ++i) {
-            k.s = k.s == 0 ? p.nk - 1 : k.s - 1;
-            if (k.s == p.nk - 1) k.par ^= 1u;
-            if (!mbar_wait(&kfull[k.s], k.par, p.status, kTreeDetail | 0x03u)) break;
-        }
-        for (int i = 0; i < p.nv && i < v.n; ++i) {
-            v.s = v.s == 0 ? p.nv - 1 : v.s - 1;
-            if (v.s == p.nv - 1) v.par ^= 1u;
-            if (!mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x04u)) break;
-        }
     }
 }
 

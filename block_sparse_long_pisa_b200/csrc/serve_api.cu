@@ -125,7 +125,7 @@ static pisa_status tree_plan(const pisa_tree_shape* s, TreePlan* t) {
     t->hsel = s->select_per_qhead ? s->heads_q : s->heads_kv;
     if (static_cast<int64_t>(t->gh) * s->drafts > (1 << 20)) return PISA_ERR_UNSUPPORTED;
     t->rows = t->gh * s->drafts;
-    t->rm = tree_row_tile(t->rows);
+    t->rm = tree_row_tile(t->rows, s->drafts, s->format == PISA_CACHE_E4M3);
     t->mt = (t->rows + t->rm - 1) / t->rm;
     if (static_cast<int64_t>(s->batch) * t->hsel * t->mt >= (int64_t(1) << 31)) return PISA_ERR_UNSUPPORTED;
     t->runs = kTreeRuns * tree_ctas_per_sm(t->rm, s->format == PISA_CACHE_E4M3);

@@ -447,6 +447,16 @@ TREE_CASES = [
     (1, 2, 1, 2, 20480, 64, 0, 128, 0, 0, 0, [20479], "chain"),
     (33, 2, 2, 2, 128, 64, 1, 64, 0, 0, 0, None, "tree"),
     (70, 4, 1, 1, 256, 128, 1, 64, 192, 2, 0, None, "chain"),
+    # two row tiles of 16, unlike ones too; as many drafted tokens as rows
+    (3, 5, 1, 5, 448, 128, 1, 64, 320, 4, 0, [400, 0, 130], "tree"),
+    (2, 2, 1, 16, 256, 64, 1, 64, 0, 0, 0, [250, 1], "tree"),
+    (1, 1, 1, 17, 256, 128, 1, 64, 0, 0, 0, [200], "any"),
+    # several pieces to a run
+    (200, 4, 2, 20, 192, 64, 1, 64, 0, 0, 0, None, "tree"),
+    (200, 4, 2, 20, 192, 128, 0, 64, 0, 0, 0, None, "tree"),
+    (120, 4, 1, 40, 320, 128, 1, 64, 128, 2, 0, None, "tree"),
+    (120, 4, 1, 40, 320, 64, 0, 64, 128, 2, 0, None, "tree"),
+    (300, 4, 1, 8, 192, 128, 1, 64, 0, 0, 0, None, "tree"),
 ]
 
 
@@ -515,9 +525,9 @@ def test_tree_attention(pisa, case):
 
 
 @pytest.mark.parametrize("case", [TREE_CASES[i] for i in (4, 10, 13, 17, 18, 19, 24)])
-@pytest.mark.parametrize("spread, qscale", [(12, 1.0), (0, 30.0), (6, 1e-3)])
+@pytest.mark.parametrize("spread, qscale", [(12, 1.0), (0, 30.0), (6, 1e-3), (30, 1e-9)])
 def test_tree_attention_of_unlike_rows(pisa, case, spread, qscale):
-    """Value rows from 2^-12 to 2^12 of one another (the unit of O moves), peaked and flat scores."""
+    """Value rows from 2^-12 (2^-30) to 2^12 (2^30) of one another (the unit of O moves), peaked and flat scores."""
     s, cache, k, v, q, dk, dv, mask, lens, idx = tree_inputs(pisa, case, 22, spread, qscale)
     ws = pisa.new_tree_workspace(s, "cuda")
     O, lse = pisa.tree_attention(s, cache, q, dk, dv, tmask(mask), i32(lens), ws, idx=None if idx is None else i32(idx))

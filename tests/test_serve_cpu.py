@@ -198,7 +198,7 @@ def test_injected_failure(monkeypatch):
 
 def test_workspace_sizes_depend_on_the_shape_alone():
     """Status word, then two partial slots (o, m, l of a row tile) for each of the runs."""
-    for drafts, rm, runs in ((1, 8, 444), (4, 8, 444), (5, 16, 296), (8, 16, 296), (16, 32, 296), (32, 128, 148), (64, 128, 148)):
+    for drafts, rm, runs in ((1, 8, 444), (4, 8, 444), (5, 16, 296), (8, 16, 296), (16, 16, 296), (17, 128, 148), (64, 128, 148)):
         s = pisa.TreeShape(**{**TREE, "drafts": drafts})
         assert pisa.tree_workspace_size(s) == 256 + 2 * runs * rm * 66 * 4
     assert pisa.norm_rope_workspace_size(pisa.NormRopeShape(2, 3, 4, 2, 64, 64)) == 592 * 64 * 4
