@@ -18,10 +18,10 @@
 // An e4m3 cache is turned into bf16 tiles on the way in: an e4m3 value times a power of two is a bf16 value
 // (rounded once below bf16's smallest normal), and everything after is the same. For each ring one warp fetches
 // the bytes, 32 rows a stage, and two or four converter warps write the swizzled tiles, some 65 instructions for
-// 512 values. That is what bounds this form (64 caches of 16K rows, 64 blocks of 128 each, tokens of four heads,
+// 512 values. That is what bounds this form (64 caches of 8 heads, 64 blocks of 64 keys selected, tokens of four heads,
 // against bf16: 16 tokens 357 us, 252 us; 64 tokens 664 us, 537 us), together with the instruction cache: with
-// the converters' loop unrolled four times and a copy of it for K and one for V, 32 tokens took 790 us and not
-// 392 us. (With e4m3 operands in the products instead, P and Q need two and three 8-bit terms and every score a
+// the converters' loop unrolled four times and a copy of it for K and one for V, 32 tokens took 786 us and not
+// 424 us (392 us since each warp takes whole steps). (With e4m3 operands in the products instead, P and Q need two and three 8-bit terms and every score a
 // factor from a table: 469 us for the 16 tokens.)
 #include <cuda.h>
 #include <cuda_bf16.h>

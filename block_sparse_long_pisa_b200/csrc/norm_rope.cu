@@ -22,6 +22,11 @@
 // The weight gradients are summed in registers along a block's tiles (a grid of at most
 // kNormRopeBlocks blocks), then over the block's groups through shared memory, then over the blocks
 // by a second kernel: fixed orders, no atomics.
+//
+// Measured (heads of 128, all dims turned): forward, 131,072 tokens of 32 + 8 heads, 2.68 GB in 464 us, 5.8 TB/s
+// (88 % of the copy rate); 64 tokens of as many heads 5.2 us. Backward, 32,768 tokens of 16 + 16 heads, 0.81 GB in
+// 164 us, 4.9 TB/s (75 %): 128 registers for the angles' products and the weight sums leave two blocks on an SM,
+// so the loads in flight bound it (DRAM 54 %, issue 54 % in the profile), and three blocks spill.
 #include <cuda_bf16.h>
 
 #include "pisa_device.cuh"
