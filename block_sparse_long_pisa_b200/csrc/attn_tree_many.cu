@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
         }
     } else if (warp == 8 * NM) {
         // ------------------------------------------------ MMA
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t q0 = smem_u32(q_s);
             int it = 0, tn = 0;       // S slots so far, and tiles among them
             int pn = 0, pit = 0;      // tiles whose P V was issued for every row tile; the S slot of the next one

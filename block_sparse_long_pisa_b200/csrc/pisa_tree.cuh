@@ -107,6 +107,16 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t two) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
+// One lane of the whole warp, in a form that the compiler knows to be one lane.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 // Barrier `bar` over `count` threads (whole warps); true if `x` holds in any of them.
 __device__ __forceinline__ bool vote_any(uint32_t bar, uint32_t count, bool x) {
     uint32_t r;
