@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
             int it = 0, tn = 0;       // S slots so far, and tiles among them
             int pn = 0, pit = 0;      // tiles whose P V was issued for every row tile; the S slot of the next one
             bool pend = false;        // P V of the tile before is still to be issued (two row tiles: for tile 1)
-            bool pdraft = false;      // and that tile is the drafted tokens
+            bool pdraft = false;      // and that tile is the drafted tokens;
+            int psteps = 0;           // its steps
             uint32_t fresh = 3u;      // bit h: the next P V of row tile h begins O
             uint32_t qpar = 0;
             bool issued = false;
@@ -385,8 +386,8 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                                 n > 0 ? 1u : 0u);
                 mma_commit(&sfull[bar_of(h, it)]);
             };
-            // P V of row tile h for tile number n (S slot sit) from the V slot at hand
-            auto pv = [&](int h, int n, int sit, bool draft) {
+            // P V of row tile h for tile number n (S slot sit) from the V slot at hand, 16 keys a step
+            auto pv = [&](int h, int n, int sit, bool draft, int steps) {
                 ok = mbar_wait(&pfull[bar_of(h, n)], par_of(n), p.status, kTreeDetail | 0x25u) &&
                      mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x26u);
                 if (!ok) return;
@@ -394,7 +395,6 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                 const uint32_t vt = smem_u32(vring + v.s * C::TILE);
                 const uint32_t a = tm + bar_of(h, sit) * 128, d = tm + C::O_COL + h * 128;
                 const uint64_t b = smem_desc_sw128(vt, draft ? 8192 : 16384, 1024);
-                const int steps = draft ? p.tp / 16 : 8;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (i < steps) mma_bf16_ts(d, a + 32 * (i / 2) + 8 * (i % 2), desc_at(b, i * 2048), idesc_bf16_f32(128, D, 0, 1),
@@ -413,9 +413,10 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                 while (ok && !over) {
                     ok = mbar_wait(&kfull[k.s], k.par, p.status, kTreeDetail | 0x2Cu);
                     if (!ok) break;
-                    const int kind = meta[k.n % kTreeMeta].x;
-                    const bool draft = kind == kTileDraft;
-                    over = kind == kTileEnd;
+                    const int4 mt = meta[k.n % kTreeMeta];
+                    const bool draft = mt.x == kTileDraft;
+                    const int steps = draft ? p.tp / 16 : mt.z > 0 ? 4 + (mt.z + 15) / 16 : (mt.y + 15) / 16;
+                    over = mt.x == kTileEnd;
                     issued = true;
                     // one step for each row tile: its S, then the P V that is due (two row tiles: of the other one)
 #pragma unroll 1
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                         }
                         const bool due = h == 0;  // of the tile before, the last product of its V slot
                         if (due && !pend) continue;
-                        pv(due ? NM - 1 : 0, due ? pn : tn, due ? pit : it, due ? pdraft : draft);
+                        pv(due ? NM - 1 : 0, due ? pn : tn, due ? pit : it, due ? pdraft : draft, due ? psteps : steps);
                         if (ok && due) {
                             mma_commit(&vempty[v.s]);
                             v.next(p.nv);
@@ -449,6 +450,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                     } else {
                         pend = true;
                         pdraft = draft;
+                        psteps = steps;
                         pit = it;
                         ++tn;
                     }
@@ -531,38 +533,41 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                 const bool draft = mt.x == kTileDraft;
                 const bool whole_tile = !draft && mt.y == 64 && mt.z == 64;
                 uint8_t* vt = vring + v.s * C::TILE;
-                if (half == 0 && (draft || (!E4M3 && !whole_tile))) {  // what follows writes V's tile: it has landed
+                if (draft || (!E4M3 && !whole_tile)) {  // what follows writes V's tile: it has landed
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&vfull[v.s], v.par, p.status, kTreeDetail | 0x2Bu));
-                }
-                // V rows that do not count must not meet P's zeros as a NaN: each row tile clears them before its
-                // own P (two row tiles: the same zeros twice)
-                if (!E4M3 && half == 0 && !draft && !whole_tile && (row & 63) >= (row < 64 ? mt.y : mt.z)) {
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint8_t* z = vt + (c / 8) * 16384 + row * 128 + 16 * (c % 8);
-                        *reinterpret_cast<uint4*>(z) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
-                if (half == 0 && draft && row < p.tp) {
-                    // a drafted value that is not finite would reach every token through 0 * x: it is taken out
-                    // here (by whichever row tile comes first) and given to the tokens that attend it at the end
-                    uint32_t bad = 0;
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint4* z = reinterpret_cast<uint4*>(vt + (c / 8) * 8192 + row * 128 + 16 * (c % 8));
-                        uint32_t w[4] = {z->x, z->y, z->z, z->w};
-                        uint32_t any = 0;
+                    // (two row tiles do the same twice: either may come first)
+                    const int t = half * 128 + row;
+                    if (draft) {
+                        // a drafted value that is not finite would reach every token through 0 * x: it is taken out
+                        // here and given to the tokens that attend it at the end; rows past the tokens become zeros
+#pragma unroll 1
+                        for (int e = t; e < p.tp * (D / 8); e += 256) {
+                            const int r = e / (D / 8), c = e % (D / 8);
+                            uint4* z = reinterpret_cast<uint4*>(vt + (c / 8) * 8192 + r * 128 + 16 * (c % 8));
+                            uint32_t w[4] = {z->x, z->y, z->z, z->w};
+                            uint32_t any = 0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u, any = 1;
-                            if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu, any = 1;
+                            for (int i = 0; i < 4; ++i) {
+                                if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u, any = 1;
+                                if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu, any = 1;
+                            }
+                            if (r >= p.T) {
+                                *z = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (any) {
+                                *z = make_uint4(w[0], w[1], w[2], w[3]);
+                                atomicOr(&dflag[piece & 1][r >> 5], 1u << (r & 31));
+                            }
                         }
-                        if (row >= p.T) {
-                            *z = make_uint4(0u, 0u, 0u, 0u);
-                        } else if (any) {
-                            *z = make_uint4(w[0], w[1], w[2], w[3]);
-                            bad = 1;
+                    } else {
+                        // V rows that do not count, in the steps that are taken, must not meet P's zeros as a NaN
+                        const int e0 = mt.z > 0 ? 64 : (mt.y + 15) & ~15, e1 = (mt.z + 15) & ~15;
+#pragma unroll 1
+                        for (int e = t; e < (e0 - mt.y + e1 - mt.z) * (D / 8); e += 256) {
+                            const int i = e / (D / 8), c = e % (D / 8);
+                            const int r = i < e0 - mt.y ? mt.y + i : 64 + mt.z + i - (e0 - mt.y);
+                            *reinterpret_cast<uint4*>(vt + (c / 8) * 16384 + r * 128 + 16 * (c % 8)) = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
-                    if (bad) atomicOr(&dflag[piece & 1][row >> 5], 1u << (row & 31));
                 }
                 const uint32_t ts = tm + lanes + bar_of(h, it) * 128;
                 const uint32_t to = tm + lanes + C::O_COL + h * 128;
