@@ -34,8 +34,7 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
     const int hs = rem / p.mt, row_base = (rem % p.mt) * p.rpt;
     const int rows = p.gh * p.T;
     const int row = static_cast<int>(blockIdx.y) * 4 + static_cast<int>(threadIdx.x >> 5);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (row >= p.rpt || row_base + row >= rows) return;
+    // (what comes before the wait reads the lengths alone, which were there before the runs began)
     const TreeJob job = tree_job(p);
     // units before this row tile (whole warp)
     const int lane = threadIdx.x & 31;
@@ -46,7 +45,8 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
     const int units = tree_units(p, tree_len(p, b));
     const int64_t x0 = before * p.rows_per_seq + static_cast<int64_t>(rem) * units;
     const int64_t c0 = job.run_of(x0), c1 = job.run_of(x0 + units - 1);
-    if (c0 == c1) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // also by a block without rows: the grid ends after the runs
+    if (c0 == c1 || row >= p.rpt || row_base + row >= rows) return;
     const int64_t stride = static_cast<int64_t>(RM) * (D + 2);
     auto slot = [&](int64_t c) { return p.part + (2 * c + (c == c0 ? 1 : 0)) * stride; };
     float M = -INFINITY;

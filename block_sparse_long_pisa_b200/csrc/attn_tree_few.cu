@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
     __shared__ int meta[kFewStages];   // keys of the stage's tile that count; 0: the piece ends
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join finds its place as CTAs end
     const TreeJob job = tree_job(p);
     if (static_cast<int64_t>(blockIdx.x) >= job.runs) return;
     int64_t pos = job.begin(blockIdx.x);

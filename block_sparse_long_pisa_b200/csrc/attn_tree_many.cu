@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
     __shared__ uint32_t tmem_slot, dflag[2][2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join finds its place as CTAs end
     const TreeJob job = tree_job(p);
     if (static_cast<int64_t>(blockIdx.x) >= job.runs) return;
     int64_t pos = job.begin(blockIdx.x);
