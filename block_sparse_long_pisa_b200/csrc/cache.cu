@@ -11,11 +11,10 @@
 // words (bf16 magnitudes order like their bits) and log2(D/8) shuffles. Each lane group keeps
 // several rows in flight.
 //
-// Measured (8 heads of 128, e4m3): write of 131,072 tokens 0.81 GB in 158 us, 5.1 TB/s (78 % of the copy rate; the
-// integer pipe is at 60 %: per value an exponent test, a scaling and half a conversion); write of one token to
-// each of 64 sequences 2.6 us; read of 7 ragged prefixes 0.29 GB in 48 us, 6.0 TB/s (91 %); pyramids of 8
-// caches of 32,768 keys 0.29 GB in 64 us, 4.5 TB/s (issue 59 %: two conversions, two multiplications and two sums
-// for two values read as two bytes).
+// Measured (8 heads of 128, e4m3): write of 131,072 tokens 0.81 GB in 120 us, 6.7 TB/s, the copy rate (two rows
+// share a word in the maximum's shuffles and pairs are scaled at once: 158 us with a word a row, at 67 % of the
+// issue slots); write of one token to each of 64 sequences 2.2 us; read of 7 ragged prefixes 0.29 GB in 48 us,
+// 6.0 TB/s (91 %); pyramids of 8 caches of 32,768 keys 0.29 GB in 64 us, 4.5 TB/s (issue 59 %).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -93,29 +92,38 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheP
     } else {
         uint8_t* dst = static_cast<uint8_t*>(is_v ? p.Vc : p.Kc) + w.at * D + 8 * lane8;
         uint8_t* dexp = (is_v ? p.ve : p.ke) + w.at;
-        uint32_t top[kCacheRows];  // largest magnitude of the even and of the odd values
+        uint32_t top[kCacheRows / 2];  // largest magnitudes of two rows
 #pragma unroll
-        for (int u = 0; u < kCacheRows; ++u)
-            top[u] = __vmaxu2(__vmaxu2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
-                              __vmaxu2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu));
+        for (int u = 0; u < kCacheRows; u += 2) {
+            uint32_t m[2];  // of the even and of the odd values of a row
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4& x = v[u + i];
+                m[i] = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+            }
+            top[u / 2] = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+        }
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) {
 #pragma unroll
-            for (int u = 0; u < kCacheRows; ++u) top[u] = __vmaxu2(top[u], __shfl_xor_sync(0xFFFFFFFFu, top[u], o));
+            for (int u = 0; u < kCacheRows / 2; ++u) top[u] = __vmaxu2(top[u], __shfl_xor_sync(0xFFFFFFFFu, top[u], o));
         }
 #pragma unroll
         for (int u = 0; u < kCacheRows; ++u) {
-            const uint32_t t = max(top[u] & 0xFFFFu, top[u] >> 16);
-            // 1.m * 2^(E - 127) <= 1.75 * 2^8 * 2^(e - 127)
-            const int E = static_cast<int>(t >> 7);
-            const bool bad = E == 255;
-            const int e = bad ? 255 : max(1, E - 8 + ((t & 0x7Fu) > 0x60u ? 1 : 0));
+            const uint32_t t = (u & 1) ? top[u / 2] >> 16 : top[u / 2] & 0xFFFFu;
+            // 1.m * 2^(E - 127) <= 1.75 * 2^8 * 2^(e - 127): the mantissas above 0x60 carry into E
+            const bool bad = t >= 0x7F80u;
+            const int e = bad ? 255 : max(1, static_cast<int>((t + 0x1Fu) >> 7) - 8);
             const float f = __uint_as_float(static_cast<uint32_t>(bad ? 127 : 254 - e) << 23);
+            const uint64_t f2 = f2_pack(f, f);
             const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
             uint32_t q[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                q[k] = e4m3x2(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xFFFF0000u) * f);
+            for (int k = 0; k < 4; ++k) {
+                float lo, hi;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xFFFF0000u)), f2), lo, hi);
+                q[k] = e4m3x2(lo, hi);
+            }
             if (u < w.n) {
                 *reinterpret_cast<uint2*>(dst + u * D) =
                     bad ? make_uint2(0u, 0u) : make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
