@@ -32,9 +32,14 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ float2 e4m3x2_values(uint32_t two) {
+// The two e4m3 values of a word's low (HI: high) half.
+template <bool HI>
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t word) {
     uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+    if constexpr (HI)
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(h) : "r"(word));
+    else
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(word));
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
@@ -170,8 +175,10 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CachePa
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t x = k < 2 ? v[u].x : v[u].y;
-                const float2 y = e4m3x2_values((k & 1) ? x >> 16 : x & 0xFFFFu);
-                o[k] = pack_bf16x2(y.x * f, y.y * f);
+                const float2 y = (k & 1) ? e4m3x2_values<true>(x) : e4m3x2_values<false>(x);
+                float lo, hi;
+                f2_unpack(f2_mul(f2_pack(y.x, y.y), f2_pack(f, f)), lo, hi);
+                o[k] = pack_bf16x2(lo, hi);
             }
             *reinterpret_cast<uint4*>(out + u * D) = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -190,7 +197,7 @@ __device__ __forceinline__ void e4m3_block_mean(const uint8_t* K, const uint8_t*
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = 0ull;
     const uint8_t* row = K + rsub * D + 16 * chunk;
-#pragma unroll 2
+#pragma unroll 1
     for (int r0 = 0; r0 < blk; r0 += 32) {
         uint4 v[N];
 #pragma unroll
@@ -203,7 +210,7 @@ __device__ __forceinline__ void e4m3_block_mean(const uint8_t* K, const uint8_t*
             const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float2 x = e4m3x2_values((k & 1) ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu);
+                const float2 x = (k & 1) ? e4m3x2_values<true>(w[k >> 1]) : e4m3x2_values<false>(w[k >> 1]);
                 asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[k]) : "l"(f2_pack(x.x, x.y)), "l"(f2));
             }
         }
@@ -211,18 +218,23 @@ __device__ __forceinline__ void e4m3_block_mean(const uint8_t* K, const uint8_t*
     float a[16];
 #pragma unroll
     for (int k = 0; k < 8; ++k) f2_unpack(acc[k], a[2 * k], a[2 * k + 1]);
+    // over the lanes of a chunk: each step two lanes share out what they hold, so a lane ends with 16 / RPI dims
+    int at = 16 * chunk;
 #pragma unroll
-    for (int o = LPR; o < 32; o <<= 1) {
+    for (int o = LPR, n = 8; o < 32; o <<= 1, n >>= 1) {
+        const bool upper = (lane & o) != 0;
+        at += upper ? n : 0;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) a[k] += __shfl_xor_sync(0xFFFFFFFFu, a[k], o);
+        for (int k = 0; k < n; ++k) {
+            const float keep = upper ? a[n + k] : a[k], give = upper ? a[k] : a[n + k];
+            a[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+        }
     }
-    if (rsub == 0) {
-        const float inv = 1.0f / static_cast<float>(blk);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            reinterpret_cast<float4*>(out + 16 * chunk)[k] =
-                make_float4(a[4 * k] * inv, a[4 * k + 1] * inv, a[4 * k + 2] * inv, a[4 * k + 3] * inv);
-    }
+    const float inv = 1.0f / static_cast<float>(blk);
+    if constexpr (RPI == 4)
+        *reinterpret_cast<float4*>(out + at) = make_float4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+    else
+        *reinterpret_cast<float2*>(out + at) = make_float2(a[0] * inv, a[1] * inv);
 }
 
 // Subtrees of S = f^m key blocks (S <= 16, or f): a CTA forms the level-0 means of its blocks that are
