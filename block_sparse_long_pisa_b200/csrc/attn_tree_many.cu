@@ -234,25 +234,37 @@ __device__ __forceinline__ void many_converter(const TreeParams& p, const CUtens
 #pragma unroll 1
             for (int row = rsub; row < SR; row += RPI) {
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                uint32_t e = 0;
+                uint32_t e = 127;
                 if (r0 + row < n) {
                     x = *reinterpret_cast<const uint4*>(src + row * D + ((D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4));
                     e = ex[row];
                 }
-                // seeeemmm as a bf16 with the exponent field eeee is the value times 2^-120, its subnormals too;
-                // times 2^(e - 7), which is no bf16 above e = 134: the rest comes after. 255: a NaN
-                const uint32_t f = e == 255u ? 0x7FC0u : (min(e, 134u) + 120u) << 7, f1 = f | (f << 16);
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                uint32_t o[8];
+                uint32_t o[8], nan = 0;
+                // seeeemmm as a bf16 with the exponent field eeee is the value times 2^-120, its subnormals too;
+                // times 2^(e - 7) then
+                const uint32_t f = (e + 120u) << 7, f1 = f | (f << 16);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const uint32_t y = __byte_perm(w[c / 2], 0u, (c & 1) ? 0x3424 : 0x1404);
                     o[c] = bf16x2_mul((y & 0x80008000u) | ((y >> 4) & 0x07F007F0u), f1);
                 }
-                if (e > 134u && e < 255u) {  // a row of very large values
-                    const uint32_t f0 = (e - 134u + 127u) << 7, f2 = f0 | (f0 << 16);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) o[c] = bf16x2_mul(o[c], f2);
+                for (int c = 0; c < 4; ++c) nan |= (w[c] & 0x7F7F7F7Fu) + 0x01010101u;
+                // 2^(e - 7) is no bf16 above e = 134; a byte that is a NaN is none of the above
+                if (e > 134u || (nan & 0x80808080u) != 0u) {
+                    const float g = __uint_as_float(e << 23);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t v = c == 0 ? x.x : c == 1 ? x.y : c == 2 ? x.z : x.w;
+                        const float2 lo = e4m3x2_f32(v & 0xFFFFu), hi = e4m3x2_f32(v >> 16);
+                        const uint32_t y0 = pack_bf16x2(lo.x * g, lo.y * g), y1 = pack_bf16x2(hi.x * g, hi.y * g);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            o[2 * q] = q == c ? y0 : o[2 * q];
+                            o[2 * q + 1] = q == c ? y1 : o[2 * q + 1];
+                        }
+                    }
                 }
                 uint8_t* dst = t + (chunk / 4) * 16384 + (r0 + row) * 128;
                 const int c = 2 * (chunk % 4);

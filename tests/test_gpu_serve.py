@@ -534,6 +534,30 @@ def test_tree_attention_of_unlike_rows(pisa, case, spread, qscale):
     check_tree(s, O, lse, k, v, q, dk, dv, mask, lens, idx)
 
 
+@pytest.mark.parametrize("T, Hq, D", [(1, 4, 128), (5, 4, 64), (5, 4, 128), (20, 4, 64), (24, 8, 128)])
+def test_tree_attention_of_a_nan_byte(pisa, T, Hq, D):
+    """A cached byte that is a NaN is one: in V for its dim of every token, in K for all dims; other sequences and
+    heads keep their bits."""
+    import torch
+    case = (2, Hq, 2, T, 256, D, 1, 64, 0, 0, 0, [200, 170], "chain")
+    s, cache, k, v, q, dk, dv, mask, lens, idx = tree_inputs(pisa, case, 23)
+    ws = pisa.new_tree_workspace(s, "cuda")
+    run = lambda: pisa.tree_attention(s, cache, q, dk, dv, tmask(mask), i32(lens), ws)[0]
+    base = run()
+    assert not torch.isnan(base).any()
+    for t, dims in ((cache.v, [3]), (cache.k, list(range(D)))):
+        byte = t.view(torch.uint8)[1, 0, 77, 3]
+        kept = int(byte)
+        byte.fill_(0xFF)
+        O = run()
+        bad = torch.zeros_like(O, dtype=torch.bool)
+        bad[1, :Hq // 2, :, dims] = True
+        assert torch.equal(torch.isnan(O), bad) and torch.equal(O[~bad], base[~bad])
+        byte.fill_(kept)
+    assert pisa.check_status(ws) == (pisa.OK, 0)
+
+
+
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("T, Hq", [(5, 1), (5, 2), (8, 4), (9, 4), (40, 2), (40, 4)])
 def test_drafts_that_are_not_attended_do_not_touch_a_token(pisa, fmt, T, Hq):
