@@ -321,7 +321,8 @@ PISA_API pisa_status pisa_norm_rope_workspace_size(const pisa_norm_rope_shape *s
  *   dXq, dXk : bf16, strided (so they may be the parts of a packed gradient); every element written;
  *              they must not overlap the inputs or each other.
  *   dwq, dwk : fp32 [D] or NULL; with wq (wk) NULL the sums are those of a weight of ones.
- *   ws       : >= pisa_norm_rope_workspace_size bytes; needs no clearing.
+ *   ws       : >= pisa_norm_rope_workspace_size bytes; needs no clearing. Calls that share one must
+ *              not overlap on the GPU.
  * Deterministic: no atomics, every sum in a fixed order. */
 PISA_API pisa_status pisa_qk_norm_rope_backward(const pisa_norm_rope_shape *shape, const void *Xq, const void *Xk,
                                                 const float *wq, const float *wk, const float *inv_freq,
@@ -411,6 +412,8 @@ PISA_API pisa_status pisa_tree_workspace_size(const pisa_tree_shape *shape, size
  *   O         : bf16 [B, heads_q, T, D].  lse : optional fp32 [B, heads_q, T] (natural log).
  *   A token that attends nothing gets O = 0 and LSE = -inf. Keys and values of drafted tokens that a
  *   token does not attend do not touch its result, whatever they hold.
+ *   ws        : >= pisa_tree_workspace_size bytes. Calls that share one must not overlap on the GPU:
+ *               one stream, or events, or a workspace for each graph that may run at the same time.
  * The result depends on the inputs alone (no atomics in any sum). */
 PISA_API pisa_status pisa_tree_attention(const pisa_tree_shape *shape, const void *Q, const void *K, const void *V,
                                          const uint64_t *mask, const void *Kc, const void *Vc, const uint8_t *k_exp,

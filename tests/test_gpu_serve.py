@@ -738,6 +738,66 @@ def test_other_stream_and_graph(pisa):
 
 # ----------------------------------------------------------------------------- together
 
+@pytest.mark.parametrize("fmt, T, Hq, D", [(1, 2, 8, 128), (1, 12, 4, 128), (1, 20, 8, 64), (0, 48, 8, 128)])
+def test_two_calls_at_once(pisa, fmt, T, Hq, D):
+    """Calls with a workspace each, on two streams and in two graphs that run at the same time, keep their bits."""
+    import torch
+    case = (6, Hq, 2, T, 2048, D, fmt, 64, 0, 0, 0, [2000, 1, 1500, 0, 777, 2048], "tree")
+    s, cache, k, v, q, dk, dv, mask, lens, idx = tree_inputs(pisa, case, 41)
+    m, n, q2 = tmask(mask), i32(lens), (q.float() * 0.5).to(torch.bfloat16)
+    ws = [pisa.new_tree_workspace(s, "cuda") for _ in range(2)]
+    want = [pisa.tree_attention(s, cache, x, dk, dv, m, n, ws[0])[0].clone() for x in (q, q2)]
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.empty_like(q) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i, x in enumerate((q, q2)):
+            pisa.tree_attention(s, cache, x, dk, dv, m, n, ws[i], O=outs[i], lse=False, stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    graphs = []
+    for i, x in enumerate((q, q2)):
+        outs[i].zero_()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            pisa.tree_attention(s, cache, x, dk, dv, m, n, ws[i], O=outs[i], lse=False)
+    for _ in range(8):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert [pisa.check_status(w) for w in ws] == [(pisa.OK, 0)] * 2
+
+
+@pytest.mark.parametrize("fmt, T", [(1, 1), (1, 20), (0, 2), (0, 20)])
+def test_offsets_past_32_bits(pisa, fmt, T):
+    """The end of a cache whose last rows lie past 2^32 bytes gives the bits of a small cache of the same rows."""
+    import torch
+    rng = np.random.default_rng(42)
+    D, H, rows = 128, 3, 2 ** (24 if fmt else 23)
+    k, v, q, dk, dv = (bf16(rng, 1, h, n, D) for h, n in ((H, 190), (H, 190), (2 * H, T), (H, T), (H, T)))
+    m = tmask(tree_bits(rng, 1, T, "chain"))
+    got = []
+    for cap in (192, rows):
+        cs = pisa.CacheShape(1, H, cap, D, fmt)
+        dt = torch.float8_e4m3fn if fmt else torch.bfloat16
+        kv = [torch.empty((1, H, cap, D), dtype=dt, device="cuda") for _ in range(2)]
+        ex = [torch.empty((1, H, cap), dtype=torch.uint8, device="cuda") if fmt else None for _ in range(2)]
+        cache = pisa.Cache(cs, *kv, *ex)
+        ws = pisa.new_cache_workspace("cuda")
+        pisa.cache_write(cache, k, v, ws, start=i32([cap - 192]))
+        back = pisa.cache_read(cache, 190, ws, start=i32([cap - 192]))
+        s = pisa.TreeShape(1, 2 * H, H, T, cap, D, fmt, 64, cap - 64, 2)
+        tw = pisa.new_tree_workspace(s, "cuda")
+        idx = torch.tensor([cap // 64 - 3, cap // 64 - 2], dtype=torch.int32, device="cuda").repeat(1, H, 1, 1)
+        O, lse = pisa.tree_attention(s, cache, q, dk, dv, m, i32([cap - 2]), tw, idx=idx)
+        assert pisa.check_status(ws) == (pisa.OK, 0) and pisa.check_status(tw) == (pisa.OK, 0)
+        got.append((*back, O, lse))
+        del cache, kv, ex
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    torch.cuda.empty_cache()
+
+
 def test_serving_loop(pisa):
     """Prompt into the cache, pyramid, then steps of: norm and rotation of five drafted tokens, selection
     for the first, tree attention over the 8-bit cache, two accepted tokens written, pyramid appended as
