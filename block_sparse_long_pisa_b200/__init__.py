@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-import functools
 import math
 import os
 
@@ -473,18 +472,12 @@ def _launch(where, call, stream, named, args):
     """call(*args, stream) with the device of the tensors current. `named`: (tensor or None, name); all
     must be on one CUDA device. `stream` must be that device's; None is its current one."""
     torch = _torch()
-    dev = -1
+    dev = named[0][0].get_device()   # (the first is always there)
     for t, name in named:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d == dev:
-            continue
-        if d < 0:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev >= 0:
-            raise ValueError(f"{name} must be on cuda:{dev}, got cuda:{d}")
-        dev = d
+        if t is not None and t.get_device() != dev or dev < 0:
+            if dev < 0 or t.get_device() < 0:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{name} must be on cuda:{dev}, got cuda:{t.get_device()}")
     if stream is None:
         raw = _current_stream(dev)
     elif stream.device.index != dev:
@@ -545,13 +538,19 @@ class NormRopeShape:
     eps: float = 1e-6
 
     def c(self, xq=(0, 0, 0), xk=(0, 0, 0), dxq=(0, 0, 0), dxk=(0, 0, 0)) -> PisaNormRopeShape:
-        return _norm_rope_struct(self, xq, xk, dxq, dxk)
-
-
-@functools.lru_cache(maxsize=256)
-def _norm_rope_struct(s, xq, xk, dxq, dxk):
-    return PisaNormRopeShape(s.batch, s.tokens, s.heads_q, s.heads_kv, s.head_dim, s.rotary_dim, int(s.interleaved),
-                             float(s.eps), _i64x3(*xq), _i64x3(*xk), _i64x3(*dxq), _i64x3(*dxk))
+        structs = self.__dict__.get("_structs")   # one a set of strides, kept by the shape itself
+        if structs is None:
+            structs = {}
+            object.__setattr__(self, "_structs", structs)
+        key = (xq, xk, dxq, dxk)
+        c = structs.get(key)
+        if c is None:
+            if len(structs) >= 64:
+                structs.clear()
+            c = structs[key] = PisaNormRopeShape(
+                self.batch, self.tokens, self.heads_q, self.heads_kv, self.head_dim, self.rotary_dim,
+                int(self.interleaved), float(self.eps), _i64x3(*xq), _i64x3(*xk), _i64x3(*dxq), _i64x3(*dxk))
+        return c
 
 
 def norm_rope_workspace_size(shape: NormRopeShape) -> int:
@@ -769,11 +768,14 @@ class TreeShape:
     select_per_qhead: int = 0
     scale: float = 0.0
 
-    @functools.lru_cache(maxsize=256)
     def c(self) -> PisaTreeShape:
-        return PisaTreeShape(self.batch, self.heads_q, self.heads_kv, self.drafts, self.capacity, self.head_dim,
-                             int(self.format), self.block, self.seq_kv, self.topk, int(self.select_per_qhead),
-                             float(self.scale))
+        c = self.__dict__.get("_struct")   # kept by the shape itself
+        if c is None:
+            c = PisaTreeShape(self.batch, self.heads_q, self.heads_kv, self.drafts, self.capacity, self.head_dim,
+                              int(self.format), self.block, self.seq_kv, self.topk, int(self.select_per_qhead),
+                              float(self.scale))
+            object.__setattr__(self, "_struct", c)
+        return c
 
     @property
     def hsel(self) -> int:
@@ -805,16 +807,21 @@ def tree_attention(shape: TreeShape, cache: Cache, Q, K, V, mask, cache_len, ws,
     B, Hq, Hkv, T, D = s.batch, s.heads_q, s.heads_kv, s.drafts, s.head_dim
     if (c.batch, c.heads_kv, c.capacity, c.head_dim, c.format) != (B, Hkv, s.capacity, D, s.format):
         raise ValueError("the shape's batch, heads_kv, capacity, head_dim and format must be the cache's")
-    _like(Q, torch.bfloat16, (B, Hq, T, D), "Q")
-    _like(K, torch.bfloat16, (B, Hkv, T, D), "K")
-    _like(V, torch.bfloat16, (B, Hkv, T, D), "V")
-    _like(mask, torch.int64, (B, T), "mask")
-    _like(cache_len, torch.int32, (B,), "cache_len")
+    qs, kvs, bf16 = (B, Hq, T, D), (B, Hkv, T, D), torch.bfloat16
+    if not (Q.dtype is bf16 and K.dtype is bf16 and V.dtype is bf16 and mask.dtype is torch.int64 and
+            cache_len.dtype is torch.int32 and Q.shape == qs and K.shape == kvs and V.shape == kvs and
+            mask.shape == (B, T) and cache_len.shape == (B,) and Q.is_contiguous() and K.is_contiguous() and
+            V.is_contiguous() and mask.is_contiguous() and cache_len.is_contiguous()):
+        _like(Q, bf16, qs, "Q")
+        _like(K, bf16, kvs, "K")
+        _like(V, bf16, kvs, "V")
+        _like(mask, torch.int64, (B, T), "mask")
+        _like(cache_len, torch.int32, (B,), "cache_len")
     if (idx is not None) != (s.topk > 0):
         raise ValueError("idx goes with topk > 0")
     if idx is not None:
         _like(idx, torch.int32, (B, s.hsel, 1, s.topk), "idx")
-    O = Q.new_empty((B, Hq, T, D)) if O is None else _like(O, torch.bfloat16, (B, Hq, T, D), "O")
+    O = torch.empty_like(Q) if O is None else _like(O, bf16, qs, "O")
     if lse is True:
         lse = Q.new_empty((B, Hq, T), dtype=torch.float32)
     elif lse is False:
