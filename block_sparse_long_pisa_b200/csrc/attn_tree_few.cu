@@ -26,9 +26,8 @@
 // A bf16 cache takes P as bf16 (range of V); so do the drafted tokens.
 //
 // Measured (64 caches of 8 heads of 128, 64 selected blocks of 64 keys and 63 keys of tail, four query heads each):
-// one token over e4m3 0.55 GB in 101 us with the merge, 5.4 TB/s (83 % of the copy rate); the cut into equal runs
-// leaves 96 us of it to this kernel. Four tokens (16 rows) 141 us, bound by issue. Over bf16 1.09 GB: one token
-// 180 us, 6.1 TB/s (92 %), four tokens 188 us.
+// one token over e4m3 0.55 GB in 98 us with the join, 5.6 TB/s (85 % of the copy rate). Four tokens (16 rows)
+// 140 us, bound by issue. Over bf16 1.09 GB: one token 179 us, 6.1 TB/s (93 %), four tokens 186 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

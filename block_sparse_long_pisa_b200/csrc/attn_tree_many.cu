@@ -6,7 +6,7 @@
 // from TMEM, so a score costs no shared memory at all. (Keys on the M side, S^T = K Q^T and O^T = V^T P^T with
 // 32 or 96 rows on N, was built first: K and V are then fetched as the 128-lane operand for every row tile,
 // the values transposed at half the rate, and P goes through shared memory; 363 us for trees of 48 tokens of
-// four heads over 8 ragged bf16 caches, 299 us this way.) A row belongs to two softmax threads, one for each
+// four heads over 8 ragged bf16 caches, 299 us in the first form of this one.) A row belongs to two softmax threads, one for each
 // half of a tile's keys; the two warps meet in one vote a tile.
 //
 // A tile is 128 keys (two units of the cache, or the drafted tokens). Two passes over S in TMEM: the row's
@@ -18,11 +18,19 @@
 // An e4m3 cache is turned into bf16 tiles on the way in: an e4m3 value times a power of two is a bf16 value
 // (rounded once below bf16's smallest normal), and everything after is the same. For each ring one warp fetches
 // the bytes, 32 rows a stage, and two or four converter warps write the swizzled tiles, some 65 instructions for
-// 512 values. That is what bounds this form (64 caches of 8 heads, 64 blocks of 64 keys selected, tokens of four heads,
-// against bf16: 16 tokens 357 us, 252 us; 64 tokens 664 us, 537 us), together with the instruction cache: with
-// the converters' loop unrolled four times and a copy of it for K and one for V, 32 tokens took 786 us and not
-// 424 us (392 us since each warp takes whole steps). (With e4m3 operands in the products instead, P and Q need two and three 8-bit terms and every score a
-// factor from a table: 469 us for the 16 tokens.)
+// 512 values. That is what bounds this form, together with the instruction cache: with the converters' loop
+// unrolled four times and a copy of it for K and one for V, 32 tokens took 786 us and not 424 us (392 us since each
+// warp takes whole steps). (With e4m3 operands in the products instead, P and Q need two and three 8-bit terms and
+// every score a factor from a table: 469 us for 16 tokens.)
+//
+// Measured, with the join: trees of 48 tokens of 32 heads over 8 ragged bf16 caches up to 32,768 rows, 0.72 GB and
+// 0.14 Tflop in 255 us (0.54 Pflop/s, 33 % of the measured peak). 64 caches of 8 heads, 64 blocks of 64 keys selected,
+// tokens of four heads, bf16 (e4m3): 8 tokens 227 us, 16 tokens 243 us (341 us), 32 tokens 278 us (379 us), 64 tokens
+// 473 us (631 us); the copy rate would be 167 us (86 us). What bounds it is the chain of a row tile, S, softmax, P V, S again, of which the other
+// row tile hides a part: tensor pipe 40 %, exponentials 31 %, issue 33 % of their peaks. Steps of 64 keys with two
+// buffers of S a row tile, which break the chain, cost more in the softmax than they hide (296 us for the trees).
+// One elected lane issues the products: to the compiler a branch on the lane's number is not known to be one lane,
+// and each product cost 90 cycles to issue (297 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

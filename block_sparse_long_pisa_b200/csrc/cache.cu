@@ -14,7 +14,8 @@
 // Measured (8 heads of 128, e4m3): write of 131,072 tokens 0.81 GB in 120 us, 6.7 TB/s, the copy rate (two rows
 // share a word in the maximum's shuffles and pairs are scaled at once: 158 us with a word a row, at 67 % of the
 // issue slots); write of one token to each of 64 sequences 2.2 us; read of 7 ragged prefixes 0.29 GB in 48 us,
-// 6.0 TB/s (91 %); pyramids of 8 caches of 32,768 keys 0.29 GB in 64 us, 4.5 TB/s (issue 59 %).
+// 6.0 TB/s (91 %); pyramids of 8 caches of 32,768 keys 0.29 GB in 60 us, 4.9 TB/s (75 %; issue 58 %: two
+// conversions and a fused multiplication for two values that are two bytes).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
