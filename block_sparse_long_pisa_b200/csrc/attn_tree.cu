@@ -24,16 +24,19 @@
 
 namespace pisa {
 
+constexpr unsigned kMergeBlocks = 148 * 12;
+
 // Joins the pieces of the row tiles that crossed runs, in run order: m = max m_i, weights
-// 2^(m_i - m). grid: (row tiles, groups of four rows); 128 threads, one float4 of a row each (D = 128).
+// 2^(m_i - m). grid: (row tiles, shares of their rows); 128 threads, one float4 of a row each (D = 128), a warp a
+// row at a time. Bound by latency and, before the wait, by the 64-bit divisions that find the runs: those are paid
+// once a warp, not once a row.
 template <int D>
 __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p, int RM) {
     const int64_t tile = blockIdx.x;
     const int b = static_cast<int>(tile / p.rows_per_seq);
     const int rem = static_cast<int>(tile % p.rows_per_seq);
     const int hs = rem / p.mt, row_base = (rem % p.mt) * p.rpt;
-    const int rows = p.gh * p.T;
-    const int row = static_cast<int>(blockIdx.y) * 4 + static_cast<int>(threadIdx.x >> 5);
+    const int rows = min(p.rpt, p.gh * p.T - row_base);
     // (what comes before the wait reads the lengths alone, which were there before the runs began)
     const TreeJob job = tree_job(p);
     // units before this row tile (whole warp)
@@ -45,44 +48,58 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
     const int units = tree_units(p, tree_len(p, b));
     const int64_t x0 = before * p.rows_per_seq + static_cast<int64_t>(rem) * units;
     const int64_t c0 = job.run_of(x0), c1 = job.run_of(x0 + units - 1);
+    // the pieces: 2 c0 + 1, then 2 (c0 + 1), 2 (c0 + 2), ..
+    const int stride = RM * (D + 2), pieces = static_cast<int>(c1 - c0) + 1;
+    const float* part = p.part + (2 * c0 + 1) * stride;
+    auto slot = [&](int i) { return part + static_cast<int64_t>(max(2 * i - 1, 0)) * stride; };
+    const int64_t orow0 = (static_cast<int64_t>(b) * p.Hq + hs * p.gh) * p.T + row_base;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // also by a block without rows: the grid ends after the runs
-    if (c0 == c1 || row >= p.rpt || row_base + row >= rows) return;
-    const int64_t stride = static_cast<int64_t>(RM) * (D + 2);
-    auto slot = [&](int64_t c) { return p.part + (2 * c + (c == c0 ? 1 : 0)) * stride; };
-    float M = -INFINITY;
-    for (int64_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, slot(c)[RM * D + 2 * row]);
+    if (pieces == 1) return;
+#pragma unroll 1
+    for (int row = static_cast<int>(blockIdx.y * 4 + (threadIdx.x >> 5)); row < rows; row += static_cast<int>(gridDim.y * 4)) {
+        // (m, l) of piece i in lane i % 32
+        auto ml_of = [&](int i) {
+            return i < pieces ? *reinterpret_cast<const float2*>(slot(i) + RM * D + 2 * row) : make_float2(-INFINITY, 0.f);
+        };
+        const float2 ml0 = ml_of(lane);
+        float M = ml0.x;
+        for (int i = 32 + lane; i < pieces; i += 32) M = fmaxf(M, ml_of(i).x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    constexpr int V = D / 32;  // values of the row per lane
-    float acc[V], l = 0.f;
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+        constexpr int V = D / 32;  // values of the row per lane
+        float acc[V], l = 0.f;
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        for (int i0 = 0; i0 < pieces; i0 += 32) {
+            const float2 ml = i0 == 0 ? ml0 : ml_of(i0 + lane);
+            const float mine = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : fast_exp2(ml.x - M);
 #pragma unroll 4
-    for (int64_t c = c0; c <= c1; ++c) {
-        const float* s = slot(c);
-        const float mc = s[RM * D + 2 * row], lc = s[RM * D + 2 * row + 1];
-        const float w = mc == -INFINITY ? (lc == 0.f ? 0.f : 1.f) : fast_exp2(mc - M);
-        float v[V];
-        if constexpr (V == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(s + row * D + 4 * lane);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-            const float2 x = *reinterpret_cast<const float2*>(s + row * D + 2 * lane);
-            v[0] = x.x, v[1] = x.y;
-        }
-        l += w * lc;
+            for (int i = i0; i < min(pieces, i0 + 32); ++i) {
+                const float* s = slot(i) + row * D;
+                float v[V];
+                if constexpr (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(s + 4 * lane);
+                    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(s + 2 * lane);
+                    v[0] = x.x, v[1] = x.y;
+                }
+                const float w = __shfl_sync(0xFFFFFFFFu, mine, i - i0);
+                l += w * __shfl_sync(0xFFFFFFFFu, ml.y, i - i0);
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] += w * v[k];
+                for (int k = 0; k < V; ++k) acc[k] += w * v[k];
+            }
+        }
+        const int64_t orow = orow0 + row;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if constexpr (V == 4)
+            *reinterpret_cast<uint2*>(p.O + orow * D + 4 * lane) =
+                make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(p.O + orow * D + 2 * lane) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        if (lane == 0 && p.lse != nullptr)
+            p.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
     }
-    const int64_t orow = (static_cast<int64_t>(b) * p.Hq + hs * p.gh) * p.T + row_base + row;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if constexpr (V == 4)
-        *reinterpret_cast<uint2*>(p.O + orow * D + 4 * lane) =
-            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<uint32_t*>(p.O + orow * D + 2 * lane) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0 && p.lse != nullptr)
-        p.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
 // ---------------------------------------------------------------- host side
@@ -103,7 +120,10 @@ int tree_ctas_per_sm(int rm, bool e4m3) { return rm > 16 ? 1 : e4m3 && rm == 8 ?
 
 bool launch_tree_merge(const TreeParams& p, int D, int rm, cudaStream_t st, int32_t* launches) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.rows_per_seq, (p.rpt + 3) / 4);
+    // blocks enough to fill the SMs, and no more than rows
+    const unsigned tiles = static_cast<unsigned>(p.B) * p.rows_per_seq, shares = (p.rpt + 3) / 4;
+    const unsigned want = tiles < kMergeBlocks ? (kMergeBlocks + tiles - 1) / tiles : 1;
+    cfg.gridDim = dim3(tiles, want < shares ? want : shares);
     cfg.blockDim = dim3(128);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
