@@ -24,9 +24,9 @@
 // every score a factor from a table: 469 us for 16 tokens.)
 //
 // Measured, with the join: trees of 48 tokens of 32 heads over 8 ragged bf16 caches up to 32,768 rows, 0.72 GB and
-// 0.14 Tflop in 255 us (0.54 Pflop/s, 33 % of the measured peak). 64 caches of 8 heads, 64 blocks of 64 keys selected,
+// 0.14 Tflop in 250 us (0.55 Pflop/s, 34 % of the measured peak). 64 caches of 8 heads, 64 blocks of 64 keys selected,
 // tokens of four heads, bf16 (e4m3): 8 tokens 227 us, 16 tokens 243 us (341 us), 32 tokens 278 us (379 us), 64 tokens
-// 473 us (631 us); the copy rate would be 167 us (86 us). What bounds it is the chain of a row tile, S, softmax, P V, S again, of which the other
+// 396 us (555 us); the copy rate would be 167 us (86 us). What bounds it is the chain of a row tile, S, softmax, P V, S again, of which the other
 // row tile hides a part: tensor pipe 40 %, exponentials 31 %, issue 33 % of their peaks. Steps of 64 keys with two
 // buffers of S a row tile, which break the chain, cost more in the softmax than they hide (296 us for the trees).
 // One elected lane issues the products: to the compiler a branch on the lane's number is not known to be one lane,
