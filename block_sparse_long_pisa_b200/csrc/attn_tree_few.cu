@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                 }
                 for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < len); left != 0 && ok; left &= left - 1) {
                     const int a = __shfl_sync(0xFFFFFFFFu, at, __ffs(left) - 1);
-                    if (lane == 0) {
+                    if (elect_one()) {
                         ok = used < p.nk || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x11u);
                         if (ok) {
                             meta[s] = min(64, len - a);
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                             }
                         }
                     }
-                    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
                     if (ok) {
                         ++used;
                         advance();
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                 }
             }
             if (u1 == units && ok) {  // the drafted tokens, in a buffer of their own
-                if (lane == 0) {
+                if (elect_one()) {
                     ok = drafts == 0 || mbar_wait(&dempty, dpar ^ 1u, p.status, kTreeDetail | 0x12u);
                     if (ok) {
                         mbar_arrive_expect_tx(&dfull, 2 * C::DRAFT);
@@ -304,21 +304,21 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                         }
                     }
                 }
-                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                ok = __all_sync(0xFFFFFFFFu, ok);
                 if (ok) {
                     ++drafts;
                     dpar ^= 1u;
                 }
             }
             if (ok) {  // end of the piece: a slot without a tile
-                if (lane == 0) {
+                if (elect_one()) {
                     ok = used < p.nk || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x13u);
                     if (ok) {
                         meta[s] = 0;
                         mbar_arrive(&full[s]);
                     }
                 }
-                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+                ok = __all_sync(0xFFFFFFFFu, ok);
                 if (ok) {
                     ++used;
                     advance();
