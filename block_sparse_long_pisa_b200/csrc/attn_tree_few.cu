@@ -27,7 +27,7 @@
 //
 // Measured (64 caches of 8 heads of 128, 64 selected blocks of 64 keys and 63 keys of tail, four query heads each):
 // one token over e4m3 0.55 GB in 98 us with the join, 5.6 TB/s (85 % of the copy rate). Four tokens (16 rows)
-// 140 us, bound by issue. Over bf16 1.09 GB: one token 179 us, 6.1 TB/s (93 %), four tokens 186 us.
+// 139 us, bound by issue. Over bf16 1.09 GB: one token 179 us, 6.1 TB/s (93 %), four tokens 186 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
