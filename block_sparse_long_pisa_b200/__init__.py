@@ -571,13 +571,18 @@ def _norm_rope_args(s: NormRopeShape, Xq, Xk, pos, inv_freq, wq, wk):
     B, T, D = s.batch, s.tokens, s.head_dim
     sq = _rows_like(Xq, torch.bfloat16, (B, T, s.heads_q, D), "Xq")
     sk = _rows_like(Xk, torch.bfloat16, (B, T, s.heads_kv, D), "Xk")
-    if s.rotary_dim or pos is not None:
+    f32, half, row = torch.float32, (s.rotary_dim // 2,), (D,)
+    for t, name in ((pos, "pos"), (inv_freq, "inv_freq")):
+        if t is None and s.rotary_dim:
+            raise ValueError(f"{name} is missing")
+    if not (pos is None or pos.dtype is torch.int32 and pos.shape == (B, T) and pos.is_contiguous()):
         _like(pos, torch.int32, (B, T), "pos")
-    if s.rotary_dim or inv_freq is not None:
-        _like(inv_freq, torch.float32, (s.rotary_dim // 2,), "inv_freq")
-    for w, name in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _like(w, torch.float32, (D,), name)
+    if not (inv_freq is None or inv_freq.dtype is f32 and inv_freq.shape == half and inv_freq.is_contiguous()):
+        _like(inv_freq, f32, half, "inv_freq")
+    if not (wq is None or wq.dtype is f32 and wq.shape == row and wq.is_contiguous()):
+        _like(wq, f32, row, "wq")
+    if not (wk is None or wk.dtype is f32 and wk.shape == row and wk.is_contiguous()):
+        _like(wk, f32, row, "wk")
     return sq, sk
 
 

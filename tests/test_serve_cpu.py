@@ -271,3 +271,14 @@ def test_oracle_tree_equals_dense_softmax_of_the_path():
     p = np.exp(s - s.max(-1, keepdims=True))
     assert np.allclose(O[0, 0], p @ vv / p.sum(-1, keepdims=True))
     assert np.allclose(L[0, 0], s.max(-1) + np.log(p.sum(-1)))
+
+
+def test_rotation_needs_positions_and_frequencies():
+    torch = pytest.importorskip("torch")
+    s = pisa.NormRopeShape(1, 2, 2, 1, 64, 32)
+    x, y = (torch.zeros((1, 2, h, 64), dtype=torch.bfloat16) for h in (2, 1))
+    pos, fr = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(16)
+    for args, name in (((None, fr), "pos"), ((pos, None), "inv_freq"), ((pos.long(), fr), "pos"),
+                       ((pos, fr[:8]), "inv_freq")):
+        with pytest.raises(ValueError, match=name):
+            pisa.qk_norm_rope(s, x, y, *args)
