@@ -226,6 +226,21 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _made(stream, make):
+    """make(), a tensor of a call that runs on `stream` (None: the current one): allocated and filled there, so that
+    neither the fill nor a later owner of freed memory can meet the call's kernels. It is returned to work on the
+    caller's current stream, which its memory is kept for too."""
+    if stream is None:
+        return make()
+    torch = _torch()
+    mine = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make()
+    if mine != stream:
+        t.record_stream(mine)
+    return t
+
+
 def _need(t, dtype, shape, name):
     torch = _torch()
     if not t.is_cuda:
@@ -730,9 +745,13 @@ def cache_read(cache: Cache, tokens: int, ws, start=None, count=None, K=None, V=
     rows = (s.batch, s.heads_kv, int(tokens), s.head_dim)
     if tokens < 1:
         raise ValueError("tokens must be at least 1")
-    make = torch.empty if count is None and start is None else torch.zeros
-    K = make(rows, dtype=torch.bfloat16, device=cache.device) if K is None else _like(K, torch.bfloat16, rows, "K")
-    V = make(rows, dtype=torch.bfloat16, device=cache.device) if V is None else _like(V, torch.bfloat16, rows, "V")
+    fill = torch.empty if count is None and start is None else torch.zeros
+
+    def make():
+        return fill(rows, dtype=torch.bfloat16, device=cache.device)
+
+    K = _made(stream, make) if K is None else _like(K, torch.bfloat16, rows, "K")
+    V = _made(stream, make) if V is None else _like(V, torch.bfloat16, rows, "V")
     _ranges(s.batch, start, count)
     _status_word(ws)
     _launch("pisa_cache_read", _lib.pisa_cache_read, stream,
