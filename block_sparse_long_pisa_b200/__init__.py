@@ -266,7 +266,8 @@ def build_pyramid(shape: Shape, K, pyramid=None, stream=None):
     _need(K, torch.bfloat16, (shape.batch, shape.heads_kv, shape.kv_rows, D), "K")
     sizes, _ = level_layout(shape)
     if pyramid is None:
-        pyramid = torch.empty((shape.batch, shape.heads_kv, sum(sizes), D), dtype=torch.float32, device=K.device)
+        pyramid = _made(stream, lambda: torch.empty((shape.batch, shape.heads_kv, sum(sizes), D), dtype=torch.float32,
+                                                    device=K.device))
     _check(_lib.pisa_build_pyramid(ctypes.byref(shape.c()), _ptr(K), _ptr(pyramid), _stream(stream)),
            "pisa_build_pyramid")
     return pyramid
@@ -285,9 +286,10 @@ def select_blocks(shape: Shape, Q, pyramid, ws, level_budget=None, idx=None, mar
     torch = _torch()
     _need(Q, torch.bfloat16, (shape.batch, shape.heads_q, shape.seq_q, shape.head_dim), "Q")
     if idx is None:
-        idx = torch.empty((shape.batch, shape.hsel, shape.n_qblocks, shape.topk), dtype=torch.int32, device=Q.device)
-    marg = torch.empty((shape.batch, shape.hsel, shape.n_qblocks), dtype=torch.float32, device=Q.device) \
-        if margin else None
+        idx = _made(stream, lambda: torch.empty((shape.batch, shape.hsel, shape.n_qblocks, shape.topk), dtype=torch.int32,
+                                                device=Q.device))
+    marg = _made(stream, lambda: torch.empty((shape.batch, shape.hsel, shape.n_qblocks), dtype=torch.float32,
+                                             device=Q.device)) if margin else None
     budget = None
     if level_budget is not None:
         budget = (ctypes.c_int32 * len(level_budget))(*[int(x) for x in level_budget])
@@ -301,8 +303,8 @@ def sparse_attention(shape: Shape, Q, K, V, idx, ws, O=None, lse=True, stream=No
     B, Hq, Nq, D = shape.batch, shape.heads_q, shape.seq_q, shape.head_dim
     _need(Q, torch.bfloat16, (B, Hq, Nq, D), "Q")
     if O is None:
-        O = torch.empty_like(Q)
-    L = torch.empty((B, Hq, Nq), dtype=torch.float32, device=Q.device) if lse is True else lse
+        O = _made(stream, lambda: torch.empty_like(Q))
+    L = _made(stream, lambda: torch.empty((B, Hq, Nq), dtype=torch.float32, device=Q.device)) if lse is True else lse
     _check(_lib.pisa_sparse_attention(ctypes.byref(shape.c()), _ptr(Q), _ptr(K), _ptr(V), _ptr(idx), _ptr(O),
                                       _ptr(L), _ptr(ws), ws.numel(), _stream(stream)), "pisa_sparse_attention")
     return O, L
@@ -316,10 +318,11 @@ def forward(shape: Shape, Q, K, V, ws, O=None, lse=True, idx=None, stream=None):
     _need(K, torch.bfloat16, (B, shape.heads_kv, shape.kv_rows, D), "K")
     _need(V, torch.bfloat16, (B, shape.heads_kv, shape.kv_rows, D), "V")
     if O is None:
-        O = torch.empty_like(Q)
-    L = torch.empty((B, Hq, Nq), dtype=torch.float32, device=Q.device) if lse is True else lse
+        O = _made(stream, lambda: torch.empty_like(Q))
+    L = _made(stream, lambda: torch.empty((B, Hq, Nq), dtype=torch.float32, device=Q.device)) if lse is True else lse
     if idx is True:
-        idx = torch.empty((B, shape.hsel, shape.n_qblocks, shape.topk), dtype=torch.int32, device=Q.device)
+        idx = _made(stream, lambda: torch.empty((B, shape.hsel, shape.n_qblocks, shape.topk), dtype=torch.int32,
+                                                device=Q.device))
     _check(_lib.pisa_forward(ctypes.byref(shape.c()), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(L), _ptr(idx),
                              _ptr(ws), ws.numel(), _stream(stream)), "pisa_forward")
     return O, L, idx
@@ -331,8 +334,8 @@ def decode_attention_noalloc(shape: Shape, Q, K, V, idx, O=None, lse=True, strea
     B, Hq, D = shape.batch, shape.heads_q, shape.head_dim
     _need(Q, torch.bfloat16, (B, Hq, 1, D), "Q")
     if O is None:
-        O = torch.empty_like(Q)
-    L = torch.empty((B, Hq, 1), dtype=torch.float32, device=Q.device) if lse is True else lse
+        O = _made(stream, lambda: torch.empty_like(Q))
+    L = _made(stream, lambda: torch.empty((B, Hq, 1), dtype=torch.float32, device=Q.device)) if lse is True else lse
     _check(_lib.pisa_decode_attention_noalloc(ctypes.byref(shape.c()), _ptr(Q), _ptr(K), _ptr(V), _ptr(idx),
                                               _ptr(O), _ptr(L), _stream(stream)), "pisa_decode_attention_noalloc")
     return O, L
@@ -364,10 +367,10 @@ def sparse_attention_backward(shape: Shape, Q, K, V, O, lse, dO, idx, ws=None, d
     _need(lse, torch.float32, (B, Hq, N), "lse")
     _need(idx, torch.int32, (B, shape.hsel, shape.n_qblocks, shape.topk), "idx")
     if ws is None:
-        ws = torch.zeros(backward_workspace_size(shape), dtype=torch.uint8, device=Q.device)
-    dQ = torch.empty_like(Q) if dQ is None else dQ
-    dK = torch.empty_like(K) if dK is None else dK
-    dV = torch.empty_like(V) if dV is None else dV
+        ws = _made(stream, lambda: torch.zeros(backward_workspace_size(shape), dtype=torch.uint8, device=Q.device))
+    dQ = _made(stream, lambda: torch.empty_like(Q)) if dQ is None else dQ
+    dK = _made(stream, lambda: torch.empty_like(K)) if dK is None else dK
+    dV = _made(stream, lambda: torch.empty_like(V)) if dV is None else dV
     _check(_lib.pisa_sparse_attention_backward(ctypes.byref(shape.c()), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse),
                                                _ptr(dO), _ptr(idx), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(),
                                                _stream(stream)), "pisa_sparse_attention_backward")
@@ -610,8 +613,8 @@ def qk_norm_rope(shape: NormRopeShape, Xq, Xk, pos, inv_freq, wq=None, wk=None, 
     s = shape
     sq, sk = _norm_rope_args(s, Xq, Xk, pos, inv_freq, wq, wk)
     qs, ks = (s.batch, s.heads_q, s.tokens, s.head_dim), (s.batch, s.heads_kv, s.tokens, s.head_dim)
-    Q = Xq.new_empty(qs) if Q is None else _like(Q, torch.bfloat16, qs, "Q")
-    K = Xq.new_empty(ks) if K is None else _like(K, torch.bfloat16, ks, "K")
+    Q = _made(stream, lambda: Xq.new_empty(qs)) if Q is None else _like(Q, torch.bfloat16, qs, "Q")
+    K = _made(stream, lambda: Xq.new_empty(ks)) if K is None else _like(K, torch.bfloat16, ks, "K")
     _launch("pisa_qk_norm_rope", _lib.pisa_qk_norm_rope, stream,
             ((Xq, "Xq"), (Xk, "Xk"), (pos, "pos"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"), (Q, "Q"), (K, "K")),
             (s.c(sq, sk), Xq.data_ptr(), Xk.data_ptr(), _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(pos), Q.data_ptr(),
@@ -630,14 +633,14 @@ def qk_norm_rope_backward(shape: NormRopeShape, Xq, Xk, pos, inv_freq, dQ, dK, w
     sq, sk = _norm_rope_args(s, Xq, Xk, pos, inv_freq, wq, wk)
     _like(dQ, torch.bfloat16, (B, s.heads_q, T, D), "dQ")
     _like(dK, torch.bfloat16, (B, s.heads_kv, T, D), "dK")
-    dXq = Xq.new_empty((B, T, s.heads_q, D)) if dXq is None else dXq
-    dXk = Xq.new_empty((B, T, s.heads_kv, D)) if dXk is None else dXk
+    dXq = _made(stream, lambda: Xq.new_empty((B, T, s.heads_q, D))) if dXq is None else dXq
+    dXk = _made(stream, lambda: Xq.new_empty((B, T, s.heads_kv, D))) if dXk is None else dXk
     gq = _rows_like(dXq, torch.bfloat16, (B, T, s.heads_q, D), "dXq")
     gk = _rows_like(dXk, torch.bfloat16, (B, T, s.heads_kv, D), "dXk")
-    dwq = wq.new_empty(D) if wq is not None else None
-    dwk = wk.new_empty(D) if wk is not None else None
+    dwq = _made(stream, lambda: wq.new_empty(D)) if wq is not None else None
+    dwk = _made(stream, lambda: wk.new_empty(D)) if wk is not None else None
     if ws is None:
-        ws = new_norm_rope_workspace(s, Xq.device)
+        ws = _made(stream, lambda: new_norm_rope_workspace(s, Xq.device))
     _launch("pisa_qk_norm_rope_backward", _lib.pisa_qk_norm_rope_backward, stream,
             ((Xq, "Xq"), (Xk, "Xk"), (pos, "pos"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"), (dQ, "dQ"),
              (dK, "dK"), (dXq, "dXq"), (dXk, "dXk"), (ws, "ws")),
@@ -845,9 +848,9 @@ def tree_attention(shape: TreeShape, cache: Cache, Q, K, V, mask, cache_len, ws,
         raise ValueError("idx goes with topk > 0")
     if idx is not None:
         _like(idx, torch.int32, (B, s.hsel, 1, s.topk), "idx")
-    O = torch.empty_like(Q) if O is None else _like(O, bf16, qs, "O")
+    O = _made(stream, lambda: torch.empty_like(Q)) if O is None else _like(O, bf16, qs, "O")
     if lse is True:
-        lse = Q.new_empty((B, Hq, T), dtype=torch.float32)
+        lse = _made(stream, lambda: Q.new_empty((B, Hq, T), dtype=torch.float32))
     elif lse is False:
         lse = None
     elif lse is not None:

@@ -68,3 +68,17 @@ def test_cache_read_fills_its_outputs_on_its_stream(made):
     n, ws = torch.zeros(2, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
     for kw in (dict(count=n), dict(start=n), dict()):
         assert all(made(lambda s: pisa.cache_read(cache, 5, ws, stream=s, **kw)))
+
+
+def test_calls_make_their_outputs_and_scratch_on_their_stream(made):
+    nr = pisa.NormRopeShape(1, 2, 2, 1, 64, 0)
+    xq, xk, w = bf16(1, 2, 2, 64), bf16(1, 2, 1, 64), torch.ones(64)
+    assert all(made(lambda s: pisa.qk_norm_rope(nr, xq, xk, None, None, stream=s)))
+    grads = (bf16(1, 2, 2, 64), bf16(1, 1, 2, 64))
+    seen = made(lambda s: pisa.qk_norm_rope_backward(nr, xq, xk, None, None, *grads, w, w, stream=s))
+    assert len(seen) == 5 and all(seen)              # dXq, dXk, dwq, dwk and the partial sums
+    s = pisa.TreeShape(1, 2, 1, 2, 64, 64)
+    q, kv, mask, n = bf16(1, 2, 2, 64), bf16(1, 1, 2, 64), torch.zeros((1, 2), dtype=torch.int64), torch.zeros(1, dtype=torch.int32)
+    cache, ws = pisa.new_cache(pisa.CacheShape(1, 1, 64, 64), "cpu"), torch.zeros(4096, dtype=torch.uint8)
+    seen = made(lambda st: pisa.tree_attention(s, cache, q, kv, kv, mask, n, ws, stream=st))
+    assert len(seen) == 2 and all(seen)
