@@ -518,7 +518,7 @@ def _like(t, dtype, shape, name):
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
@@ -528,7 +528,7 @@ def _rows_like(t, dtype, shape, name):
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     a, b, c, last = t.stride()
     if last != 1:
         raise ValueError(f"{name} must have adjacent elements in its last dimension")
@@ -666,37 +666,65 @@ class CacheShape:
 class Cache:
     """A K/V cache's buffers: k and v [B, heads_kv, capacity, D] (bf16, or float8_e4m3fn with the
     exponent bytes k_exp and v_exp, uint8 [B, heads_kv, capacity]: a row is its values times
-    2^(byte - 127)). v and v_exp may be None for calls that only read keys (cache_append_pyramid)."""
+    2^(byte - 127)). v and v_exp may be None for calls that only read keys (cache_append_pyramid).
+    The buffers are those of its making (a larger cache is a new Cache); every call checks that they
+    are still such buffers and takes their addresses as they are then."""
 
     def __init__(self, shape: CacheShape, k, v, k_exp=None, v_exp=None):
+        if v is None and v_exp is not None:
+            raise ValueError("v_exp without v")
+        self._shape, self._c, self._buffers = shape, shape.c(), (k, v, k_exp, v_exp)
         torch = _torch()
-        s = shape
-        fp8 = s.format == CACHE_E4M3
-        rows = (s.batch, s.heads_kv, s.capacity)
+        self._rows = torch.Size((shape.batch, shape.heads_kv, shape.capacity))
+        self._whole = torch.Size((*self._rows, shape.head_dim))
+        self._types = (torch.float8_e4m3fn if shape.format == CACHE_E4M3 else torch.bfloat16, torch.uint8)
+        self._check()
+
+    def _check(self):
+        dt, u8 = self._types
+        k, v, k_exp, v_exp = self._buffers
+        fp8 = self._shape.format == CACHE_E4M3
         for t, e, name in ((k, k_exp, "k"), (v, v_exp, "v")):
             if t is None and name == "v":
-                if e is not None:
-                    raise ValueError("v_exp without v")
                 continue
-            _like(t, torch.float8_e4m3fn if fp8 else torch.bfloat16, (*rows, s.head_dim), name)
+            _like(t, dt, self._whole, name)
             if fp8:
                 if e is None:
                     raise ValueError(f"{name}_exp is missing")
-                _like(e, torch.uint8, rows, f"{name}_exp")
+                _like(e, u8, self._rows, f"{name}_exp")
             elif e is not None:
                 raise ValueError(f"{name}_exp belongs to an e4m3 cache")
-        self.shape, self.k, self.v, self.k_exp, self.v_exp = s, k, v, k_exp, v_exp
-        self.device = k.device
-        self._c = s.c()
-        self._ptrs = tuple(_ptr(t) for t in (k, v, k_exp, v_exp))
         for t, name in ((v, "v"), (k_exp, "k_exp"), (v_exp, "v_exp")):
             if t is not None and t.device != k.device:
                 raise ValueError(f"{name} must be on {k.device}, got {t.device}")
 
+    shape = property(lambda self: self._shape)
+    k = property(lambda self: self._buffers[0])
+    v = property(lambda self: self._buffers[1])
+    k_exp = property(lambda self: self._buffers[2])
+    v_exp = property(lambda self: self._buffers[3])
+    device = property(lambda self: self._buffers[0].device)
+
     def _both(self):
-        if self.v is None:
+        if self._buffers[1] is None:
             raise ValueError("the cache has no v")
         return self
+
+    def _ptrs(self):
+        """The buffers' addresses at this call; what a resize_ or set_ made of them is checked first."""
+        k, v, k_exp, v_exp = self._buffers
+        dt, u8 = self._types
+        whole, rows, dev = self._whole, self._rows, k.get_device()
+        if not (k.dtype is dt and k.shape == whole and k.is_contiguous() and
+                (v is None or v.dtype is dt and v.shape == whole and v.is_contiguous() and v.get_device() == dev)):
+            self._check()
+        if k_exp is None:
+            return k.data_ptr(), _ptr(v), None, None
+        if not (k_exp.dtype is u8 and k_exp.shape == rows and k_exp.is_contiguous() and k_exp.get_device() == dev and
+                (v_exp is None or v_exp.dtype is u8 and v_exp.shape == rows and v_exp.is_contiguous() and
+                 v_exp.get_device() == dev)):
+            self._check()
+        return k.data_ptr(), _ptr(v), k_exp.data_ptr(), _ptr(v_exp)
 
 
 def new_cache(shape: CacheShape, device) -> Cache:
@@ -737,7 +765,7 @@ def cache_write(cache: Cache, K, V, ws, start=None, count=None, stream=None) -> 
     _launch("pisa_cache_write", _lib.pisa_cache_write, stream,
             ((cache.k, "cache"), (K, "K"), (V, "V"), (start, "start"), (count, "count"), (ws, "ws")),
             (cache._c, rows[2], K.data_ptr(), V.data_ptr(), _i64x3(*sk), _i64x3(*sv), _ptr(start), _ptr(count),
-             *cache._ptrs, ws.data_ptr()))
+             *cache._ptrs(), ws.data_ptr()))
 
 
 def cache_read(cache: Cache, tokens: int, ws, start=None, count=None, K=None, V=None, stream=None):
@@ -759,7 +787,7 @@ def cache_read(cache: Cache, tokens: int, ws, start=None, count=None, K=None, V=
     _status_word(ws)
     _launch("pisa_cache_read", _lib.pisa_cache_read, stream,
             ((cache.k, "cache"), (K, "K"), (V, "V"), (start, "start"), (count, "count"), (ws, "ws")),
-            (cache._c, rows[2], *cache._ptrs, _ptr(start), _ptr(count), K.data_ptr(), V.data_ptr(), ws.data_ptr()))
+            (cache._c, rows[2], *cache._ptrs(), _ptr(start), _ptr(count), K.data_ptr(), V.data_ptr(), ws.data_ptr()))
     return K, V
 
 
@@ -773,9 +801,9 @@ def cache_append_pyramid(shape: Shape, cache: Cache, pyramid, seq_kv_old: int, s
     if (s.batch, s.heads_kv, s.capacity, s.head_dim) != (shape.batch, shape.heads_kv, shape.kv_rows, shape.head_dim):
         raise ValueError("the shape's batch, heads_kv, capacity and head_dim must be the cache's")
     _like(pyramid, torch.float32, (s.batch, s.heads_kv, shape.n_nodes, s.head_dim), "pyramid")
+    k, _, k_exp, _ = cache._ptrs()
     _launch("pisa_cache_append_pyramid", _lib.pisa_cache_append_pyramid, stream,
-            ((cache.k, "cache"), (pyramid, "pyramid")),
-            (shape.c(), cache._ptrs[0], cache._ptrs[2], pyramid.data_ptr(), int(seq_kv_old)))
+            ((cache.k, "cache"), (pyramid, "pyramid")), (shape.c(), k, k_exp, pyramid.data_ptr(), int(seq_kv_old)))
     return pyramid
 
 
@@ -859,7 +887,7 @@ def tree_attention(shape: TreeShape, cache: Cache, Q, K, V, mask, cache_len, ws,
     _launch("pisa_tree_attention", _lib.pisa_tree_attention, stream,
             ((Q, "Q"), (K, "K"), (V, "V"), (mask, "mask"), (cache_len, "cache_len"), (cache.k, "cache"), (idx, "idx"),
              (O, "O"), (lse, "lse"), (ws, "ws")),
-            (s.c(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), mask.data_ptr(), *cache._ptrs, cache_len.data_ptr(),
+            (s.c(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), mask.data_ptr(), *cache._ptrs(), cache_len.data_ptr(),
              _ptr(idx), O.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel()))
     return O, lse
 
