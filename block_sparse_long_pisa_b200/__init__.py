@@ -641,6 +641,8 @@ def qk_norm_rope_backward(shape: NormRopeShape, Xq, Xk, pos, inv_freq, dQ, dK, w
     dwk = _made(stream, lambda: wk.new_empty(D)) if wk is not None else None
     if ws is None:
         ws = _made(stream, lambda: new_norm_rope_workspace(s, Xq.device))
+    elif not ws.is_contiguous():   # its bytes are counted from its elements
+        raise ValueError("ws must be contiguous")
     _launch("pisa_qk_norm_rope_backward", _lib.pisa_qk_norm_rope_backward, stream,
             ((Xq, "Xq"), (Xk, "Xk"), (pos, "pos"), (inv_freq, "inv_freq"), (wq, "wq"), (wk, "wk"), (dQ, "dQ"),
              (dK, "dK"), (dXq, "dXq"), (dXk, "dXk"), (ws, "ws")),

@@ -282,3 +282,15 @@ def test_rotation_needs_positions_and_frequencies():
                        ((pos, fr[:8]), "inv_freq")):
         with pytest.raises(ValueError, match=name):
             pisa.qk_norm_rope(s, x, y, *args)
+
+
+def test_norm_rope_backward_needs_a_workspace_of_adjacent_bytes():
+    """A workspace of one repeated byte, or every other byte of one, counts more bytes than it has."""
+    torch = pytest.importorskip("torch")
+    s = pisa.NormRopeShape(1, 2, 2, 1, 64, 0)
+    x, y = torch.zeros((1, 2, 2, 64), dtype=torch.bfloat16), torch.zeros((1, 2, 1, 64), dtype=torch.bfloat16)
+    n = pisa.norm_rope_workspace_size(s)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(n), torch.zeros(2 * n, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            pisa.qk_norm_rope_backward(s, x, y, None, None, x.transpose(1, 2).contiguous(), y.transpose(1, 2).contiguous(),
+                                       ws=ws)
