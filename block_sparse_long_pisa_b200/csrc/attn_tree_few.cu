@@ -110,7 +110,7 @@ struct FewCfg {
 };
 
 // One warp's state: for its rows 2 (lane % 4), + 1 of every row tile of 8 the reference that its
-// probabilities are taken against (a maximum so far, log2 units; 0 while there is none) and the sum over
+// probabilities are taken against (a maximum so far, log2 units; kTreeNone while there is none) and the sum over
 // its keys; O^T: tile j is dims 16 j + lane / 4 (+ 8) (e4m3: 16 j + 2 (lane / 4), + 1); the unit exponent of
 // O and the V exponent that it was set by.
 template <int D, int NT>
@@ -148,8 +148,7 @@ __device__ __forceinline__ void few_softmax(FewState<D, NT>& s, float (&x)[NT][4
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
                 const float old = s.ref[t][e2];
-                // a row with nothing so far keeps 0 (its scores are all -inf and give 0)
-                const float now = s.fresh ? (top == -INFINITY ? 0.f : top) : fmaxf(old, top);
+                const float now = s.fresh ? fmaxf(kTreeNone, top) : fmaxf(old, top);
                 a[e2] = s.fresh || now == old ? 1.f : fast_exp2(old - now);
                 s.ref[t][e2] = now;
                 s.l[t][e2] *= a[e2];
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) st.o[t][j][0] = st.o[t][j][1] = st.o[t][j][2] = st.o[t][j][3] = 0.f;
-            st.ref[t][0] = st.ref[t][1] = 0.f;
+            st.ref[t][0] = st.ref[t][1] = kTreeNone;
             st.l[t][0] = st.l[t][1] = 0.f;
         }
         st.u = 0;

@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&qfull);
 
-            float m = 0.f;      // the reference: a maximum so far, log2 units; 0 while there is none
+            float m = kTreeNone;  // the reference: a maximum so far, log2 units
             uint64_t l2 = 0ull; // the row's sum, in two halves
             bool fresh = true;
             while (true) {
@@ -639,8 +639,7 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                         *mine_x = top;
                         named_bar_sync(pair, 64);
                         top = fmaxf(top, *other_x);
-                        // a row with nothing so far keeps 0 (its scores are all -inf and give 0)
-                        const float now = fresh ? (top == -INFINITY ? 0.f : top) : fmaxf(m, top);
+                        const float now = fmaxf(m, top);
                         const float a = fresh || now == m ? 1.f : fast_exp2(m - now);
                         m = now;
                         if (!fresh) {

@@ -10,6 +10,9 @@ namespace pisa {
 
 constexpr uint32_t kTreeDetail = kKernTree << 8;
 constexpr int kTreeUMin = -100;  // smallest unit exponent of O (e4m3)
+// The reference of a row without a finite score so far: below every score, so that the first one moves it, and finite, so
+// that a score of minus infinity stays one. (A reference of 0 would round scores below -126 away that come later.)
+constexpr float kTreeNone = -3.402823466e+38f;
 
 // ---------------------------------------------------------------- the runs
 

@@ -1,8 +1,10 @@
-"""The operators around the attention in calls that an earlier form of them answered wrongly."""
+"""The operators around the attention in calls that an earlier form of them answered wrongly. Tolerances are those of
+test_gpu_serve.py."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_serve import bf16, f32, fill, i32
+from oracle import serve_oracle as so
+from tests.test_gpu_serve import bf16, f32, fill, host, i32, raw, tmask, tree_bits, tree_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -67,7 +69,6 @@ def test_scratch_of_the_gradients_is_kept_from_others(pisa):
 def test_outputs_made_on_another_stream(pisa):
     """Outputs of a call on another stream do not take memory that the current stream has yet to read."""
     import torch
-    from tests.test_gpu_serve import tmask, tree_inputs
     case = (2, 4, 2, 5, 512, 128, 1, 64, 0, 0, 0, [500, 77], "tree")
     s, cache, k, v, q, dk, dv, mask, lens, idx = tree_inputs(pisa, case, 73)
     ws, m, n, side = pisa.new_tree_workspace(s, "cuda"), tmask(mask), i32(lens), torch.cuda.Stream()
@@ -80,3 +81,42 @@ def test_outputs_made_on_another_stream(pisa):
     O, lse = pisa.tree_attention(s, cache, q, dk, dv, m, n, ws, stream=side)
     torch.cuda.synchronize()
     assert bool((kept == 5.0).all()) and torch.equal(O, want) and torch.equal(lse, want_lse)
+
+
+# T, Hq, D: 4, 16 and two tiles of 16 rows (few), one and two tiles of 128 (many)
+FORMS = [(1, 4, 128), (1, 4, 64), (4, 4, 128), (7, 2, 64), (7, 4, 128), (24, 4, 128), (40, 4, 64)]
+
+
+# ----------------------------------------------------------------------------- scores of minus infinity
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("T, Hq, D", FORMS)
+def test_keys_of_minus_infinity_come_first(pisa, T, Hq, D, fmt):
+    """Two blocks of keys whose scores overflow to minus infinity, then keys with scores of about -300: the result is that
+    of the later keys alone. 400 sequences of the same rows, so that a run holds several units of each."""
+    rng = np.random.default_rng(9)
+    import torch
+    B, cap = 400, 320
+    K, V = bf16(rng, 1, 1, cap, D), bf16(rng, 1, 1, cap, D)
+    q = bf16(rng, 1, Hq, T, D, scale=0.05).add_(1).mul_(2.0 ** 60)
+    K = (K * 0.02 - 300.0 / np.sqrt(D)) * 2.0 ** -60
+    K[:, :, :128] = -2.0 ** 100
+    dk, dv = bf16(rng, 1, 1, T, D), bf16(rng, 1, 1, T, D)
+    wide = lambda t: t.expand(B, -1, -1, -1).contiguous()
+    cache = pisa.new_cache(pisa.CacheShape(B, 1, cap, D, fmt), "cuda")
+    pisa.cache_write(cache, wide(K), wide(V), pisa.new_cache_workspace("cuda"))
+    if fmt:
+        kb, vb, ke, ve = raw(cache)
+        k, v = so.row_values(kb[:1], ke[:1]), so.row_values(vb[:1], ve[:1])
+    else:
+        k, v = host(cache.k[:1]), host(cache.v[:1])
+    s = pisa.TreeShape(B, Hq, 1, T, cap, D, fmt, 64, 256, 4)
+    idx = np.tile(np.array([0, 1, 2, 3], np.int32), (B, 1, 1, 1))
+    mask, lens, ws = np.zeros((B, T), np.uint64), np.full(B, cap), pisa.new_tree_workspace(s, "cuda")
+    O, lse = pisa.tree_attention(s, cache, wide(q), wide(dk), wide(dv), tmask(mask), i32(lens), ws, idx=i32(idx))
+    later = np.array([-1, -1, 2, 3], np.int32).reshape(1, 1, 1, 4)
+    ref, L, A, S = so.tree_attention(host(q), host(dk), host(dv), mask[:1], k, v, lens[:1], later, block=64, seq_kv=256,
+                                     topk=4, per_qhead=False, scale=0.0)
+    e = 2.0 ** -18 * S
+    assert (np.abs(host(O) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e[..., None]) * A).all()
+    assert (np.abs(host(lse) - L) <= e + 2.0 ** -20 * np.abs(L) + 2.0 ** -18).all()
