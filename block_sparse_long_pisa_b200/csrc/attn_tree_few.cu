@@ -122,8 +122,8 @@ struct FewState {
 };
 
 // Scores of 16 keys (log2 units, -inf where masked; [0], [1]: this thread's first key, [2], [3]: its
-// second), ev: the larger V exponent of the two -> probabilities. References move, and O and the sums
-// with them, when a score exceeds one by kFewLazy; the unit when an exponent exceeds the one it was set by.
+// second), ev: the larger V exponent of the two -> probabilities. A row's reference moves, and its O and sum
+// with it, when one of its scores exceeds it by kFewLazy; the unit when an exponent exceeds the one it was set by.
 template <int D, int NT>
 __device__ __forceinline__ void few_softmax(FewState<D, NT>& s, float (&x)[NT][4], int ev) {
     bool over = s.fresh || ev > s.uexp;
@@ -148,7 +148,8 @@ __device__ __forceinline__ void few_softmax(FewState<D, NT>& s, float (&x)[NT][4
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
                 const float old = s.ref[t][e2];
-                const float now = s.fresh ? fmaxf(kTreeNone, top) : fmaxf(old, top);
+                // only a row that exceeds its own reference moves it: what another row attends changes no bit of this one
+                const float now = s.fresh ? fmaxf(kTreeNone, top) : top > old + kFewLazy ? top : old;
                 a[e2] = s.fresh || now == old ? 1.f : fast_exp2(old - now);
                 s.ref[t][e2] = now;
                 s.l[t][e2] *= a[e2];

@@ -639,7 +639,9 @@ __global__ void __launch_bounds__(ManyCfg<D, E4M3, NM>::THREADS, 1)
                         *mine_x = top;
                         named_bar_sync(pair, 64);
                         top = fmaxf(top, *other_x);
-                        const float now = fmaxf(m, top);
+                        // only a row that exceeds its own reference moves it: what another row attends changes no bit of
+                        // this one
+                        const float now = fresh ? fmaxf(m, top) : top > m + kManyLazy ? top : m;
                         const float a = fresh || now == m ? 1.f : fast_exp2(m - now);
                         m = now;
                         if (!fresh) {

@@ -120,3 +120,25 @@ def test_keys_of_minus_infinity_come_first(pisa, T, Hq, D, fmt):
     e = 2.0 ** -18 * S
     assert (np.abs(host(O) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e[..., None]) * A).all()
     assert (np.abs(host(lse) - L) <= e + 2.0 ** -20 * np.abs(L) + 2.0 ** -18).all()
+
+
+# ----------------------------------------------------------------------------- drafted tokens that are not attended
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("T, Hq, D", [(5, 1, 128), (8, 2, 64), (7, 4, 128), (24, 4, 128), (40, 4, 64)])
+def test_drafts_that_are_not_attended_change_no_bit(pisa, fmt, T, Hq, D):
+    """Drafted tokens 1 and 2 become other finite or non-finite rows: tokens that attend neither keep O and LSE bit for bit."""
+    import torch
+    case = (2, 2 * Hq, 2, T, 512, D, fmt, 64, 0, 0, 0, [500, 77], "chain")
+    s, cache, k, v, q, dk, dv, mask, lens, idx = tree_inputs(pisa, case, 61)
+    for t in range(T):
+        mask[:, t] = np.uint64((1 << t) | (1 if t % 3 else 0b110 if t > 2 else 0))
+    rest = [t for t in range(T) if t not in (1, 2) and t % 3]
+    ws = pisa.new_tree_workspace(s, "cuda")
+    O, lse = pisa.tree_attention(s, cache, q, dk, dv, tmask(mask), i32(lens), ws)
+    for scale_k, scale_v in ((30.0, 1.0), (1.0, 2.0 ** 40), (30.0, float("inf")), (float("nan"), float("nan"))):
+        dk2, dv2 = dk.clone(), dv.clone()
+        dk2[:, :, 1:3] *= scale_k
+        dv2[:, :, 1:3] *= scale_v
+        O2, lse2 = pisa.tree_attention(s, cache, q, dk2, dv2, tmask(mask), i32(lens), ws)
+        assert torch.equal(O[:, :, rest], O2[:, :, rest]) and torch.equal(lse[:, :, rest], lse2[:, :, rest])
