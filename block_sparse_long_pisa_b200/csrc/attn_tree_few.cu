@@ -17,17 +17,21 @@
 //   * Q is scaled by a power of two per row to a maximum in [2^14, 2^15) and rounded to fp16, which
 //     keeps bf16's 8 bits for values down to 2^-29 of the row's largest.
 //   * K's row exponent and Q's come back as an exact factor of the score, in fp32.
-//   * V's row exponent goes into P: P' = p 2^(e - 127 - u), u the largest V exponent so far less 7, O in
-//     units of 2^u. P <= 2^8, so P' <= 2^15 fits fp16; it keeps 11 bits down to 2^-21 of the largest
-//     row times the largest p, and a floor of 2^-31 below.
+//   * V's row exponent goes into P. A key's weight is p 2^(e - 127), and every row has a power of two f of its own, set by
+//     the largest weight that it has met: P' = p f 2^(e - 127), 2^3 to 2^4 for that key and at most 2^15 for any, O in
+//     units of 1 / f. In fp16 P' keeps 11 bits down to 2^-17 of the largest weight and is a multiple of 2^-27 of it
+//     below: off by 2^-28 of the largest entry that another row adds, where that row's own rounding in the cache is
+//     up to 2^-19 of it (half of e4m3's smallest step against 448). (With one unit a warp, set by the largest exponent
+//     whatever its probability, a value row of 2^34 times the others hid them all, at any weight. With a second
+//     exponential a score, of its weight, four tokens below take 160 us, and eight 296 us and not 272 us.)
 //   * ldmatrix hands out byte pairs: in Q K^T the dims of a 16-dim chunk take the order that the bytes
 //     come in (any order does), in V^T P^T the even dims of a chunk are rows 0-7 of the product and the
 //     odd ones rows 8-15.
-// A bf16 cache takes P as bf16 (range of V); so do the drafted tokens.
+// A bf16 cache takes P as bf16 (range of V); so do the drafted tokens, whose largest magnitude stands for the exponent.
 //
 // Measured (64 caches of 8 heads of 128, 64 selected blocks of 64 keys and 63 keys of tail, four query heads each):
-// one token over e4m3 0.55 GB in 98 us with the join, 5.6 TB/s (85 % of the copy rate). Four tokens (16 rows)
-// 139 us, bound by issue. Over bf16 1.09 GB: one token 179 us, 6.1 TB/s (93 %), four tokens 186 us.
+// one token over e4m3 0.55 GB in 99 us with the join, 5.5 TB/s (84 % of the copy rate). Four tokens (16 rows)
+// 147 us, bound by issue. Over bf16 1.09 GB: one token 179 us, 6.1 TB/s (93 %), four tokens 186 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,6 +42,11 @@
 namespace pisa {
 
 constexpr float kFewLazy = 8.0f;    // log2 units a score may exceed the kept maximum by
+constexpr float kFewTop = 15.0f;    // log2 of the largest P': fp16 ends below 2^16
+constexpr float kFewUnit = 4.0f;    // log2 of P' of the largest weight when f is set, rounded down: weights may rise by 2^11,
+                                    // exponents by 3 above that key's, before it is looked at again
+constexpr float kFewMaxF = 100.0f;  // largest log2 f: P' of a drafted token is a finite bf16
+constexpr float kFewDraftMin = -90.0f;  // smallest exponent of a drafted row
 constexpr int kFewStages = 8;       // most stages of the ring
 constexpr int kFewThreads = 160;    // four consumer warps and the producer
 
@@ -110,50 +119,71 @@ struct FewCfg {
 };
 
 // One warp's state: for its rows 2 (lane % 4), + 1 of every row tile of 8 the reference that its
-// probabilities are taken against (a maximum so far, log2 units; kTreeNone while there is none) and the sum over
-// its keys; O^T: tile j is dims 16 j + lane / 4 (+ 8) (e4m3: 16 j + 2 (lane / 4), + 1); the unit exponent of
-// O and the V exponent that it was set by.
-template <int D, int NT>
+// probabilities are taken against (a maximum so far, log2 units; kTreeNone while there is none; whole for e4m3, so that
+// rescaling is exact) and the sum over its keys; O^T: tile j is dims 16 j + lane / 4 (+ 8) (e4m3: 16 j + 2 (lane / 4),
+// + 1); e4m3: f, and the largest exponent byte with which no P' of a score below ref + kFewLazy passes its largest.
+template <int D, bool E4M3, int NT>
 struct FewState {
     float o[NT][D / 16][4];
     float ref[NT][2], l[NT][2];
-    int u, uexp;
+    float f[E4M3 ? NT : 1][2];
+    int emax;
     bool fresh;   // no key yet
 };
 
+__device__ __forceinline__ float few_rows_max(float x) {  // over the keys of a row
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+    return x;
+}
+__device__ __forceinline__ float few_log2(float f) {  // of a power of two
+    return static_cast<float>(static_cast<int>(__float_as_uint(f) >> 23) - 127);
+}
+
 // Scores of 16 keys (log2 units, -inf where masked; [0], [1]: this thread's first key, [2], [3]: its
-// second), ev: the larger V exponent of the two -> probabilities. A row's reference moves, and its O and sum
-// with it, when one of its scores exceeds it by kFewLazy; the unit when an exponent exceeds the one it was set by.
-template <int D, int NT>
-__device__ __forceinline__ void few_softmax(FewState<D, NT>& s, float (&x)[NT][4], int ev) {
-    bool over = s.fresh || ev > s.uexp;
+// second) -> what multiplies the keys' values: probabilities, or (e4m3) P', with e0 and e1 the exponent bytes of the
+// two keys' values (255: the row stands for NaN). Drafted tokens (DRAFT): w0 and w1 are their exponents, which their
+// values hold themselves. A row's reference or f moves, and its sum or O with it, when one of its own scores or weights
+// asks for it: what another row attends changes no bit of this one.
+template <int D, bool E4M3, int NT, bool DRAFT>
+__device__ __forceinline__ void few_softmax(FewState<D, E4M3, NT>& s, float (&x)[NT][4], int e0, int e1, float w0, float w1) {
+    bool over = s.fresh || (E4M3 && (DRAFT || max(e0, e1) > s.emax));
 #pragma unroll
     for (int t = 0; t < NT; ++t)
         over = over || fmaxf(x[t][0], x[t][2]) > s.ref[t][0] + kFewLazy || fmaxf(x[t][1], x[t][3]) > s.ref[t][1] + kFewLazy;
     if (__any_sync(0xFFFFFFFFu, over)) {
-        float g = 1.f;
-        const int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(ev)));
-        if (e > s.uexp) {
-            s.uexp = e;
-            const int u = max(kTreeUMin, min(e, 254) - 127 - 7);
-            g = s.fresh ? 1.f : pow2i(max(-126, s.u - u));
-            s.u = u;
+        if constexpr (E4M3 && !DRAFT) {
+            w0 = e0 == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>(e0 - 127);
+            w1 = e1 == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>(e1 - 127);
         }
+        float least = INFINITY;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float a[2];
 #pragma unroll
-            for (int e2 = 0; e2 < 2; ++e2) {
-                float top = fmaxf(x[t][e2], x[t][2 + e2]);
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const float old = s.ref[t][e2];
-                // only a row that exceeds its own reference moves it: what another row attends changes no bit of this one
-                const float now = s.fresh ? fmaxf(kTreeNone, top) : top > old + kFewLazy ? top : old;
-                a[e2] = s.fresh || now == old ? 1.f : fast_exp2(old - now);
-                s.ref[t][e2] = now;
-                s.l[t][e2] *= a[e2];
-                a[e2] *= g;
+            for (int e = 0; e < 2; ++e) {
+                const float top = few_rows_max(fmaxf(x[t][e], x[t][2 + e]));
+                const float old = s.ref[t][e];
+                float now;
+                if constexpr (E4M3) {
+                    const float wtop = few_rows_max(fmaxf(x[t][e] + w0, x[t][2 + e] + w1));
+                    const float lf = few_log2(s.f[t][e]);
+                    const bool none = old == kTreeNone;
+                    const bool move = none || top > old + kFewLazy || wtop - old + lf > kFewTop;
+                    now = move ? fmaxf(old, ceilf(top)) : old;
+                    // the unit of O stays, unless a weight is larger than the one that set it
+                    const float stay = none ? kFewMaxF : fminf(kFewMaxF, lf + (now - old));
+                    const float lfn = move ? fmaxf(-126.f, fminf(stay, floorf(kFewUnit - (wtop - now)))) : lf;
+                    a[e] = none ? 1.f : fast_exp2((old - now) + (lfn - lf));
+                    s.l[t][e] *= none ? 1.f : fast_exp2(old - now);
+                    s.f[t][e] = __uint_as_float(static_cast<uint32_t>(static_cast<int>(lfn) + 127) << 23);
+                    least = fminf(least, kFewTop - kFewLazy - lfn);
+                } else {
+                    now = s.fresh ? fmaxf(kTreeNone, top) : top > old + kFewLazy ? top : old;
+                    a[e] = s.fresh || now == old ? 1.f : fast_exp2(old - now);
+                    s.l[t][e] *= a[e];
+                }
+                s.ref[t][e] = now;
             }
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
@@ -164,15 +194,29 @@ __device__ __forceinline__ void few_softmax(FewState<D, NT>& s, float (&x)[NT][4
             }
         }
         s.fresh = false;
+        if constexpr (E4M3) {
+            least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, 1));
+            least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, 2));
+            s.emax = 127 + static_cast<int>(least);
+        }
     }
+    const float g0 = __uint_as_float(static_cast<uint32_t>(e0) << 23), g1 = __uint_as_float(static_cast<uint32_t>(e1) << 23);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        x[t][0] = fast_exp2(x[t][0] - s.ref[t][0]);
-        x[t][1] = fast_exp2(x[t][1] - s.ref[t][1]);
-        x[t][2] = fast_exp2(x[t][2] - s.ref[t][0]);
-        x[t][3] = fast_exp2(x[t][3] - s.ref[t][1]);
-        s.l[t][0] += x[t][0] + x[t][2];
-        s.l[t][1] += x[t][1] + x[t][3];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            x[t][e] = fast_exp2(x[t][e] - s.ref[t][e]);
+            x[t][2 + e] = fast_exp2(x[t][2 + e] - s.ref[t][e]);
+            s.l[t][e] += x[t][e] + x[t][2 + e];
+            if constexpr (E4M3) {  // (p f first: f 2^(e - 127) may be no fp32)
+                x[t][e] *= s.f[t][e];
+                x[t][2 + e] *= s.f[t][e];
+                if constexpr (!DRAFT) {
+                    x[t][e] *= g0;
+                    x[t][2 + e] *= g1;
+                }
+            }
+        }
     }
 }
 
@@ -354,16 +398,16 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
         const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
         const int64_t out0 = (static_cast<int64_t>(b) * p.Hq + hs * p.gh) * p.T + base;  // first output row
 
-        FewState<D, NT> st;
+        FewState<D, E4M3, NT> st;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) st.o[t][j][0] = st.o[t][j][1] = st.o[t][j][2] = st.o[t][j][3] = 0.f;
             st.ref[t][0] = st.ref[t][1] = kTreeNone;
             st.l[t][0] = st.l[t][1] = 0.f;
+            if constexpr (E4M3) st.f[t][0] = st.f[t][1] = 1.f;
         }
-        st.u = 0;
-        st.uexp = 0;
+        st.emax = 0;
         st.fresh = true;
 
         // Q as the B operand: row 8 t + r; bf16: dims 16 k + 2 q4 (+ 8); e4m3: dims 16 k + 4 q4 .. + 3 as
@@ -424,7 +468,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
             if (key0 < lim) {
                 if (key0 + 16 > lim) {
                     // rows past the sequence hold whatever the cache held: V's must not reach the product
-                    // as NaN (0 * NaN), exponents must not set the unit
+                    // as NaN (0 * NaN), nor V's exponents
                     for (int e = lane; e < 16 * (C::ROW / 16); e += 32) {
                         const int key = key0 + e / (C::ROW / 16), c = e % (C::ROW / 16);
                         if (key >= lim) {
@@ -483,17 +527,13 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                         if (key0 + r + 8 >= lim) x[t][2] = x[t][3] = -INFINITY;
                     }
                 }
-                const int e0 = E4M3 ? es[64 + key0 + r] : 0, e1 = E4M3 ? es[64 + key0 + r + 8] : 0;
-                few_softmax<D, NT>(st, x, max(e0, e1));
+                few_softmax<D, E4M3, NT, false>(st, x, E4M3 ? es[64 + key0 + r] : 0, E4M3 ? es[64 + key0 + r + 8] : 0, 0.f, 0.f);
                 uint32_t pb[NT][2];  // P^T: keys 2 q4, + 1 (+ 8) of row 8 t + r
                 if constexpr (E4M3) {
-                    // a row of exponent 255 stands for NaN for every token (its bytes are zero, 0 * inf)
-                    const float g0 = __uint_as_float(static_cast<uint32_t>(e0 == 255 ? 255 : max(e0 - st.u, 0)) << 23);
-                    const float g1 = __uint_as_float(static_cast<uint32_t>(e1 == 255 ? 255 : max(e1 - st.u, 0)) << 23);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        pb[t][0] = few_transpose(pack_f16x2(x[t][0] * g0, x[t][1] * g0));
-                        pb[t][1] = few_transpose(pack_f16x2(x[t][2] * g1, x[t][3] * g1));
+                        pb[t][0] = few_transpose(pack_f16x2(x[t][0], x[t][1]));
+                        pb[t][1] = few_transpose(pack_f16x2(x[t][2], x[t][3]));
                     }
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
@@ -577,13 +617,33 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                             x[t][2 + e] = (mk[t][e] >> (r + 8)) & 1u ? x[t][2 + e] * p.scale_log2 : -INFINITY;
                         }
                     }
-                    few_softmax<D, NT>(st, x, 0);
-                    const float g = E4M3 ? pow2i(min(127, max(-126, -st.u))) : 1.f;
+                    float ed0 = 0.f, ed1 = 0.f;  // of this thread's keys, the exponents that their values would have in the cache
+                    if constexpr (E4M3) {
+                        uint32_t top = 0;  // largest finite magnitude of key lane % 16, half of the dims a lane
+                        if ((lane & 15) < p.T) {
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                const int c = (lane >> 4) * (D / 16) + i;
+                                const uint4 v = *reinterpret_cast<const uint4*>(dk_s + C::DRAFT + (c / 8) * 2048 + few_at128(lane & 15, c % 8));
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+                                    top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                                }
+                            }
+                        }
+                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                        const float e = fmaxf(kFewDraftMin, static_cast<float>(static_cast<int>(top >> 7) - 127 - 8));
+                        ed0 = __shfl_sync(0xFFFFFFFFu, e, r);
+                        ed1 = __shfl_sync(0xFFFFFFFFu, e, r + 8);
+                    }
+                    few_softmax<D, E4M3, NT, true>(st, x, 0, 0, ed0, ed1);
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        pb[t][0] = few_transpose(pack_bf16x2(x[t][0] * g, x[t][1] * g));
-                        pb[t][1] = few_transpose(pack_bf16x2(x[t][2] * g, x[t][3] * g));
+                        pb[t][0] = few_transpose(pack_bf16x2(x[t][0], x[t][1]));
+                        pb[t][1] = few_transpose(pack_bf16x2(x[t][2], x[t][3]));
                     }
                     // V value by value, in the order of O's tiles: rows past the tokens are left out, and so is a
                     // value that is not finite, which would reach every token through 0 * x
@@ -635,8 +695,7 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
         }
 
         // ---- the piece's end: the four warps meet in shared memory, CH dims at a time
-        float uf = 1.f;
-        if constexpr (E4M3) uf = pow2i(min(127, max(-126, st.u)));
+        float uf[NT][2];  // O's unit
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -649,6 +708,8 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                     cml[2 * row] = l == 0.f ? -INFINITY : st.ref[t][e];
                     cml[2 * row + 1] = l;
                 }
+                if constexpr (E4M3) uf[t][e] = __uint_as_float((254u << 23) - __float_as_uint(st.f[t][e]));  // 1 / f
+                else uf[t][e] = 1.f;
             }
         }
         const bool whole = unit == 0 && u1 == units;
@@ -665,8 +726,8 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float* at = comb + (warp * C::RM + 8 * t + 2 * q4 + e) * C::CH;
-                        at[d0] = st.o[t][j][e] * uf;
-                        at[d1] = st.o[t][j][2 + e] * uf;
+                        at[d0] = st.o[t][j][e] * uf[t][e];
+                        at[d1] = st.o[t][j][2 + e] * uf[t][e];
                     }
                 }
             }

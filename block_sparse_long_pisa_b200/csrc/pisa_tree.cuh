@@ -9,7 +9,6 @@
 namespace pisa {
 
 constexpr uint32_t kTreeDetail = kKernTree << 8;
-constexpr int kTreeUMin = -100;  // smallest unit exponent of O (e4m3)
 // The reference of a row without a finite score so far: below every score, so that the first one moves it, and finite, so
 // that a score of minus infinity stays one. (A reference of 0 would round scores below -126 away that come later.)
 constexpr float kTreeNone = -3.402823466e+38f;
@@ -81,9 +80,6 @@ __device__ __forceinline__ void tree_find(const TreeParams& p, int64_t x, int64_
     unit = 0;
 }
 
-__device__ __forceinline__ float pow2i(int e) {  // e in [-126, 127]
-    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

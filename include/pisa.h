@@ -410,6 +410,9 @@ PISA_API pisa_status pisa_tree_workspace_size(const pisa_tree_shape *shape, size
  *               topk = 0. Entries < 0 are skipped; an entry >= seq_kv / block is skipped and recorded as
  *               PISA_ERR_BAD_INDEX; a repeated entry is attended twice.
  *   O         : bf16 [B, heads_q, T, D].  lse : optional fp32 [B, heads_q, T] (natural log).
+ *   Each key's probability is rounded to 8 bits (bf16). For up to 16 rows (heads of a selection row x T), or 32 with
+ *   T <= 16, over a PISA_CACHE_E4M3 cache a cached key's probability times 2^(e - 127) of its value row is rounded to
+ *   11 bits, or to a multiple of 2^-27 of the largest such product of its token and head where that is coarser.
  *   A token that attends nothing gets O = 0 and LSE = -inf. Keys and values of drafted tokens that a
  *   token does not attend do not touch its result, whatever they hold.
  *   ws        : >= pisa_tree_workspace_size bytes. Calls that share one must not overlap on the GPU:

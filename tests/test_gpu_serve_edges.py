@@ -1,10 +1,10 @@
 """The operators around the attention in calls that an earlier form of them answered wrongly. Tolerances are those of
-test_gpu_serve.py."""
+test_gpu_serve.py, and for few rows over an e4m3 cache one term more, derived at `floor_of`."""
 import numpy as np
 import pytest
 
 from oracle import serve_oracle as so
-from tests.test_gpu_serve import bf16, f32, fill, host, i32, raw, tmask, tree_bits, tree_inputs
+from tests.test_gpu_serve import bf16, check_tree, f32, fill, host, i32, raw, tmask, tree_bits, tree_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -85,6 +85,98 @@ def test_outputs_made_on_another_stream(pisa):
 
 # T, Hq, D: 4, 16 and two tiles of 16 rows (few), one and two tiles of 128 (many)
 FORMS = [(1, 4, 128), (1, 4, 64), (4, 4, 128), (7, 2, 64), (7, 4, 128), (24, 4, 128), (40, 4, 64)]
+
+
+# ----------------------------------------------------------------------------- value rows of unlike size
+
+def floor_of(s, q, k, dk, v_exp, dv, mask, lens, idx):
+    """What few rows over an e4m3 cache may be off by beside check_tree's terms. A weight (probability times its row's
+    scale) times a power of two f is held in fp16, f such that the largest weight comes to 2^3 or more, and to less than
+    2^16: its step is never above 2^-24 for weights below 2^-14, so rounding is off by at most 2^-25, 2^-28 of the largest
+    weight; a value is at most 448 (a drafted one, whose scale is its largest magnitude over 256, at most 2^9) scales. So
+    n keys: n 2^-28 2^9 max_j p_j 2^(e_j - 127) / sum p."""
+    B, Hq, T, D = q.shape
+    g = Hq // k.shape[1]
+    out = np.zeros((B, Hq, T))
+    for b in range(B):
+        for h in range(Hq):
+            kv = h // g
+            at = so.seen_positions(lens[b], s.capacity, s.seq_kv, s.topk, s.block,
+                                   idx[b, h if s.select_per_qhead else kv, 0] if s.topk else None)
+            for t in range(T):
+                js = [j for j in range(T) if (int(mask[b, t]) >> j) & 1]
+                x = np.concatenate([k[b, kv][at], dk[b, kv][js]]) @ q[b, h, t] / np.sqrt(D)
+                if len(x) == 0:
+                    continue
+                scale = np.concatenate([2.0 ** (v_exp[b, kv][at].astype(float) - 127), np.abs(dv[b, kv][js]).max(-1, initial=0) / 256])
+                p = np.exp(x - x.max())
+                out[b, h, t] = len(x) * 2.0 ** -19 * (p * scale).max() / p.sum()
+    return out
+
+
+def check_with_floor(s, O, lse, cache, k, v, q, dk, dv, mask, lens, idx):
+    ref, L, A, S = so.tree_attention(host(q), host(dk), host(dv), mask, k, v, lens, idx, block=s.block, seq_kv=s.seq_kv,
+                                     topk=s.topk, per_qhead=bool(s.select_per_qhead), scale=s.scale)
+    e = 2.0 ** -18 * S
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e[..., None]) * A
+    tol += floor_of(s, host(q), k, host(dk), cache.v_exp.cpu().numpy(), host(dv), mask, lens, idx)[..., None]
+    err = np.abs(host(O) - ref)
+    assert (err <= tol).all(), (np.nanmax(err - tol), np.argwhere(~(err <= tol))[:5])
+    assert (np.abs(host(lse) - L) <= e + 2.0 ** -20 * np.abs(L) + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("T, Hq, D", FORMS)
+@pytest.mark.parametrize("top, mixed", [(20, 0), (28, 0), (34, 0), (60, 0), (100, 0), (34, 1), (60, 1)])
+def test_a_large_value_row_of_vanishing_weight_hides_no_other(pisa, T, Hq, D, top, mixed):
+    """Three cached value rows are 2^top times the others and their keys 2^-(top + 26) times as likely: they add nothing, and
+    the others keep their precision. Mixed: every second head and token turns to those keys instead."""
+    rng = np.random.default_rng(top)
+    import torch
+    n, cap = 150, 192
+    K, V = bf16(rng, 1, 1, n, D, scale=0.25), bf16(rng, 1, 1, n, D)
+    q = bf16(rng, 1, Hq, T, D, scale=0.25)
+    q[..., 0] = 8.0
+    if mixed:
+        q[:, 1::2, :, 0] *= -1
+        q[:, :, 1::2, 0] *= -1
+    K[..., 0] = 0
+    for at in (3, 70, 149):
+        K[0, 0, at, 0] = -float(np.log(2) * (top + 26) * np.sqrt(D) / 8)
+        V[0, 0, at] = V[0, 0, at] * 2.0 ** top
+    dk, dv = bf16(rng, 1, 1, T, D, scale=0.25), bf16(rng, 1, 1, T, D)
+    cache = pisa.new_cache(pisa.CacheShape(1, 1, cap, D), "cuda")
+    pisa.cache_write(cache, K, V, pisa.new_cache_workspace("cuda"))
+    kb, vb, ke, ve = raw(cache)
+    s = pisa.TreeShape(1, Hq, 1, T, cap, D)
+    mask, lens, ws = tree_bits(rng, 1, T, "tree"), np.array([n]), pisa.new_tree_workspace(s, "cuda")
+    O, lse = pisa.tree_attention(s, cache, q, dk, dv, tmask(mask), i32(lens), ws)
+    assert pisa.check_status(ws) == (pisa.OK, 0)
+    check_with_floor(s, O, lse, cache, so.row_values(kb, ke), so.row_values(vb, ve), q, dk, dv, mask, lens, None)
+    assert bool(torch.isfinite(O).all())
+
+
+@pytest.mark.parametrize("T, Hq, D", FORMS)
+@pytest.mark.parametrize("spread, qscale", [(30, 30.0), (30, 4.0), (12, 8.0), (60, 10.0)])
+def test_value_rows_of_unlike_size_under_peaked_scores(pisa, T, Hq, D, spread, qscale):
+    case = (3, 2 * Hq, 2, T, 704, D, 1, 64, 576, 5, 0, [700, 300, 0], "tree")
+    s, cache, k, v, q, dk, dv, mask, lens, idx = tree_inputs(pisa, case, 52, spread, qscale)
+    ws = pisa.new_tree_workspace(s, "cuda")
+    O, lse = pisa.tree_attention(s, cache, q, dk, dv, tmask(mask), i32(lens), ws, idx=i32(idx))
+    check_with_floor(s, O, lse, cache, k, v, q, dk, dv, mask, lens, idx)
+
+
+@pytest.mark.parametrize("T, Hq, D", FORMS)
+@pytest.mark.parametrize("big", [0, 25, 90])
+def test_drafted_values_over_a_cache_of_zero_rows(pisa, T, Hq, D, big):
+    """Zero rows have the smallest exponent; drafted values of 2^big beside them come out as they are."""
+    rng = np.random.default_rng(7)
+    cache = pisa.new_cache(pisa.CacheShape(1, 1, 128, D), "cuda")
+    s = pisa.TreeShape(1, Hq, 1, T, 128, D)
+    q, dk, dv = bf16(rng, 1, Hq, T, D), bf16(rng, 1, 1, T, D), bf16(rng, 1, 1, T, D) * 2.0 ** big
+    mask, lens, ws = tree_bits(rng, 1, T, "tree"), np.array([100]), pisa.new_tree_workspace(s, "cuda")
+    O, lse = pisa.tree_attention(s, cache, q, dk, dv, tmask(mask), i32(lens), ws)
+    zero = np.zeros((1, 1, 128, D))
+    check_tree(s, O, lse, zero, zero, q, dk, dv, mask, lens, None)
 
 
 # ----------------------------------------------------------------------------- scores of minus infinity
