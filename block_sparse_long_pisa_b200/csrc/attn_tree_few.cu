@@ -274,68 +274,8 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
             prefetch_tmap(&tmDK);
             prefetch_tmap(&tmDV);
         }
-        while (pos < end && ok) {
-            const int b = static_cast<int>(tile / p.rows_per_seq);
-            const int hs = static_cast<int>(tile % p.rows_per_seq) / p.mt;
-            const int kvh = p.per_qhead ? hs / p.g : hs;
-            const int64_t plane = static_cast<int64_t>(b) * p.Hkv + kvh;
-            const int len = tree_len(p, b);
-            const int units = tree_units(p, len);
-            const int u1 = static_cast<int>(min(static_cast<int64_t>(units), unit + (end - pos)));
-            if (tile % p.rows_per_seq == 0 && unit == 0 && lane == 0 && p.len[b] != len)
-                record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB0u);
-            const int32_t* row = p.topk > 0 ? p.idx + (static_cast<int64_t>(b) * p.Hsel + hs) * p.topk : nullptr;
-            const int nsel = p.topk * p.upb;
-            const int uc = min(u1, units - 1);  // the last unit is the drafted tokens
-            for (int u = unit; u < uc && ok; u += 32) {
-                // up to 32 units at a time: position of each unit's first key, -1 = nothing there
-                int at = -1;
-                if (u + lane < uc) {
-                    const int c = u + lane;
-                    if (p.topk == 0) {
-                        at = 64 * c;
-                    } else if (c >= nsel) {
-                        at = p.seq + 64 * (c - nsel);
-                    } else {
-                        const int j = __ldg(row + c / p.upb);
-                        if (j >= p.n0)
-                            record_error(p.status, PISA_ERR_BAD_INDEX, kTreeDetail | 0xB1u);
-                        else if (j >= 0)
-                            at = (j * p.upb + c % p.upb) * 64;
-                    }
-                }
-                for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < len); left != 0 && ok; left &= left - 1) {
-                    const int a = __shfl_sync(0xFFFFFFFFu, at, __ffs(left) - 1);
-                    if (elect_one()) {
-                        ok = used < p.nk || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x11u);
-                        if (ok) {
-                            meta[s] = min(64, len - a);
-                            uint8_t* kt = ring + s * C::STAGE;
-                            const int64_t krow = plane * p.cap + a;
-                            const int y = static_cast<int>(krow);
-                            mbar_arrive_expect_tx(&full[s], C::STAGE + C::EXPS);
-                            if constexpr (E4M3) {
-                                tma_load_2d(kt, &tmK, 0, y, &full[s]);
-                                tma_load_2d(kt + C::TILE, &tmV, 0, y, &full[s]);
-                                bulk_load(exps + s * 128, p.k_exp + krow, 64, &full[s]);
-                                bulk_load(exps + s * 128 + 64, p.v_exp + krow, 64, &full[s]);
-                            } else {
-#pragma unroll
-                                for (int c = 0; c < D / 64; ++c) {
-                                    tma_load_2d(kt + c * 8192, &tmK, 64 * c, y, &full[s]);
-                                    tma_load_2d(kt + C::TILE + c * 8192, &tmV, 64 * c, y, &full[s]);
-                                }
-                            }
-                        }
-                    }
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (ok) {
-                        ++used;
-                        advance();
-                    }
-                }
-            }
-            if (u1 == units && ok) {  // the drafted tokens, in a buffer of their own
+        auto issue = [&](int kind, int64_t plane, int len, int a, int) {
+            if (kind == kTileDraft) {  // the drafted tokens, in a buffer of their own
                 if (elect_one()) {
                     ok = drafts == 0 || mbar_wait(&dempty, dpar ^ 1u, p.status, kTreeDetail | 0x12u);
                     if (ok) {
@@ -353,25 +293,40 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                     ++drafts;
                     dpar ^= 1u;
                 }
+                return;
             }
-            if (ok) {  // end of the piece: a slot without a tile
-                if (elect_one()) {
-                    ok = used < p.nk || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x13u);
-                    if (ok) {
-                        meta[s] = 0;
-                        mbar_arrive(&full[s]);
+            if (elect_one()) {
+                ok = used < p.nk || mbar_wait(&empty[s], par ^ 1u, p.status, kTreeDetail | 0x11u);
+                if (ok && kind == kTileEnd) {  // a slot without a tile
+                    meta[s] = 0;
+                    mbar_arrive(&full[s]);
+                } else if (ok) {
+                    meta[s] = min(64, len - a);
+                    uint8_t* kt = ring + s * C::STAGE;
+                    const int64_t krow = plane * p.cap + a;
+                    const int y = static_cast<int>(krow);
+                    mbar_arrive_expect_tx(&full[s], C::STAGE + C::EXPS);
+                    if constexpr (E4M3) {
+                        tma_load_2d(kt, &tmK, 0, y, &full[s]);
+                        tma_load_2d(kt + C::TILE, &tmV, 0, y, &full[s]);
+                        bulk_load(exps + s * 128, p.k_exp + krow, 64, &full[s]);
+                        bulk_load(exps + s * 128 + 64, p.v_exp + krow, 64, &full[s]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            tma_load_2d(kt + c * 8192, &tmK, 64 * c, y, &full[s]);
+                            tma_load_2d(kt + C::TILE + c * 8192, &tmV, 64 * c, y, &full[s]);
+                        }
                     }
                 }
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (ok) {
-                    ++used;
-                    advance();
-                }
             }
-            pos += u1 - unit;
-            unit = 0;
-            ++tile;
-        }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok) {
+                ++used;
+                advance();
+            }
+        };
+        tree_entries<false>(p, pos, end, tile, unit, true, ok, issue);
         // every copy lands before the block ends, also when a consumer gave up (earlier uses of a stage
         // were complete before it was filled again)
         if (lane == 0) {

@@ -123,7 +123,7 @@ __device__ __forceinline__ void many_producer(const TreeParams& p, const CUtenso
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
     };
-    tree_entries(p, pos, end, tile, unit, true, ok, issue);
+    tree_entries<true>(p, pos, end, tile, unit, true, ok, issue);
     // every copy lands before the block ends, also when another role gave up (earlier uses of a slot were
     // complete before it was filled again)
     if (lane == 0) {
@@ -185,7 +185,7 @@ __device__ __forceinline__ void many_fetch(const TreeParams& p, const CUtensorMa
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
     };
-    tree_entries(p, pos, end, tile, unit, !is_v, ok, issue);
+    tree_entries<true>(p, pos, end, tile, unit, !is_v, ok, issue);
     if (lane == 0) {
 #pragma unroll 1
         for (int i = 0; i < NC; ++i) step(kStepStop, 0, 0, 0, false);

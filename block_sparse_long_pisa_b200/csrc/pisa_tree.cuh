@@ -144,10 +144,10 @@ struct RingAt {
     }
 };
 
-// The entries of a CTA's pieces in order: issue(kind, plane, len, a0, a1) for every tile of 128 keys (two
-// units, first keys a0 and a1, a1 = -1 for none), for the drafted tokens, and for the end of each piece.
-// Run by a whole warp; `reports`: this warp records bad lengths and indices. Stops when ok is cleared.
-template <class Issue>
+// The entries of a CTA's pieces in order: issue(kind, plane, len, a0, a1) for every tile (PAIRS: of 128 keys, two
+// units, first keys a0 and a1, a1 = -1 for none; else of one unit, a1 = -1), for the drafted tokens, and for the end of
+// each piece. Run by a whole warp; `reports`: this warp records bad lengths and indices. Stops when ok is cleared.
+template <bool PAIRS, class Issue>
 __device__ __forceinline__ void tree_entries(const TreeParams& p, int64_t pos, int64_t end, int64_t tile, int unit,
                                              bool reports, bool& ok, Issue issue) {
     const int lane = threadIdx.x & 31;
@@ -184,7 +184,9 @@ __device__ __forceinline__ void tree_entries(const TreeParams& p, int64_t pos, i
             }
             for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < len); left != 0 && ok; left &= left - 1) {
                 const int a = __shfl_sync(0xFFFFFFFFu, at, __ffs(left) - 1);
-                if (first < 0) {
+                if (!PAIRS) {
+                    issue(kTileCache, plane, len, a, -1);
+                } else if (first < 0) {
                     first = a;
                 } else {
                     issue(kTileCache, plane, len, first, a);
@@ -192,7 +194,7 @@ __device__ __forceinline__ void tree_entries(const TreeParams& p, int64_t pos, i
                 }
             }
         }
-        if (first >= 0 && ok) issue(kTileCache, plane, len, first, -1);
+        if (PAIRS && first >= 0 && ok) issue(kTileCache, plane, len, first, -1);
         if (u1 == units && ok) issue(kTileDraft, plane, len, 0, 0);
         if (ok) issue(kTileEnd, plane, len, 0, 0);
         pos += u1 - unit;
