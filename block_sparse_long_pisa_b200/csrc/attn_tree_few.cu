@@ -83,17 +83,6 @@ __device__ __forceinline__ void few_mma(float (&d)[4], uint32_t a0, uint32_t a1,
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// two e4m3 values (of the low, the high half of a register) -> two fp16
-__device__ __forceinline__ uint32_t few_f16(uint32_t two) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(two));
-    return h;
-}
-__device__ __forceinline__ uint32_t few_f16_hi(uint32_t two) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(h) : "r"(two));
-    return h;
-}
 // byte offset of 16-byte chunk `c` of row `row` in a tile of 128-byte (64-byte) swizzled rows
 __device__ __forceinline__ uint32_t few_at128(int row, int c) {
     return static_cast<uint32_t>(row * 128 + ((c ^ (row & 7)) << 4));
@@ -444,8 +433,8 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                         few_ldsm4(kb + few_at_e4m3<D>(key0 + mr + 8 * (mi & 1), 2 * c + (mi >> 1)), a);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t a0 = few_f16(a[2 * h]), a2 = few_f16_hi(a[2 * h]);
-                            const uint32_t a1 = few_f16(a[2 * h + 1]), a3 = few_f16_hi(a[2 * h + 1]);
+                            const uint32_t a0 = e4m3x2_f16x2<false>(a[2 * h]), a2 = e4m3x2_f16x2<true>(a[2 * h]);
+                            const uint32_t a1 = e4m3x2_f16x2<false>(a[2 * h + 1]), a3 = e4m3x2_f16x2<true>(a[2 * h + 1]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
                                 few_mma<true>(x[t], a0, a1, a2, a3, qf[t][2 * c + h][0], qf[t][2 * c + h][1]);
@@ -498,8 +487,8 @@ __global__ void __launch_bounds__(kFewThreads, (FewCfg<D, E4M3, NT>::CTAS))
                         for (int i = 0; i < 4; ++i) a[i] = __byte_perm(a[i], 0u, 0x3120);  // (even, even, odd, odd)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t a0 = few_f16(a[2 * h]), a1 = few_f16_hi(a[2 * h]);
-                            const uint32_t a2 = few_f16(a[2 * h + 1]), a3 = few_f16_hi(a[2 * h + 1]);
+                            const uint32_t a0 = e4m3x2_f16x2<false>(a[2 * h]), a1 = e4m3x2_f16x2<true>(a[2 * h]);
+                            const uint32_t a2 = e4m3x2_f16x2<false>(a[2 * h + 1]), a3 = e4m3x2_f16x2<true>(a[2 * h + 1]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) few_mma<true>(st.o[t][2 * c + h], a0, a1, a2, a3, pb[t][0], pb[t][1]);
                         }

@@ -36,12 +36,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // The two e4m3 values of a word's low (HI: high) half.
 template <bool HI>
 __device__ __forceinline__ float2 e4m3x2_values(uint32_t word) {
-    uint32_t h;
-    if constexpr (HI)
-        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(h) : "r"(word));
-    else
-        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(word));
-    return __half22float2(*reinterpret_cast<__half2*>(&h));
+    const uint32_t h = e4m3x2_f16x2<HI>(word);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // 2^(e - 127) of an exponent byte 1 .. 254; 255 gives an infinity, which times a zero byte is the

@@ -51,11 +51,6 @@ __device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint64_t nr_mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint64_t nr_fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -235,7 +230,7 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRope
                 uint64_t x[4], m[4];
                 unpack8(v[u], x);
                 mate_values<INTER>(v[u], x, lm.mate, m);
-                uint64_t s2 = nr_mul2(x[0], x[0]);
+                uint64_t s2 = f2_mul(x[0], x[0]);
 #pragma unroll
                 for (int k = 1; k < 4; ++k) s2 = nr_fma2(x[k], x[k], s2);
                 float s0, s1;
@@ -243,7 +238,7 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRope
                 const float r = rsqrtf(row_sum<D>(s0 + s1) * (1.f / D) + p.eps);
                 const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = nr_mul2(nr_fma2(m[k], c[k], nr_mul2(x[k], a[k])), r2);
+                for (int k = 0; k < 4; ++k) x[k] = f2_mul(nr_fma2(m[k], c[k], f2_mul(x[k], a[k])), r2);
                 if (ok) *reinterpret_cast<uint4*>(dst) = pack8(x);
                 dst += dstep;
                 if (i + u + U < n) v[u] = load_row(src);
@@ -319,8 +314,8 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_backward_kernel(const
                 for (int k = 0; k < 4; ++k) {
                     // du: the turn taken back; then dn = du w
                     g[k] = nr_fma2(m[k], f2_pack(-tn.s[2 * k], -tn.s[2 * k + 1]),
-                                   nr_mul2(g[k], f2_pack(tn.c[2 * k], tn.c[2 * k + 1])));
-                    m[k] = nr_mul2(g[k], wl[k]);
+                                   f2_mul(g[k], f2_pack(tn.c[2 * k], tn.c[2 * k + 1])));
+                    m[k] = f2_mul(g[k], wl[k]);
                     s2 = nr_fma2(x[k], x[k], s2);
                     d2 = nr_fma2(m[k], x[k], d2);
                 }
@@ -334,8 +329,8 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_backward_kernel(const
                 const uint64_t r2 = f2_pack(r, r), f2 = f2_pack(f, f);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    m[k] = nr_mul2(nr_fma2(x[k], f2, m[k]), r2);
-                    g2[k] = nr_fma2(g[k], nr_mul2(x[k], r2), g2[k]);
+                    m[k] = f2_mul(nr_fma2(x[k], f2, m[k]), r2);
+                    g2[k] = nr_fma2(g[k], f2_mul(x[k], r2), g2[k]);
                 }
                 if (ok) *reinterpret_cast<uint4*>(dst) = pack8(m);
                 dst += dstep;

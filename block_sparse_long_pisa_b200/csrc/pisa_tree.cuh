@@ -97,9 +97,8 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     return r;
 }
 __device__ __forceinline__ float2 e4m3x2_f32(uint32_t two) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-    return __half22float2(*reinterpret_cast<__half2*>(&h));
+    const uint32_t h = e4m3x2_f16x2<false>(two);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 // One lane of the whole warp, in a form that the compiler knows to be one lane.
 __device__ __forceinline__ bool elect_one() {
