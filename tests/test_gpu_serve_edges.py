@@ -234,3 +234,22 @@ def test_drafts_that_are_not_attended_change_no_bit(pisa, fmt, T, Hq, D):
         dv2[:, :, 1:3] *= scale_v
         O2, lse2 = pisa.tree_attention(s, cache, q, dk2, dv2, tmask(mask), i32(lens), ws)
         assert torch.equal(O[:, :, rest], O2[:, :, rest]) and torch.equal(lse[:, :, rest], lse2[:, :, rest])
+
+
+# ----------------------------------------------------------------------------- lengths past the cache
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("T, Hq", [(2, 2), (24, 4)])
+@pytest.mark.parametrize("topk", [0, 2])
+def test_a_length_past_the_cache_is_its_capacity(pisa, fmt, T, Hq, topk):
+    """The clamped length gives the bits of the capacity, where the cache's rows are finite up to there."""
+    import torch
+    case = (2, 2 * Hq, 2, T, 256, 64, fmt, 64, 192 if topk else 0, topk, 0, [256, 256], "tree")
+    s, cache, k, v, q, dk, dv, mask, lens, idx = tree_inputs(pisa, case, 81)
+    ws, ix = pisa.new_tree_workspace(s, "cuda"), None if idx is None else i32(idx)
+    want = pisa.tree_attention(s, cache, q, dk, dv, tmask(mask), i32([256, 0]), ws, idx=ix)
+    assert pisa.check_status(ws) == (pisa.OK, 0)
+    for n in ([257, -1], [2147483647, -2147483648]):
+        got = pisa.tree_attention(s, cache, q, dk, dv, tmask(mask), i32(n), ws, idx=ix)
+        assert pisa.check_status(ws) == (pisa.ERR_BAD_INDEX, 0x7B0)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
