@@ -667,8 +667,8 @@ class CacheShape:
 
 class Cache:
     """A K/V cache's buffers: k and v [B, heads_kv, capacity, D] (bf16, or float8_e4m3fn with the
-    exponent bytes k_exp and v_exp, uint8 [B, heads_kv, capacity]: a row is its values times
-    2^(byte - 127)). v and v_exp may be None for calls that only read keys (cache_append_pyramid).
+    exponent bytes k_exp and v_exp, uint8 [B, heads_kv, capacity], 1 .. 255: a row is its values times
+    2^(byte - 127), or NaN for 255). v and v_exp may be None for calls that only read keys (cache_append_pyramid).
     The buffers are those of its making (a larger cache is a new Cache); every call checks that they
     are still such buffers and takes their addresses as they are then."""
 

@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p
 // Rows of one row tile for a selection row of `rows` rows, T drafted tokens: 8 or 16 (attn_tree_few.cu), 128 or
 // 256 (attn_tree_many.cu); where a tile does not hold them several share them evenly. Up to 32 rows over an
 // e4m3 cache are two tiles of 16 (each reads the cache): 64 caches of 8 heads, 64 blocks of 64 keys selected, eight
-// tokens of four heads, 272 us against 321 us as one tile of 128. A third tile would lose (nine tokens, 388 us
-// against 326 us), and so would two over a bf16 cache (351 us against 227 us).
+// tokens of four heads, 276 us against 317 us as one tile of 128. A third tile would lose (nine tokens, 399 us
+// against 320 us), and so would two over a bf16 cache (351 us against 221 us).
 int tree_row_tile(int rows, int T, bool e4m3) {
     if (rows <= 8) return 8;
     if (rows <= 16 || (e4m3 && rows <= 32 && T <= 16)) return 16;

@@ -23,7 +23,7 @@
 //     below: off by 2^-28 of the largest entry that another row adds, where that row's own rounding in the cache is
 //     up to 2^-19 of it (half of e4m3's smallest step against 448). (With one unit a warp, set by the largest exponent
 //     whatever its probability, a value row of 2^34 times the others hid them all, at any weight. With a second
-//     exponential a score, of its weight, four tokens below take 160 us, and eight 296 us and not 272 us.)
+//     exponential a score, of its weight, four tokens below take 160 us, and eight 296 us and not 276 us.)
 //   * ldmatrix hands out byte pairs: in Q K^T the dims of a 16-dim chunk take the order that the bytes
 //     come in (any order does), in V^T P^T the even dims of a chunk are rows 0-7 of the product and the
 //     odd ones rows 8-15.
@@ -31,7 +31,7 @@
 //
 // Measured (64 caches of 8 heads of 128, 64 selected blocks of 64 keys and 63 keys of tail, four query heads each):
 // one token over e4m3 0.55 GB in 99 us with the join, 5.5 TB/s (84 % of the copy rate). Four tokens (16 rows)
-// 147 us, bound by issue. Over bf16 1.09 GB: one token 179 us, 6.1 TB/s (93 %), four tokens 186 us.
+// 148 us, bound by issue. Over bf16 1.09 GB: one token 179 us, 6.1 TB/s (93 %), four tokens 184 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

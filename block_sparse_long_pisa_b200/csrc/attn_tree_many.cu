@@ -10,8 +10,10 @@
 // half of a tile's keys; the two warps meet in one vote a tile.
 //
 // A tile is 128 keys (two units of the cache, or the drafted tokens). Two passes over S in TMEM: the row's
-// maximum (the kept one moves when a score exceeds it by 2^kManyLazy, and O with it, by the two warps), then
-// the probabilities, written as operand A of P V over the columns of S that have been read. Order of the
+// maximum (the kept one moves when one of the row's scores exceeds it by kManyLazy, and O with it, by the two warps), then
+// the probabilities, written as operand A of P V over the columns of S that have been read. They are rounded to bf16,
+// the type of the operand beside V, whose range a bf16 cache needs: O is 0.0023 from its 64-bit value where fp32
+// probabilities leave 0.0017, the rounding of O itself (relative root mean squares, the trees below). Order of the
 // MMA lane with two row tiles: S(0, g), P V(1, g - 1), S(1, g), P V(0, g): the softmax of one runs under the
 // products of the other; with one row tile S has two buffers and the order is S(g), P V(g - 1).
 //
@@ -25,10 +27,14 @@
 //
 // Measured, with the join: trees of 48 tokens of 32 heads over 8 ragged bf16 caches up to 32,768 rows, 0.72 GB and
 // 0.14 Tflop in 250 us (0.55 Pflop/s, 34 % of the measured peak). 64 caches of 8 heads, 64 blocks of 64 keys selected,
-// tokens of four heads, bf16 (e4m3): 8 tokens 227 us, 16 tokens 243 us (341 us), 32 tokens 278 us (379 us), 64 tokens
-// 396 us (555 us); the copy rate would be 167 us (86 us). What bounds it is the chain of a row tile, S, softmax, P V, S again, of which the other
-// row tile hides a part: tensor pipe 40 %, exponentials 31 %, issue 33 % of their peaks. Steps of 64 keys with two
-// buffers of S a row tile, which break the chain, cost more in the softmax than they hide (296 us for the trees).
+// tokens of four heads, bf16 (e4m3): 8 tokens 221 us, 16 tokens 227 us (326 us), 32 tokens 243 us (344 us), 64 tokens
+// 396 us (555 us); the copy rate would be 167 us (86 us). What bounds it is the length of a row tile's own chain, S,
+// softmax, P V, S again, of which the other row tile hides a part: tensor pipe 40 %, exponentials 31 %, issue 33 % of
+// their peaks. In it the softmax makes two passes over S, each of blocking loads of 32 columns, with a vote of two warps
+// between them. (The prefill kernel, with the same tiles and more keys a row, makes one pass against the kept maximum
+// and reaches 0.96 Pflop/s; that form has not been tried here.) A quarter of the products of 48 tokens of four heads is
+// empty rows, 192 in two tiles of 128. Steps of 64 keys with two buffers of S a row tile, which break the chain, cost
+// more in the softmax than they hide (296 us for the trees).
 // One elected lane issues the products: to the compiler a branch on the lane's number is not known to be one lane,
 // and each product cost 90 cycles to issue (297 us).
 #include <cuda.h>

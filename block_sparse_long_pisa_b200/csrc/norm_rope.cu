@@ -25,8 +25,11 @@
 //
 // Measured (heads of 128, all dims turned): forward, 131,072 tokens of 32 + 8 heads, 2.68 GB in 464 us, 5.8 TB/s
 // (88 % of the copy rate); 64 tokens of as many heads 5.2 us. Backward, 32,768 tokens of 16 + 16 heads, 0.81 GB in
-// 164 us, 4.9 TB/s (75 %): 128 registers for the angles' products and the weight sums leave two blocks on an SM,
-// so the loads in flight bound it (DRAM 54 %, issue 54 % in the profile), and three blocks spill.
+// 166 us, 4.9 TB/s (74 %): rows travel through registers, and with the angles' products and the weight sums beside
+// them two blocks fit an SM (128 registers and, D = 128, 52 bytes of spills a thread; at three blocks 584 bytes), so the
+// loads in flight bound it (DRAM 54 %, issue 54 % in the profile). The forward pass spills 104 bytes at its three
+// blocks. 3 x 1,537 tokens of 12 + 4 heads of 64: backward 20 us, 6 us of them the weight sums' kernel, which runs after
+// the rows' one.
 #include <cuda_bf16.h>
 
 #include "pisa_device.cuh"
@@ -452,7 +455,8 @@ bool launch_norm_rope_backward(NormRopeParams p, int D, bool inter, float* dwq, 
     if (cudaGetLastError() != cudaSuccess) return false;
     ++*launches;
     if (dwq == nullptr && dwk == nullptr) return true;
-    // launched while the rows are still being worked on: it waits for them itself
+    // The rows' kernel does not trigger it early, so it starts when the last block has exited; what the attribute saves is
+    // the launch itself. It waits for the rows' sums all the same.
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(D / 32), 2);
     cfg.blockDim = dim3(1024);

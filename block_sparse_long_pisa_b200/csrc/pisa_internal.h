@@ -217,8 +217,9 @@ struct BwdParams {
     float scale, scale_log2;
 };
 
-// Blocks of the norm-and-rotation grids: four of 256 threads on each of 148 SMs (rows of partial
-// weight gradients; smaller tiles are taken while a grid has fewer).
+// Most blocks of the norm-and-rotation backward grid, and so rows of partial weight gradients: two waves of the two
+// blocks that each of 148 SMs holds. Tiles are made smaller while a grid, the forward pass's too, has fewer than half
+// of it.
 constexpr int kNormRopeBlocks = 592;
 
 struct NormRopeParams {

@@ -333,8 +333,8 @@ PISA_API pisa_status pisa_qk_norm_rope_backward(const pisa_norm_rope_shape *shap
 /* A K/V cache: [batch, heads_kv, capacity, head_dim] for K and for V.
  *   PISA_CACHE_BF16 : bf16 rows, no exponents (k_exp = v_exp = NULL).
  *   PISA_CACHE_E4M3 : 8-bit rows (e4m3) and one exponent byte e per row in k_exp and v_exp
- *                     (uint8 [batch, heads_kv, capacity]): the row's values are its bytes' values
- *                     times 2^(e - 127).
+ *                     (uint8 [batch, heads_kv, capacity], 1 .. 255): the row's values are its bytes'
+ *                     values times 2^(e - 127), or all NaN for e = 255 (whose bytes are zero).
  *   head_dim 64 or 128, capacity >= 1, batch * heads_kv * capacity < 2^31. */
 #define PISA_CACHE_BF16 0
 #define PISA_CACHE_E4M3 1
