@@ -342,8 +342,8 @@ typedef struct {
     int32_t batch, heads_kv, capacity, head_dim, format;
 } pisa_cache_shape;
 
-/* Writes `tokens` rows of K and V of every sequence into the cache, quantising as it writes: row t
- * of sequence b goes to position start[b] + t. For PISA_CACHE_E4M3 a row's e is the smallest byte
+/* Writes `tokens` (1 .. capacity) rows of K and V of every sequence into the cache, quantising as it writes:
+ * row t of sequence b goes to position start[b] + t. For PISA_CACHE_E4M3 a row's e is the smallest byte
  * >= 1 with max |x| <= 448 * 2^(e - 127), and its values are x * 2^(127 - e) rounded to nearest even
  * (the scaling is exact, so there is one rounding; relative error <= 2^-4, or 2^-10 of 2^(e - 127)
  * for values that small). A row that holds an infinity or a NaN gets e = 255 and zero bytes, and
@@ -361,8 +361,8 @@ PISA_API pisa_status pisa_cache_write(const pisa_cache_shape *shape, int32_t tok
                                       const int32_t *count, void *Kc, void *Vc, uint8_t *k_exp, uint8_t *v_exp,
                                       void *ws, pisa_stream_t stream);
 
-/* Reads rows back: K[b, h, t] and V[b, h, t] (bf16, contiguous [batch, heads_kv, tokens, D]) are the
- * cache's rows start[b] + t, for t < count[b]; the outputs keep what they held elsewhere. Values are
+/* Reads rows back: K[b, h, t] and V[b, h, t] (bf16, contiguous [batch, heads_kv, tokens, D], tokens 1 .. capacity)
+ * are the cache's rows start[b] + t, for t < count[b]; the outputs keep what they held elsewhere. Values are
  * rounded once, to bf16 (exact but for exponents below bf16's). start, count, ws and refusals as in
  * pisa_cache_write. */
 PISA_API pisa_status pisa_cache_read(const pisa_cache_shape *shape, int32_t tokens, const void *Kc, const void *Vc,

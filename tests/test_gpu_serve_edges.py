@@ -83,6 +83,36 @@ def test_outputs_made_on_another_stream(pisa):
     assert bool((kept == 5.0).all()) and torch.equal(O, want) and torch.equal(lse, want_lse)
 
 
+def test_calls_on_a_forked_stream_are_captured(pisa):
+    """A graph whose capture forks to another stream, the calls there making their own outputs: replays give the eager bits."""
+    import torch
+    case = (2, 4, 2, 5, 512, 128, 1, 64, 0, 0, 0, [500, 77], "tree")
+    s, cache, k, v, q, dk, dv, mask, lens, idx = tree_inputs(pisa, case, 74)
+    ws, sws, m, n, count = pisa.new_tree_workspace(s, "cuda"), pisa.new_cache_workspace("cuda"), tmask(mask), i32(lens), i32([9, 4])
+    nr, w = pisa.NormRopeShape(2, 5, 4, 2, 128, 0), f32(np.ones(128))
+    xq, xk = q.transpose(1, 2).contiguous(), dk.transpose(1, 2).contiguous()
+
+    def calls(stream):
+        return [*pisa.tree_attention(s, cache, q, dk, dv, m, n, ws, stream=stream),
+                *pisa.cache_read(cache, 9, sws, count=count, stream=stream),
+                *pisa.qk_norm_rope_backward(nr, xq, xk, None, None, q, dk, w, w, stream=stream)]
+
+    want = calls(None)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = calls(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert pisa.check_status(ws) == (pisa.OK, 0) and pisa.check_status(sws) == (pisa.OK, 0)
+
+
 # T, Hq, D: 4, 16 and two tiles of 16 rows (few), one and two tiles of 128 (many)
 FORMS = [(1, 4, 128), (1, 4, 64), (4, 4, 128), (7, 2, 64), (7, 4, 128), (24, 4, 128), (40, 4, 64)]
 
